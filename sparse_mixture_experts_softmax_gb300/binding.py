@@ -68,6 +68,11 @@ class moe_ep_rows(ctypes.Structure):
         "f32_scratch")] + [("f32_scratch_bytes", ctypes.c_size_t)]
 
 
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("D", c_int32), ("x_type", c_int32), ("delta_type", c_int32),
+                ("z_type", c_int32), ("eps", c_float)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, fn: str, status: int, text: str):
         super().__init__(f"{fn}: {text} (status {status})")
@@ -172,6 +177,12 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_ep_router_update.argtypes = [P(moe_config), c_void_p, c_void_p, c_float, c_void_p]
     L.moe_ep_get_routing.argtypes = [P(moe_config), P(moe_ep_config), c_void_p, c_size_t] + \
         [c_void_p] * 8
+    L.moe_norm_workspace_size.argtypes = [P(moe_norm_config)]
+    L.moe_norm_workspace_size.restype = c_size_t
+    L.moe_norm_forward.argtypes = [P(moe_norm_config)] + [c_void_p] * 9
+    L.moe_norm_backward.argtypes = [P(moe_norm_config)] + [c_void_p] * 10 + [c_size_t, c_void_p]
+    for fn in ("moe_norm_forward", "moe_norm_backward"):
+        getattr(L, fn).restype = c_int32
     for fn in ("moe_ep_buffer_offsets", "moe_ep_get_routing", "moe_ep_route",
                "moe_ep_expert_forward",
                "moe_ep_combine", "moe_ep_expert_backward", "moe_ep_router_backward",
@@ -464,3 +475,28 @@ def moe_debug_poke_routing(cfg, workspace, field: int, index: int, value: int, s
     _check("moe_debug_poke_routing",
            lib().moe_debug_poke_routing(ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
                                         int(field), int(index), int(value), _stream(stream)))
+
+
+# ---- layer norm of the pre-norm block (include/moe_block.h)
+
+def make_norm_config(T, D, x_type="f32", delta_type="f32", z_type="f32",
+                     eps=1e-5) -> moe_norm_config:
+    return moe_norm_config(T, D, DTYPE[x_type], DTYPE[delta_type], DTYPE[z_type], float(eps))
+
+
+def moe_norm_forward(cfg, x, delta, gamma, beta, h, z, mean=None, rstd=None, stream=None):
+    _check("moe_norm_forward",
+           lib().moe_norm_forward(ctypes.byref(cfg), _ptr(x), _ptr(delta), _ptr(gamma), _ptr(beta),
+                                  _ptr(h), _ptr(z), _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def moe_norm_workspace_size(cfg) -> int:
+    return int(lib().moe_norm_workspace_size(ctypes.byref(cfg)))
+
+
+def moe_norm_backward(cfg, h, dz, mean, rstd, gamma, dres, dx, dgamma, dbeta, workspace,
+                      stream=None):
+    _check("moe_norm_backward",
+           lib().moe_norm_backward(ctypes.byref(cfg), _ptr(h), _ptr(dz), _ptr(mean), _ptr(rstd),
+                                   _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+                                   _ptr(workspace), workspace.numel(), _stream(stream)))

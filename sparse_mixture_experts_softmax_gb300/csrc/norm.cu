@@ -1,0 +1,308 @@
+// Layer norm over rows of D values with the residual add in front of it, and
+// its backward pass with the residual gradient behind it.
+//
+//   forward    h = x + delta;  m = mean(h);  r = rsqrt(mean((h - m)^2) + eps);
+//              z = (h - m) r gamma + beta
+//   backward   xh = (h - m) r,  g = dz gamma:
+//              dx = dres + r (g - mean(g) - xh mean(g xh)),
+//              dgamma = sum_t dz xh,  dbeta = sum_t dz
+//
+// Both are bound by HBM: a row is read once, held in registers while its sums
+// are formed, and written once.  The variance is the mean squared deviation
+// from the row's mean (two reductions over registers, not sum(h^2) - m^2, which
+// cancels when a row's offset is large against its spread).
+#include "common.cuh"
+#include "kernels.h"
+#include "norm.h"
+
+namespace moe {
+namespace {
+
+// W consecutive values, widened to fp32.  W = 8 needs 16-byte aligned rows
+// (D a multiple of 8); W = 1 takes any D.
+template <typename T, int W> struct Row;
+template <> struct Row<float, 8> {
+  static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+template <> struct Row<bf16, 8> {
+  static __device__ __forceinline__ void load(const bf16* p, float (&v)[8]) {
+    Vec<bf16> q;
+    q.load(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = q.get(i);
+  }
+  static __device__ __forceinline__ void store(bf16* p, const float (&v)[8]) {
+    Vec<bf16> q;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q.set(i, v[i]);
+    q.store(p);
+  }
+};
+template <typename T> struct Row<T, 1> {
+  static __device__ __forceinline__ void load(const T* p, float (&v)[1]) { v[0] = to_f(*p); }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { *p = from_f<T>(v[0]); }
+};
+
+constexpr int MAX_WARPS = 32;
+
+// Sum of `v` over the blockDim.x threads of a row.  A one-warp row needs no
+// barrier; a wider row has its block to itself (blockDim.y = 1), and `slot`
+// alternates between uses so that one barrier a sum is enough.
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (blockDim.x == 32) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  const int nw = blockDim.x >> 5;
+  return warp_sum(lane < nw ? red[lane] : 0.f);
+}
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if (blockDim.x == 32) return make_float2(a, b);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = make_float2(a, b);
+  __syncthreads();
+  const float2 t = lane < (int)(blockDim.x >> 5) ? red[lane] : make_float2(0.f, 0.f);
+  return make_float2(warp_sum(t.x), warp_sum(t.y));
+}
+
+// One row per blockDim.x threads; a thread holds V pieces of W values, at
+// stride blockDim.x * W.
+template <typename XT, typename ZT, int W, int V>
+__global__ void __launch_bounds__(1024)
+norm_fwd_kernel(NormFwd a) {
+  __shared__ float red[2][MAX_WARPS];
+  pdl_begin();
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= a.T) return;    // whole warps: a wider row has one row per block
+  const int D = a.D, step = blockDim.x * W;
+  const long long base = row * D;
+  const XT* x = static_cast<const XT*>(a.x) + base;
+  float v[V][W];
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x * W + i * step;
+    if (c < D) {
+      Row<XT, W>::load(x + c, v[i]);
+      if (a.delta != nullptr) {
+        float d[W];
+        if (a.delta_type == 0) Row<float, W>::load(static_cast<const float*>(a.delta) + base + c, d);
+        else Row<bf16, W>::load(static_cast<const bf16*>(a.delta) + base + c, d);
+        // the norm reads the stream as it is stored, so that the backward
+        // pass, which reads it from memory, sees the same values
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[i][j] = to_f(from_f<XT>(v[i][j] + d[j]));
+        Row<XT, W>::store(static_cast<XT*>(a.h) + base + c, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) s += v[i][j];
+    }
+  }
+  const float inv = 1.0f / (float)D;
+  const float mean = row_sum(s, red[0]) * inv;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x * W + i * step;
+    if (c < D) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        v[i][j] -= mean;
+        s = fmaf(v[i][j], v[i][j], s);
+      }
+    }
+  }
+  const float rstd = 1.0f / sqrtf(row_sum(s, red[1]) * inv + a.eps);
+  if (threadIdx.x == 0) {
+    if (a.mean != nullptr) a.mean[row] = mean;
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x * W + i * step;
+    if (c < D) {
+      float g[W], b[W];
+      Row<float, W>::load(a.gamma + c, g);
+      if (a.beta != nullptr) Row<float, W>::load(a.beta + c, b);
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        v[i][j] = a.beta != nullptr ? fmaf(v[i][j] * rstd, g[j], b[j]) : v[i][j] * rstd * g[j];
+      Row<ZT, W>::store(static_cast<ZT*>(a.z) + base + c, v[i]);
+    }
+  }
+}
+
+// Rows at stride gridDim.x * blockDim.y; a thread keeps the sums of its own
+// columns over its rows, and the block writes one partial row of dgamma and of
+// dbeta, which norm_cols_kernel adds in a fixed order.
+template <typename XT, int W, int V>
+__global__ void __launch_bounds__(1024)
+norm_bwd_kernel(NormBwd a) {
+  __shared__ float2 red[2][MAX_WARPS];
+  extern __shared__ __align__(16) float cols[];    // blockDim.y > 1: [blockDim.y][D] of one sum at a time
+  pdl_begin();
+  const int D = a.D, step = blockDim.x * W;
+  const float inv = 1.0f / (float)D;
+  float dg[V][W], db[V][W];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j) dg[i][j] = db[i][j] = 0.f;
+  int phase = 0;
+  for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < a.T;
+       row += (long long)gridDim.x * blockDim.y) {
+    const long long base = row * D;
+    const float m = a.mean[row], r = a.rstd[row];
+    float xh[V][W], g[V][W];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = threadIdx.x * W + i * step;
+      if (c < D) {
+        float dz[W];
+        Row<XT, W>::load(static_cast<const XT*>(a.h) + base + c, xh[i]);
+        Row<float, W>::load(a.dz + base + c, dz);
+        Row<float, W>::load(a.gamma + c, g[i]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          xh[i][j] = (xh[i][j] - m) * r;
+          dg[i][j] = fmaf(dz[j], xh[i][j], dg[i][j]);
+          db[i][j] += dz[j];
+          g[i][j] *= dz[j];
+          s1 += g[i][j];
+          s2 = fmaf(g[i][j], xh[i][j], s2);
+        }
+      }
+    }
+    const float2 s = row_sum2(s1, s2, red[phase]);
+    phase ^= 1;
+    const float c1 = s.x * inv, c2 = s.y * inv;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = threadIdx.x * W + i * step;
+      if (c < D) {
+        float o[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = r * (g[i][j] - c1 - xh[i][j] * c2);
+        if (a.dres != nullptr) {
+          float e[W];
+          Row<float, W>::load(a.dres + base + c, e);
+#pragma unroll
+          for (int j = 0; j < W; ++j) o[j] += e[j];
+        }
+        Row<float, W>::store(a.dx + base + c, o);
+      }
+    }
+  }
+  auto emit = [&](const float (&v)[V][W], float* out) {
+    if (blockDim.y > 1) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = threadIdx.x * W + i * step;
+      if (c < D) Row<float, W>::store(blockDim.y > 1 ? cols + threadIdx.y * D + c : out + c, v[i]);
+    }
+    if (blockDim.y == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < D; c += blockDim.x * blockDim.y) {
+      float t = 0.f;
+      for (int q = 0; q < (int)blockDim.y; ++q) t += cols[q * D + c];
+      out[c] = t;
+    }
+  };
+  float* part = a.part + (long long)blockIdx.x * 2 * D;
+  emit(dg, part);
+  if (a.want_beta) emit(db, part + D);
+}
+
+// dgamma and dbeta from the nparts partial rows [nparts][2][D]: 32 columns by
+// 32 slices of the partials per block, the slices added in order.
+__global__ void __launch_bounds__(1024)
+norm_cols_kernel(const float* __restrict__ part, int nparts, int D, float* __restrict__ dgamma,
+                 float* __restrict__ dbeta) {
+  __shared__ float s[32][33];
+  pdl_begin();
+  const int c = blockIdx.x * 32 + threadIdx.x, w = blockIdx.y;
+  float t = 0.f;
+  if (c < D)
+    for (int p = threadIdx.y; p < nparts; p += 32) t += part[((long long)p * 2 + w) * D + c];
+  s[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  // each warp sums one column over the slices (a fixed tree)
+  const float sum = warp_sum(s[threadIdx.x][threadIdx.y]);
+  const int col = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && col < D) (w == 0 ? dgamma : dbeta)[col] = sum;
+}
+
+// Threads per row and pieces per thread: the fewest threads that hold the row.
+struct Shape {
+  int W, V, tpr, rows;   // values a piece, pieces a thread, threads a row, rows a block
+};
+Shape norm_shape(int D, int vmax) {
+  Shape s{};
+  s.W = D % 8 == 0 ? 8 : 1;
+  s.V = s.W == 8 ? vmax : 8;
+  const int per = s.W * s.V;
+  s.tpr = 32;
+  while (s.tpr * per < D && s.tpr < 1024) s.tpr *= 2;
+  s.rows = s.tpr == 32 ? 8 : 1;
+  return s;
+}
+
+}  // namespace
+
+int norm_bwd_blocks(long long T, int D) {
+  const Shape s = norm_shape(D, D > 8192 ? 2 : 1);
+  const int per_sm = 1024 / (s.tpr * s.rows);
+  const long long need = (T + s.rows - 1) / s.rows;
+  const long long most = 152LL * (per_sm < 1 ? 1 : per_sm);
+  return (int)(need < most ? need : most);
+}
+
+template <typename XT, typename ZT>
+static cudaError_t fwd_t(const NormFwd& a, cudaStream_t st) {
+  // few rows: one piece a thread, for the shortest chain; many: two, for
+  // fewer threads a row
+  const Shape s = norm_shape(a.D, a.T < 304 && a.D <= 8192 ? 1 : 2);
+  const dim3 grid((unsigned)((a.T + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
+  if (s.W == 1) return launch_pdl(norm_fwd_kernel<XT, ZT, 1, 8>, grid, block, 0, st, a);
+  if (s.V == 1) return launch_pdl(norm_fwd_kernel<XT, ZT, 8, 1>, grid, block, 0, st, a);
+  return launch_pdl(norm_fwd_kernel<XT, ZT, 8, 2>, grid, block, 0, st, a);
+}
+
+cudaError_t launch_norm_fwd(int x_type, int z_type, const NormFwd& a, cudaStream_t st) {
+  if (x_type == 0) return z_type == 0 ? fwd_t<float, float>(a, st) : fwd_t<float, bf16>(a, st);
+  return z_type == 0 ? fwd_t<bf16, float>(a, st) : fwd_t<bf16, bf16>(a, st);
+}
+
+template <typename XT>
+static cudaError_t bwd_t(const NormBwd& a, cudaStream_t st) {
+  const Shape s = norm_shape(a.D, a.D > 8192 ? 2 : 1);
+  const dim3 grid((unsigned)norm_bwd_blocks(a.T, a.D)), block(s.tpr, s.rows);
+  const size_t smem = s.rows > 1 ? (size_t)s.rows * a.D * 4 : 0;   // D <= 256 there
+  if (s.W == 1) return launch_pdl(norm_bwd_kernel<XT, 1, 8>, grid, block, smem, st, a);
+  if (s.V == 1) return launch_pdl(norm_bwd_kernel<XT, 8, 1>, grid, block, smem, st, a);
+  return launch_pdl(norm_bwd_kernel<XT, 8, 2>, grid, block, smem, st, a);
+}
+
+cudaError_t launch_norm_bwd(int x_type, const NormBwd& a, cudaStream_t st) {
+  return x_type == 0 ? bwd_t<float>(a, st) : bwd_t<bf16>(a, st);
+}
+
+cudaError_t launch_norm_cols(const float* part, int nparts, int D, float* dgamma, float* dbeta,
+                             cudaStream_t st) {
+  return launch_pdl(norm_cols_kernel, dim3((D + 31) / 32, dbeta != nullptr ? 2 : 1), dim3(32, 32),
+                    0, st, part, nparts, D, dgamma, dbeta);
+}
+
+}  // namespace moe
