@@ -4,7 +4,9 @@
  *
  *   - moe_norm_forward / moe_norm_backward: layer norm over rows of D values,
  *     with the residual add of the layer's output fused in front of it, and
- *     the residual gradient fused behind its backward pass.
+ *     the residual gradient fused behind its backward pass;
+ *   - moe_decode: the layer itself for 1 to MOE_DECODE_MAX_TOKENS tokens, in
+ *     one launch, for serving (no gradients, nothing kept for a backward).
  *
  * The conventions of moe.h hold: device pointers, 16-byte aligned, dense
  * row-major tensors, caller-owned memory, work enqueued on `stream`, arguments
@@ -63,6 +65,36 @@ MOE_API moe_status moe_norm_backward(const moe_norm_config* cfg, const void* h, 
                                      const float* mean, const float* rstd, const float* gamma,
                                      const float* dres, float* dx, float* dgamma, float* dbeta,
                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The layer of moe.h for a few tokens: the same configuration, weights and
+ * routing as moe_forward (scores, groups, correction bias, shared branch and
+ * capacity included), as one cooperative kernel that reads each chosen expert's
+ * weights once.  x [T,D] and y [T,D] are in cfg.dtype; y must not overlap x or
+ * a weight.  MOE_BF16 layers route with a bf16 copy of w_gate's values, as
+ * moe_forward does; products are summed in fp32, hidden activations stay fp32,
+ * and y is rounded once.  idx [T,k] (int32) and gate [T,k] (fp32) receive the
+ * routing, or are NULL.  T <= MOE_DECODE_MAX_TOKENS, D <= 2^20, F <= 2^19
+ * (MOE_ERR_UNSUPPORTED beyond).  aux_alpha is not read.
+ *
+ * The workspace holds the counters of the kernel's grid barriers: call
+ * moe_decode_init once before its first use (and after a status other than
+ * MOE_OK).  Every call leaves it ready for the next, on any T up to the size it
+ * was made for (the size grows with T).  Calls that share a workspace must not
+ * overlap on the GPU.  A call captures into a CUDA graph. */
+#define MOE_DECODE_MAX_TOKENS 64
+MOE_API size_t moe_decode_workspace_size(const moe_config* cfg);
+MOE_API moe_status moe_decode_init(const moe_config* cfg, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+MOE_API moe_status moe_decode(const moe_config* cfg, const moe_weights* w, const void* x, void* y,
+                              int32_t* idx, float* gate, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Reads the device status of the calls since moe_decode_init: 0, MOE_ERR_TIMEOUT
+ * when a bounded device-side wait expired (the call ended early and its outputs
+ * are invalid), or MOE_ERR_INVALID_ARG when a call found its workspace without
+ * moe_decode_init (it wrote nothing else).  Synchronises `stream`. */
+MOE_API moe_status moe_decode_status(const moe_config* cfg, const void* workspace,
+                                     size_t workspace_bytes, int32_t* status_host, void* stream);
 
 #ifdef __cplusplus
 }

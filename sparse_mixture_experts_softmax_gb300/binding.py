@@ -181,7 +181,13 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_norm_workspace_size.restype = c_size_t
     L.moe_norm_forward.argtypes = [P(moe_norm_config)] + [c_void_p] * 9
     L.moe_norm_backward.argtypes = [P(moe_norm_config)] + [c_void_p] * 10 + [c_size_t, c_void_p]
-    for fn in ("moe_norm_forward", "moe_norm_backward"):
+    L.moe_decode_workspace_size.argtypes = [P(moe_config)]
+    L.moe_decode_workspace_size.restype = c_size_t
+    L.moe_decode_init.argtypes = [P(moe_config), c_void_p, c_size_t, c_void_p]
+    L.moe_decode.argtypes = [P(moe_config), P(moe_weights)] + [c_void_p] * 5 + [c_size_t, c_void_p]
+    L.moe_decode_status.argtypes = [P(moe_config), c_void_p, c_size_t, c_void_p, c_void_p]
+    for fn in ("moe_norm_forward", "moe_norm_backward", "moe_decode_init", "moe_decode",
+               "moe_decode_status"):
         getattr(L, fn).restype = c_int32
     for fn in ("moe_ep_buffer_offsets", "moe_ep_get_routing", "moe_ep_route",
                "moe_ep_expert_forward",
@@ -218,6 +224,18 @@ def _stream(stream) -> Optional[int]:
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_on(stream, device) -> int:
+    """The raw stream for a call on `device` (a CUDA torch.device): the given
+    one, or the device's current stream.  The current stream is read as a plain
+    address (0.1 us; building torch's Stream object takes 3 us, as long as a
+    kernel of a few tokens)."""
+    if stream is None:
+        if device.type != "cuda":
+            return 0
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -500,3 +518,31 @@ def moe_norm_backward(cfg, h, dz, mean, rstd, gamma, dres, dx, dgamma, dbeta, wo
            lib().moe_norm_backward(ctypes.byref(cfg), _ptr(h), _ptr(dz), _ptr(mean), _ptr(rstd),
                                    _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ---- the layer for a few tokens (include/moe_block.h)
+
+MOE_DECODE_MAX_TOKENS = 64
+
+
+def moe_decode_workspace_size(cfg) -> int:
+    return int(lib().moe_decode_workspace_size(ctypes.byref(cfg)))
+
+
+def moe_decode_init(cfg, workspace, stream=None):
+    _check("moe_decode_init", lib().moe_decode_init(ctypes.byref(cfg), _ptr(workspace),
+                                                    workspace.numel(), _stream(stream)))
+
+
+def moe_decode(cfg, weights, x, y, workspace, idx=None, gate=None, stream=None):
+    _check("moe_decode",
+           lib().moe_decode(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(y), _ptr(idx),
+                            _ptr(gate), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def moe_decode_status(cfg, workspace, stream=None) -> int:
+    out = ctypes.c_int32(0)
+    _check("moe_decode_status",
+           lib().moe_decode_status(ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
+                                   ctypes.addressof(out), _stream(stream)))
+    return int(out.value)

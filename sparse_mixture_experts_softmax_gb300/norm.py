@@ -40,7 +40,9 @@ class LayerNorm:
         for name, p in (("gamma", gamma), ("beta", beta)):
             if p is not None and (p.dtype != torch.float32 or tuple(p.shape) != (self.D,)):
                 raise ValueError(f"{name} must be float32 of shape [{self.D}]")
-        self.gamma, self.beta = gamma, beta
+        if beta is not None and beta.device != gamma.device:
+            raise ValueError(f"beta is on {beta.device}, gamma on {gamma.device}")
+        self.gamma, self.beta, self.device = gamma, beta, gamma.device
         self.x_type, self.z_type, self.eps = _TORCH[x_dtype], _TORCH[z_dtype], float(eps)
         self.workspace = None
         self._cfg = {}
@@ -59,20 +61,26 @@ class LayerNorm:
             c = self._cfg[key] = (cfg, ctypes.byref(cfg), B.moe_norm_workspace_size(cfg))
         return c
 
+    def _wrong(self, name, t, dtype, shape):
+        """Raises for a tensor that is not contiguous `dtype` of `shape` on the
+        parameters' device."""
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the parameters on {self.device}")
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
     def _rows(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, got "
-                             f"{t.dtype} {tuple(t.shape)}")
-        if t.device != self.gamma.device:
-            raise ValueError(f"{name} is on {t.device}, the parameters on {self.gamma.device}")
+        if (t.dtype != dtype or t.shape != shape or t.device != self.device or
+                not t.is_contiguous()):
+            self._wrong(name, t, dtype, shape)
 
     def forward(self, x, delta=None, stats=True, out=None, stream=None) -> NormOut:
         """h = x + delta (x itself without a delta), z = norm(h).  ``out``: a
         NormOut whose tensors are written instead of new ones; its h may be
         ``x``.  stats=False leaves mean and rstd out (serving)."""
-        if x.dim() != 2 or x.shape[1] != self.D:
-            raise ValueError(f"x must be [T, {self.D}], got {tuple(x.shape)}")
         shape = x.shape
+        if len(shape) != 2 or shape[1] != self.D:
+            raise ValueError(f"x must be [T, {self.D}], got {tuple(shape)}")
         T = shape[0]
         self._rows("x", x, self.x_type, shape)
         if delta is not None:
@@ -81,9 +89,10 @@ class LayerNorm:
             self._rows("delta", delta, delta.dtype, shape)
         if out is None:
             out = NormOut(torch.empty_like(x) if delta is not None else None,
-                          torch.empty(shape, dtype=self.z_type, device=x.device),
-                          torch.empty(T, device=x.device) if stats else None,
-                          torch.empty(T, device=x.device) if stats else None)
+                          torch.empty_like(x) if self.z_type is self.x_type else
+                          torch.empty_like(x, dtype=self.z_type),
+                          torch.empty(T, dtype=torch.float32, device=self.device) if stats else None,
+                          torch.empty(T, dtype=torch.float32, device=self.device) if stats else None)
         else:
             if (out.h is not None) != (delta is not None):
                 raise ValueError("out.h goes with a delta")
@@ -97,16 +106,16 @@ class LayerNorm:
         B._check("moe_norm_forward", B.lib().moe_norm_forward(
             cfg[1], x.data_ptr(), None if delta is None else delta.data_ptr(),
             self.gamma.data_ptr(), B._ptr(self.beta), None if delta is None else out.h.data_ptr(),
-            out.z.data_ptr(), B._ptr(out.mean), B._ptr(out.rstd), B._stream(stream)))
+            out.z.data_ptr(), B._ptr(out.mean), B._ptr(out.rstd), B._stream_on(stream, self.device)))
         return out
 
     def backward(self, dz, h, mean, rstd, dres=None, out=None, stream=None) -> NormGrads:
         """Gradients at the stream h that ``forward`` normalised (its h, or its
         x without a delta); dres: the gradient reaching h past the norm.
         ``out``: a NormGrads to write; its dx may be ``dz`` or ``dres``."""
-        if h.dim() != 2 or h.shape[1] != self.D:
-            raise ValueError(f"h must be [T, {self.D}], got {tuple(h.shape)}")
         shape = h.shape
+        if len(shape) != 2 or shape[1] != self.D:
+            raise ValueError(f"h must be [T, {self.D}], got {tuple(shape)}")
         T = shape[0]
         self._rows("h", h, self.x_type, shape)
         self._rows("dz", dz, torch.float32, shape)
@@ -129,5 +138,5 @@ class LayerNorm:
             cfg[1], h.data_ptr(), dz.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
             self.gamma.data_ptr(), B._ptr(dres), out.dx.data_ptr(), out.dgamma.data_ptr(),
             B._ptr(out.dbeta), self.workspace.data_ptr(), self.workspace.numel(),
-            B._stream(stream)))
+            B._stream_on(stream, self.device)))
         return out
