@@ -17,13 +17,7 @@
 //   3  y = sum_j gate_j W2 a_j     one row per warp, all rows of an output
 //      column in one block, which adds them in j order
 // No floating-point atomics: sums are taken in a fixed order.
-#include <float.h>
-
-#include <type_traits>
-
-#include "common.cuh"
-#include "decode.h"
-#include "kernels.h"
+#include "decode_common.cuh"
 
 namespace moe {
 namespace {
@@ -33,81 +27,6 @@ constexpr int STAGE = 4096;       // bytes of one stage of a warp's ring
 constexpr int NS = 2;             // stages of a ring
 constexpr int RING = WARPS * NS * STAGE;
 constexpr int TT = 8;             // tokens that share one pass over a weight row
-constexpr int SMEM_MAX = 226 * 1024;   // dynamic part of 227 KB
-constexpr unsigned long long WAIT_NS = 2000000000ull;
-
-// ---- waits: every one is bounded, and an expired one ends the kernel in order
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
-  const unsigned long long t0 = now_ns();
-  while (!mbar_try(bar, parity))
-    if (now_ns() - t0 > WAIT_NS) return false;
-  return true;
-}
-
-// One of the kernel's grid barriers.  Each has a counter of its own, zero on
-// entry; the last block to leave the kernel zeroes them for the next call.
-// Returns false when the wait expired (uniform over the block).
-__device__ bool grid_barrier(int* ctl, int which, int* flag) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int* bar = ctl + DC_BAR + which;
-    __threadfence();
-    atomicAdd(bar, 1);
-    int seen = 0;
-    unsigned long long t0 = 0;
-    while (true) {
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(bar) : "memory");
-      if (seen >= (int)gridDim.x) break;
-      const unsigned long long t = now_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > WAIT_NS) {
-        ctl[DC_STATUS] = DEV_STATUS_TIMEOUT;
-        *flag = 1;
-        break;
-      }
-    }
-    __threadfence();
-  }
-  __syncthreads();
-  return *flag == 0;
-}
-
-// ---- arithmetic on pairs of fp32 values (one instruction for two lanes of a dot product)
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(uint32_t lo, uint32_t hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ float sum2(f32x2 v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return __uint_as_float(lo) + __uint_as_float(hi);
-}
-__device__ __forceinline__ f32x2 widen(uint32_t two_bf16) {
-  return pack2(two_bf16 << 16, two_bf16 & 0xffff0000u);
-}
 
 // Eight values of a weight row and of an activation row for one lane, as four
 // pairs.  Two bf16 rows are read 8 consecutive values a lane; a row beside an
@@ -275,70 +194,48 @@ __device__ __forceinline__ bool one_item(Ring& r, int n, int K, const AT* act, c
   }
 }
 
-// Selection keys as whole numbers in the order of the selection: a larger key
-// first, NaN after every number, an excluded expert (its group was not kept)
-// after both.  Equal ones go to the smaller id.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 1u;
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
 // Shared-memory plan of a call, the same on host and device.
 struct Plan {
-  int R, tiles_max;
-  int off_bar, off_key, off_idx, off_gate, off_tok, off_slot, off_eoff, off_tile, off_red,
-      off_part, off_act;
+  int off_bar, off_idx, off_gate, off_tok, off_slot, off_tile, off_part, off_act;
   int part_rows;      // output rows whose partial results are held at a time
   int act_bytes;      // space for the activations (x, then the hidden values)
-  int total;
 };
 __host__ __device__ inline int up16(int v) { return (v + 15) & ~15; }
 __host__ __device__ inline Plan make_plan(const DecodeArgs& a) {
   Plan p;
-  p.R = a.T * a.k;
-  p.tiles_max = (a.E < p.R ? a.E : p.R) + p.R / TT + (a.Fs ? (a.T + TT - 1) / TT : 0);
-  // the selection's scores and keys live where the ring will be
-  p.off_key = 0;
+  const int R = a.T * a.k;
+  const int tiles = (a.E < R ? a.E : R) + R / TT + (a.Fs ? (a.T + TT - 1) / TT : 0);
+  // (the router's and the selection's scratch lies where the ring will be)
   int o = RING;
   p.off_bar = o; o += up16(WARPS * NS * 8);
-  p.off_red = o; o += up16(WARPS * TT * 4);
-  p.off_idx = o; o += up16(p.R * 2);
-  p.off_gate = o; o += up16(p.R * 4);
-  p.off_tok = o; o += up16(p.R * 2);
-  p.off_slot = o; o += up16(p.R * 2);
-  p.off_eoff = o; o += up16((a.E + 1) * 4);
-  p.off_tile = o; o += up16(p.tiles_max * 8);
+  p.off_idx = o; o += up16(R * 2);
+  p.off_gate = o; o += up16(R * 4);
+  p.off_tok = o; o += up16(R * 2);
+  p.off_slot = o; o += up16(R * 2);
+  p.off_tile = o; o += up16(tiles * 8);
   p.off_part = o;
-  const int row = (p.R + (a.Fs ? a.T : 0)) * 4;
+  const int row = (R + (a.Fs ? a.T : 0)) * 4;
   p.part_rows = 24576 / row < 1 ? 1 : 24576 / row;
   if (p.part_rows > 64) p.part_rows = 64;
   o += up16(p.part_rows * row);
   p.off_act = o;
   p.act_bytes = SMEM_MAX - o;
-  p.total = SMEM_MAX;
   return p;
 }
-struct Tile {
-  short e, n;         // expert (-1: the shared branch), tokens
-  int start;          // first slot (first token for the shared branch)
-};
 
 template <typename WT>
 __global__ void __launch_bounds__(THREADS, 1)
 decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(128) char sm[];
-  __shared__ int flag, n_tiles, n_routed;
+  __shared__ int flag, n_tiles, n_routed, scan[16];
   const Plan P = make_plan(a);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = a.T, D = a.D, F = a.F, E = a.E, k = a.k, R = P.R;
+  const int T = a.T, D = a.D, F = a.F, k = a.k, R = T * k;
   const int G = gridDim.x, cta = blockIdx.x;
-  short* idx_s = reinterpret_cast<short*>(sm + P.off_idx);
-  float* gate_s = reinterpret_cast<float*>(sm + P.off_gate);
-  short* tok_s = reinterpret_cast<short*>(sm + P.off_tok);
-  short* slot_s = reinterpret_cast<short*>(sm + P.off_slot);
-  int* eoff = reinterpret_cast<int*>(sm + P.off_eoff);
-  Tile* tiles = reinterpret_cast<Tile*>(sm + P.off_tile);
+  const Routing rt{reinterpret_cast<short*>(sm + P.off_idx), reinterpret_cast<float*>(sm + P.off_gate),
+                   reinterpret_cast<short*>(sm + P.off_tok), reinterpret_cast<short*>(sm + P.off_slot),
+                   reinterpret_cast<Tile*>(sm + P.off_tile), scan};
+  const Tile* tiles = rt.tiles;
   float* part = reinterpret_cast<float*>(sm + P.off_part);
   char* act = sm + P.off_act;
   const WT* x = static_cast<const WT*>(a.x);
@@ -353,57 +250,10 @@ decode_kernel(const DecodeArgs a) {
     return;
   }
 
-  // ---- 1: logits.  The layer multiplies with W_g in its own type, as its
-  // training forward does; products are exact or fp32, each thread's chain is
-  // a few terms long and the rest is a tree.
-  float* red = reinterpret_cast<float*>(sm + P.off_red);
-  const int ntt = (T + TT - 1) / TT;
-  for (int u = cta; u < E * ntt; u += G) {
-    const int e = u / ntt, t0 = (u % ntt) * TT, nt = min(TT, T - t0);
-    float s[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) s[t] = 0.f;
-    for (int d = tid * 4; d < D; d += THREADS * 4) {
-      float4 w = __ldg(reinterpret_cast<const float4*>(a.w_gate + (long long)e * D + d));
-      if constexpr (sizeof(WT) == 2) {
-        w.x = to_f(from_f<bf16>(w.x)); w.y = to_f(from_f<bf16>(w.y));
-        w.z = to_f(from_f<bf16>(w.z)); w.w = to_f(from_f<bf16>(w.w));
-      }
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        if (t < nt) {
-          const WT* px = x + (long long)(t0 + t) * D + d;
-          float4 v;
-          if constexpr (sizeof(WT) == 2) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(px));
-            v = make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
-                            __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
-          } else {
-            v = __ldg(reinterpret_cast<const float4*>(px));
-          }
-          s[t] = fmaf(w.x, v.x, s[t]);
-          s[t] = fmaf(w.y, v.y, s[t]);
-          s[t] = fmaf(w.z, v.z, s[t]);
-          s[t] = fmaf(w.w, v.w, s[t]);
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      if (t < nt) {
-        const float v = warp_sum(s[t]);
-        if (lane == 0) red[warp * TT + t] = v;
-      }
-    }
-    __syncthreads();
-    if (tid < nt) {
-      float v = 0.f;
-      for (int w = 0; w < WARPS; ++w) v += red[w * TT + tid];
-      if (a.logit_bias != nullptr) v += a.logit_bias[e];
-      __stcg(a.logits + (long long)(t0 + tid) * E + e, v);
-    }
-    __syncthreads();
-  }
+  // ---- 1: logits; several experts a unit once there are units enough
+  float* scratch = reinterpret_cast<float*>(sm);
+  if (a.E * ((T + 7) / 8) > 2 * G) router_logits<WT, 4, WARPS>(a, scratch);
+  else router_logits<WT, 1, WARPS>(a, scratch);
   // the tokens into shared memory while the other blocks finish their logits
   const bool x_in = (long long)T * D * (int)sizeof(WT) <= P.act_bytes;
   if (x_in) {
@@ -411,130 +261,9 @@ decode_kernel(const DecodeArgs a) {
     for (int i = tid; i < n16; i += THREADS)
       reinterpret_cast<uint4*>(act)[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
   }
-  bool ok = grid_barrier(a.ctl, 0, &flag);
-
-  // ---- selection: scores and keys (one warp per token), kept groups, then
-  // each expert's place among its token's keys by counting the ones before it
-  if (ok) {
-    float* sc = reinterpret_cast<float*>(sm + P.off_key);
-    uint32_t* key = reinterpret_cast<uint32_t*>(sc + T * E);
-    for (int t = warp; t < T; t += WARPS) {
-      const float* lg = a.logits + (long long)t * E;
-      float m = -FLT_MAX, z = 0.f;
-      if (a.score == 0) {
-        for (int e = lane; e < E; e += 32) m = fmaxf(m, __ldcg(lg + e));
-        m = warp_max(m);
-      }
-      for (int e = lane; e < E; e += 32) {
-        const float l = __ldcg(lg + e);
-        const float s = a.score == 0 ? expf(l - m) : sigmoidf_(l);
-        sc[t * E + e] = s;
-        z += s;
-      }
-      z = warp_sum(z);
-      const float inv = a.score == 0 ? 1.0f / z : 1.0f;
-      for (int e = lane; e < E; e += 32) {
-        const float s = a.score == 0 ? sc[t * E + e] * inv : sc[t * E + e];
-        sc[t * E + e] = s;
-        const float kv = a.corr_bias != nullptr ? s + a.corr_bias[e] : s;
-        key[t * E + e] = __float_as_uint(kv);    // ordered below, once the groups are ranked
-      }
-    }
-    __syncthreads();
-    const int NG = a.n_groups, per = E / NG;
-    if (NG > 1) {
-      float* gs = part;                                // [T][NG], before `part` is in use
-      for (int i = tid; i < T * NG; i += THREADS) {
-        const uint32_t* row = key + (i / NG) * E + (i % NG) * per;
-        float m1 = -INFINITY, m2 = -INFINITY;
-        for (int e = 0; e < per; ++e) {
-          const float v = __uint_as_float(row[e]);
-          if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
-        }
-        gs[i] = (per == 1 || a.group_score == 1) ? m1 : m1 + m2;
-      }
-      __syncthreads();
-      for (int i = tid; i < T * E; i += THREADS) {
-        const int t = i / E, g = (i % E) / per;
-        const uint32_t mine = order_key(gs[t * NG + g]);
-        int before = 0;
-        for (int h = 0; h < NG; ++h) {
-          const uint32_t o = order_key(gs[t * NG + h]);
-          before += (o > mine || (o == mine && h < g)) ? 1 : 0;
-        }
-        key[i] = before < a.topk_groups ? order_key(__uint_as_float(key[i])) : 0u;
-      }
-    } else {
-      for (int i = tid; i < T * E; i += THREADS) key[i] = order_key(__uint_as_float(key[i]));
-    }
-    __syncthreads();
-    int P2 = 1;                                        // lanes that share one expert's count
-    while (P2 < 32 && T * E * P2 * 2 <= THREADS) P2 *= 2;
-    const int rounds = (T * E * P2 + THREADS - 1) / THREADS;
-    for (int q = 0; q < rounds; ++q) {
-      const int g = q * THREADS + tid, i = g / P2, p = g % P2;
-      const bool on = i < T * E;
-      const int t = on ? i / E : 0, e = on ? i % E : 0;
-      const uint32_t* row = key + t * E;
-      const uint32_t mine = row[e];
-      int before = 0;
-      for (int j = p; j < E; j += P2) {
-        const uint32_t o = row[j];
-        before += (o > mine || (o == mine && j < e)) ? 1 : 0;
-      }
-      for (int o = P2 / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-      if (on && p == 0 && before < k) {
-        idx_s[t * k + before] = (short)e;
-        gate_s[t * k + before] = sc[t * E + e];
-      }
-    }
-    __syncthreads();
-    for (int t = tid; t < T; t += THREADS) {
-      float s = 0.f;
-      for (int j = 0; j < k; ++j) s += gate_s[t * k + j];
-      for (int j = 0; j < k; ++j) gate_s[t * k + j] /= s;
-    }
-    // expert-major slots in token order, the first `cap` of each expert
-    int mine = 0;
-    if (tid < E) {
-      for (int r = 0; r < R; ++r) mine += idx_s[r] == tid ? 1 : 0;
-      mine = min(mine, a.cap);
-      eoff[tid + 1] = mine;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int o = 0, nt = 0;
-      eoff[0] = 0;
-      for (int e = 0; e < E; ++e) {
-        const int c = eoff[e + 1];
-        for (int i = 0; i < c; i += TT) tiles[nt++] = Tile{(short)e, (short)min(TT, c - i), o + i};
-        o += c;
-        eoff[e + 1] = o;
-      }
-      n_routed = nt;
-      if (a.Fs > 0)
-        for (int t = 0; t < T; t += TT) tiles[nt++] = Tile{(short)-1, (short)min(TT, T - t), t};
-      n_tiles = nt;
-    }
-    __syncthreads();
-    if (tid < E) {
-      int o = eoff[tid], c = 0;
-      for (int r = 0; r < R; ++r) {
-        if (idx_s[r] != tid) continue;
-        if (c < mine) tok_s[o + c] = (short)(r / k);
-        slot_s[r] = c < mine ? (short)(o + c) : (short)-1;
-        ++c;
-      }
-    }
-    __syncthreads();
-    if (cta == 0) {
-      for (int r = tid; r < R; r += THREADS) {
-        if (a.idx != nullptr) a.idx[r] = idx_s[r];
-        if (a.gate != nullptr) a.gate[r] = gate_s[r];
-      }
-    }
-  }
-  // the ring's memory held the keys: order those accesses before the copies
+  bool ok = grid_barrier<THREADS>(a.ctl, 0, &flag);
+  if (ok) select_all<WARPS>(a, rt, TT, scratch, &n_routed, &n_tiles);
+  // the ring's memory held scratch: order those accesses before the copies
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
 
@@ -570,7 +299,7 @@ decode_kernel(const DecodeArgs a) {
     for (int q = gw; q < rows_up && ok; q += step) {
       const Item it = up_src(q);
       const Tile tl = tiles[it.tile];
-      auto off_of = [&](int t) { return (tl.e >= 0 ? tok_s[tl.start + t] : tl.start + t) * D; };
+      auto off_of = [&](int t) { return (tl.e >= 0 ? rt.tok[tl.start + t] : tl.start + t) * D; };
       auto emit = [&](int t, float h1, float h3) {
         float v;
         if (PAIR) {
@@ -617,7 +346,7 @@ decode_kernel(const DecodeArgs a) {
     if (ok)
       for (int s = 0; s < NS; ++s) refill();
     if (r0 == 0) {
-      const bool all = grid_barrier(a.ctl, 1, &flag);
+      const bool all = grid_barrier<THREADS>(a.ctl, 1, &flag);
       ok = ok && all;
       if (a_in && all) {
         const int n1 = R * F / 4, n2 = T * a.Fs / 4;
@@ -648,11 +377,11 @@ decode_kernel(const DecodeArgs a) {
       const long long d = cta + (long long)(r0 + row) * G;
       float v = 0.f;
       for (int j = 0; j < k; ++j) {
-        const int s = slot_s[t * k + j];
+        const int s = rt.slot[t * k + j];
         if (s < 0) continue;
         float h = part[row * prow + s];
-        if (a.b2 != nullptr) h += a.b2[(long long)idx_s[t * k + j] * D + d];
-        v = fmaf(gate_s[t * k + j], h, v);
+        if (a.b2 != nullptr) h += a.b2[(long long)rt.idx[t * k + j] * D + d];
+        v = fmaf(rt.gate[t * k + j], h, v);
       }
       if (a.Fs > 0) v += part[row * prow + R + t];
       if (ok) static_cast<WT*>(a.y)[(long long)t * D + d] = from_f<WT>(v);
@@ -666,12 +395,7 @@ decode_kernel(const DecodeArgs a) {
     ++ring.got;
   }
   __syncthreads();
-  if (tid == 0 && atomicAdd(a.ctl + DC_EXIT, 1) == G - 1) {
-    a.ctl[DC_BAR] = 0;
-    a.ctl[DC_BAR + 1] = 0;
-    __threadfence();
-    a.ctl[DC_EXIT] = 0;
-  }
+  if (tid == 0) leave(a.ctl);
 }
 
 __global__ void decode_init_kernel(int* ctl) {
@@ -695,28 +419,14 @@ int sm_count() {
 }  // namespace
 
 template <typename WT>
-static cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
+static cudaError_t launch_t(const DecodeArgs& a, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = ensure_dynamic_smem(decode_kernel<WT>, SMEM_MAX, attr_done);
-  if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorUnknown;
-  cudaLaunchConfig_t cfg = {};
   // a block per SM, or fewer where each would have less than 16 KB of weights
   const long long experts = (long long)a.T * a.k < a.E ? (long long)a.T * a.k : a.E;
   const long long bytes = (experts * a.F + a.Fs) * a.D * (a.act == 2 ? 3 : 2) * (int)sizeof(WT);
-  long long blocks = (bytes + 16383) / 16384;
-  if (blocks > sms) blocks = sms;
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM_MAX;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;   // the blocks wait on one another
-  attr[0].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<WT>, a);
+  const long long blocks = (bytes + 16383) / 16384;
+  return launch_cooperative(decode_kernel<WT>, (int)(blocks < sms ? blocks : sms), THREADS,
+                            attr_done, st, a);
 }
 
 cudaError_t launch_decode_init(int* ctl, cudaStream_t st) {
@@ -724,7 +434,10 @@ cudaError_t launch_decode_init(int* ctl, cudaStream_t st) {
 }
 
 cudaError_t launch_decode(int dtype, const DecodeArgs& a, cudaStream_t st) {
-  return dtype == 1 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorUnknown;
+  if (dtype == 1 && decode_mma_fits(a)) return launch_decode_mma(a, sms, st);
+  return dtype == 1 ? launch_t<bf16>(a, sms, st) : launch_t<float>(a, sms, st);
 }
 
 }  // namespace moe

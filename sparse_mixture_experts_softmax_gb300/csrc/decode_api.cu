@@ -21,7 +21,7 @@ moe_status check_decode(const moe_config* cfg) {
 }
 
 struct DecodeLayout {
-  size_t logits, hidden, hidden_s, total;
+  size_t logits, hidden, hidden_s, ye, total;
 };
 DecodeLayout decode_layout(const moe_config& c) {
   DecodeLayout L{};
@@ -33,6 +33,8 @@ DecodeLayout decode_layout(const moe_config& c) {
   o += align_up(R * c.F * 4);
   L.hidden_s = o;
   o += align_up(T * Fs * 4);
+  L.ye = o;      // (for every T: the size must not shrink as T grows)
+  if (c.dtype == MOE_BF16) o += align_up((R + (Fs ? T : 0)) * c.D * 4);
   L.total = o;
   return L;
 }
@@ -100,6 +102,7 @@ moe_status moe_decode(const moe_config* cfg, const moe_weights* w, const void* x
   a.logits = reinterpret_cast<float*>(base + L.logits);
   a.hidden = reinterpret_cast<float*>(base + L.hidden);
   a.hidden_s = reinterpret_cast<float*>(base + L.hidden_s);
+  a.ye = reinterpret_cast<float*>(base + L.ye);
   KL("decode", launch_decode(c.dtype, a, st));
   return MOE_OK;
 }

@@ -1,0 +1,420 @@
+// What the two kernels of the few-token MoE layer share: bounded waits, the grid
+// barrier, the router's logits and the selection.
+#pragma once
+
+#include <float.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "decode.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int SMEM_MAX = 226 * 1024;   // dynamic part of 227 KB
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+// ---- waits: every one is bounded, and an expired one ends the kernel in order
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try(bar, parity))
+    if (now_ns() - t0 > WAIT_NS) return false;
+  return true;
+}
+
+// One of the kernel's grid barriers.  Each has a counter of its own, zero on
+// entry; the last block to leave the kernel zeroes them for the next call.
+// Returns false when the wait expired (uniform over the block).
+// The first NTHREADS threads of the block take part.
+template <int NTHREADS>
+__device__ __forceinline__ void bar_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+}
+template <int NTHREADS>
+__device__ __forceinline__ bool grid_barrier(int* ctl, int which, int* flag) {
+  bar_sync<NTHREADS>();
+  if (threadIdx.x == 0) {
+    int* bar = ctl + DC_BAR + which;
+    __threadfence();
+    atomicAdd(bar, 1);
+    int seen = 0;
+    unsigned long long t0 = 0;
+    while (true) {
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(bar) : "memory");
+      if (seen >= (int)gridDim.x) break;
+      const unsigned long long t = now_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > WAIT_NS) {
+        ctl[DC_STATUS] = DEV_STATUS_TIMEOUT;
+        *flag = 1;
+        break;
+      }
+    }
+    __threadfence();
+  }
+  bar_sync<NTHREADS>();
+  return *flag == 0;
+}
+
+// ---- arithmetic on pairs of fp32 values (one instruction for two lanes of a dot product)
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(uint32_t lo, uint32_t hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return __uint_as_float(lo) + __uint_as_float(hi);
+}
+__device__ __forceinline__ f32x2 widen(uint32_t two_bf16) {
+  return pack2(two_bf16 << 16, two_bf16 & 0xffff0000u);
+}
+
+
+// Sums 32 values over the warp at once: lane l gets the whole sum of v[l].
+// (31 exchanges; one at a time they would take 160.)
+__device__ __forceinline__ float warp_sum32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+// Logits of the units (EB experts, 8 tokens) that fall to this block, one unit
+// at a time by its NW warps.  The layer multiplies with W_g in its own type, as
+// its training forward does; bf16 products are exact in fp32, a thread's chain
+// is a few terms long and the rest is a tree, so that a near-tie of two experts
+// is as narrow as fp32 allows.  red: NW * 32 floats of shared memory.
+template <typename WT, int EB, int NW>
+__device__ __forceinline__ void router_logits(const DecodeArgs& a, float* red) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.T, D = a.D, E = a.E;
+  const int ntt = (T + 7) / 8, neb = (E + EB - 1) / EB;
+  const WT* x = static_cast<const WT*>(a.x);
+  for (int u = blockIdx.x; u < neb * ntt; u += gridDim.x) {
+    const int e0 = (u / ntt) * EB, t0 = (u % ntt) * 8, nt = min(8, T - t0), ne = min(EB, E - e0);
+    float s[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = 0.f;
+    for (int d = tid * 4; d < D; d += NW * 128) {
+      float w[EB][4];
+#pragma unroll
+      for (int e = 0; e < EB; ++e) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(
+            a.w_gate + (long long)(e0 + min(e, ne - 1)) * D + d));
+        w[e][0] = q.x; w[e][1] = q.y; w[e][2] = q.z; w[e][3] = q.w;
+        if constexpr (sizeof(WT) == 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[e][i] = to_f(from_f<bf16>(w[e][i]));
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (t < nt) {
+          const WT* px = x + (long long)(t0 + t) * D + d;
+          float v[4];
+          if constexpr (sizeof(WT) == 2) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(px));
+            v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+            v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+          } else {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(px));
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+          }
+#pragma unroll
+          for (int e = 0; e < EB; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[e * 8 + t] = fmaf(w[e][i], v[i], s[e * 8 + t]);
+        }
+      }
+    }
+    if (EB * nt == 1) {
+      const float v = warp_sum(s[0]);
+      if (lane == 0) red[warp * 32] = v;
+    } else {
+      red[warp * 32 + lane] = warp_sum32(s, lane);
+    }
+    __syncthreads();
+    if (tid < EB * 8) {
+      const int e = tid / 8, t = tid % 8;
+      if (e < ne && t < nt) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += red[w * 32 + tid];
+        if (a.logit_bias != nullptr) v += a.logit_bias[e0 + e];
+        __stcg(a.logits + (long long)(t0 + t) * E + e0 + e, v);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Selection keys as whole numbers in the order of the selection: a larger key
+// first, NaN after every number; 0 is left for what may not be chosen.  Equal
+// ones go to the smaller id.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 1u;
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// One token's scores, kept groups, k experts and gates by one warp; a lane
+// holds the experts lane + 32 c, c < NC.  Each of the k picks is two
+// whole-number reductions: the largest key, then the smallest id that has it.
+// row: E floats of shared memory of the warp's own.
+template <int NC>
+__device__ __forceinline__ void select_token(const DecodeArgs& a, const float* logits, float* row,
+                                             short* idx, float* gate, uint32_t* mask, uint32_t bit,
+                                             int lane) {
+  const int E = a.E, k = a.k;
+  float s[NC];
+  uint32_t key[NC];
+  float m = -FLT_MAX, z = 0.f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int e = lane + 32 * c;
+    s[c] = e < E ? __ldcg(logits + e) : -INFINITY;
+  }
+  if (a.score == 0) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) m = fmaxf(m, s[c]);
+    m = warp_max(m);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      s[c] = lane + 32 * c < E ? expf(s[c] - m) : 0.f;
+      z += s[c];
+    }
+    const float inv = 1.0f / warp_sum(z);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) s[c] *= inv;
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) s[c] = sigmoidf_(s[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int e = lane + 32 * c;
+    const float kv = (a.corr_bias != nullptr && e < E) ? s[c] + a.corr_bias[e] : s[c];
+    key[c] = e < E ? order_key(kv) : 0u;
+    if (e < E) row[e] = kv;
+  }
+  if (a.n_groups > 1) {
+    const int NG = a.n_groups, per = E / NG;
+    __syncwarp();
+    uint32_t gk = 0u;
+    if (lane < NG) {
+      float m1 = -INFINITY, m2 = -INFINITY;
+      for (int e = lane * per; e < (lane + 1) * per; ++e) {
+        const float v = row[e];
+        if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
+      }
+      gk = order_key((per == 1 || a.group_score == 1) ? m1 : m1 + m2);
+    }
+    uint32_t keep = 0u;
+    for (int r = 0; r < a.topk_groups; ++r) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, gk);
+      const int g = __ffs(__ballot_sync(0xffffffffu, lane < NG && gk == best)) - 1;
+      keep |= 1u << g;
+      if (lane == g) gk = 0u;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int e = lane + 32 * c;
+      if (e < E && !((keep >> (e / per)) & 1u)) key[c] = 0u;
+    }
+    __syncwarp();
+  }
+  // the scores take the keys' place: a pick looks its own up at the end
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    if (lane + 32 * c < E) row[lane + 32 * c] = s[c];
+  __syncwarp();
+  int pick = 0;
+  for (int j = 0; j < k; ++j) {
+    uint32_t top = 0u;
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int c = NC - 1; c >= 0; --c)
+      if (key[c] >= top && key[c] != 0u) { top = key[c]; at = lane + 32 * c; }
+    const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+    const int e = __reduce_min_sync(0xffffffffu, top == best ? at : 0x7fffffff);
+    if (lane == j) pick = e;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (lane + 32 * c == e) key[c] = 0u;
+  }
+  const float mine = lane < k ? row[pick] : 0.f;
+  const float sum = warp_sum(mine);
+  if (lane < k) {
+    idx[lane] = (short)pick;
+    gate[lane] = mine / sum;
+    atomicOr(mask + 2 * pick, bit);     // whole numbers: the order does not matter
+  }
+  __syncwarp();
+}
+
+struct Tile {
+  short e, n;         // expert (-1: the shared branch), tokens
+  int start;          // first slot (first token for the shared branch)
+};
+// The routing of a call in shared memory.
+struct Routing {
+  short* idx;         // [T, k]
+  float* gate;        // [T, k]
+  short* tok;         // [R] slot -> token; slots are expert-major, tokens ascending
+  short* slot;        // [T, k] -> slot, or -1 (dropped by the capacity)
+  Tile* tiles;        // token tiles of the chosen experts, then of the shared branch
+  int* scan;          // 2 * 8 words of scratch
+};
+
+// Selection and the expert-major lists, by NW warps (every block for itself:
+// cheaper than another grid barrier).  An expert's tokens are a mask of at most
+// 64 bits, so that its count, its slots' order and the capacity's cut are
+// population counts.  TT: tokens of a tile; scratch: 768 + NW * E words.
+template <int NW>
+__device__ __forceinline__ void select_all(const DecodeArgs& a, const Routing& r, int TT,
+                                           float* scratch, int* n_routed, int* n_tiles) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.T, E = a.E, k = a.k, R = T * k;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(scratch);      // [256][2]
+  int* base_of = reinterpret_cast<int*>(scratch) + 512;       // [256]
+  float* row = scratch + 768 + warp * E;
+  for (int i = tid; i < 512; i += NW * 32) mask[i] = 0u;
+  __syncthreads();
+  for (int t = warp; t < T; t += NW) {
+    const float* lg = a.logits + (long long)t * E;
+    short* ix = r.idx + t * k;
+    float* gt = r.gate + t * k;
+    uint32_t* mk = mask + (t >> 5);
+    const uint32_t bit = 1u << (t & 31);
+    if (E <= 32) select_token<1>(a, lg, row, ix, gt, mk, bit, lane);
+    else if (E <= 64) select_token<2>(a, lg, row, ix, gt, mk, bit, lane);
+    else if (E <= 128) select_token<4>(a, lg, row, ix, gt, mk, bit, lane);
+    else select_token<8>(a, lg, row, ix, gt, mk, bit, lane);
+  }
+  __syncthreads();
+  // expert tid's first slot and tiles: scans over the experts' kept counts
+  int mine = 0, mt = 0, incl = 0, incl_t = 0;
+  if (warp < 8) {
+    mine = min(__popc(mask[2 * tid]) + __popc(mask[2 * tid + 1]), a.cap);
+    mt = (mine + TT - 1) / TT;
+    incl = mine;
+    incl_t = mt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_t, o);
+      if (lane >= o) {
+        incl += u;
+        incl_t += v;
+      }
+    }
+    if (lane == 31) {
+      r.scan[warp] = incl;
+      r.scan[8 + warp] = incl_t;
+    }
+  }
+  __syncthreads();
+  if (warp < 8) {
+    int base = incl - mine, tile = incl_t - mt, total_t = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) {
+        base += r.scan[w];
+        tile += r.scan[8 + w];
+      }
+      total_t += r.scan[8 + w];
+    }
+    base_of[tid] = base;
+    for (int i = 0; i < mine; i += TT)
+      r.tiles[tile++] = Tile{(short)tid, (short)min(TT, mine - i), base + i};
+    const int nsh = a.Fs > 0 ? (T + TT - 1) / TT : 0;
+    if (tid < nsh)
+      r.tiles[total_t + tid] = Tile{(short)-1, (short)min(TT, T - tid * TT), tid * TT};
+    if (tid == 0) {
+      *n_routed = total_t;
+      *n_tiles = total_t + nsh;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < R; i += NW * 32) {
+    const int e = r.idx[i], t = i / k;
+    const uint32_t below = (1u << (t & 31)) - 1u;
+    const int place = t < 32 ? __popc(mask[2 * e] & below)
+                             : __popc(mask[2 * e]) + __popc(mask[2 * e + 1] & below);
+    const int s = base_of[e] + place;
+    const bool kept = place < a.cap;
+    r.slot[i] = kept ? (short)s : (short)-1;
+    if (kept) r.tok[s] = (short)t;
+    if (blockIdx.x == 0) {
+      if (a.idx != nullptr) a.idx[i] = e;
+      if (a.gate != nullptr) a.gate[i] = r.gate[i];
+    }
+  }
+  __syncthreads();
+}
+
+// The last block out zeroes the barriers' counters for the next call.
+__device__ __forceinline__ void leave(int* ctl) {
+  if (atomicAdd(ctl + DC_EXIT, 1) == (int)gridDim.x - 1) {
+    ctl[DC_BAR] = 0;
+    ctl[DC_BAR + 1] = 0;
+    ctl[DC_BAR + 2] = 0;
+    __threadfence();
+    ctl[DC_EXIT] = 0;
+  }
+}
+
+// Launches `kernel` with one block per SM at most, all resident together (its
+// blocks wait on one another).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cooperative(void (*kernel)(KArgs...), int blocks, int threads,
+                               std::atomic<unsigned long long>& attr_done, cudaStream_t st,
+                               const Args&... args) {
+  cudaError_t e = ensure_dynamic_smem(kernel, SMEM_MAX, attr_done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = SMEM_MAX;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+}  // namespace moe
