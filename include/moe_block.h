@@ -92,7 +92,7 @@ MOE_API moe_status moe_decode(const moe_config* cfg, const moe_weights* w, const
 /* Reads the device status of the calls since moe_decode_init: 0, MOE_ERR_TIMEOUT
  * when a bounded device-side wait expired (the call ended early and its outputs
  * are invalid), or MOE_ERR_INVALID_ARG when a call found its workspace without
- * moe_decode_init (it wrote nothing else).  Synchronises `stream`. */
+ * moe_decode_init (it wrote no output).  Synchronises `stream`. */
 MOE_API moe_status moe_decode_status(const moe_config* cfg, const void* workspace,
                                      size_t workspace_bytes, int32_t* status_host, void* stream);
 

@@ -225,7 +225,7 @@ __host__ __device__ inline Plan make_plan(const DecodeArgs& a) {
 
 template <typename WT>
 __global__ void __launch_bounds__(THREADS, 1)
-decode_kernel(const DecodeArgs a) {
+decode_kernel(const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(128) char sm[];
   __shared__ int flag, n_tiles, n_routed, scan[16];
   const Plan P = make_plan(a);
@@ -240,26 +240,27 @@ decode_kernel(const DecodeArgs a) {
   char* act = sm + P.off_act;
   const WT* x = static_cast<const WT*>(a.x);
 
-  if (tid == 0) flag = a.ctl[DC_MAGIC] == DECODE_MAGIC ? 0 : 2;
+  const int magic = tid == 0 ? __ldcg(a.ctl + DC_MAGIC) : 0;     // (looked at after the logits)
   if (tid < WARPS * NS)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(sm + P.off_bar) + tid * 8));
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
-  if (flag != 0) {   // the workspace was not initialised: the counters mean nothing
-    if (tid == 0) a.ctl[DC_STATUS] = DEV_STATUS_INVALID_INDEX;
-    return;
-  }
 
-  // ---- 1: logits; several experts a unit once there are units enough
+  // ---- 1: logits
   float* scratch = reinterpret_cast<float*>(sm);
-  if (a.E * ((T + 7) / 8) > 2 * G) router_logits<WT, 4, WARPS>(a, scratch);
-  else router_logits<WT, 1, WARPS>(a, scratch);
+  router<WT, WARPS>(a, scratch);
   // the tokens into shared memory while the other blocks finish their logits
   const bool x_in = (long long)T * D * (int)sizeof(WT) <= P.act_bytes;
   if (x_in) {
     const int n16 = T * D * (int)sizeof(WT) / 16;
     for (int i = tid; i < n16; i += THREADS)
       reinterpret_cast<uint4*>(act)[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
+  }
+  if (tid == 0) flag = magic == DECODE_MAGIC ? 0 : 2;
+  __syncthreads();
+  if (flag != 0) {   // the workspace was not initialised: the counters mean nothing
+    if (tid == 0) a.ctl[DC_STATUS] = DEV_STATUS_INVALID_INDEX;
+    return;
   }
   bool ok = grid_barrier<THREADS>(a.ctl, 0, &flag);
   if (ok) select_all<WARPS>(a, rt, TT, scratch, &n_routed, &n_tiles);
@@ -421,10 +422,10 @@ int sm_count() {
 template <typename WT>
 static cudaError_t launch_t(const DecodeArgs& a, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  // a block per SM, or fewer where each would have less than 16 KB of weights
+  // a block per SM, or fewer where each would have less than 4 KB of weights
   const long long experts = (long long)a.T * a.k < a.E ? (long long)a.T * a.k : a.E;
   const long long bytes = (experts * a.F + a.Fs) * a.D * (a.act == 2 ? 3 : 2) * (int)sizeof(WT);
-  const long long blocks = (bytes + 16383) / 16384;
+  const long long blocks = (bytes + 4095) / 4096;
   return launch_cooperative(decode_kernel<WT>, (int)(blocks < sms ? blocks : sms), THREADS,
                             attr_done, st, a);
 }

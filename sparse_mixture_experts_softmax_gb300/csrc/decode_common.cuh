@@ -1,5 +1,10 @@
 // What the two kernels of the few-token MoE layer share: bounded waits, the grid
 // barrier, the router's logits and the selection.
+//
+// A block runs most of this once and from a cold instruction cache, where the
+// weights that stream through L2 leave nothing of the last call's code: the
+// larger pieces are functions of their own, not inlined at every use (one token
+// of the large layer: 90 -> 79 us).
 #pragma once
 
 #include <float.h>
@@ -53,6 +58,7 @@ __device__ __forceinline__ void bar_sync() {
 template <int NTHREADS>
 __device__ __forceinline__ bool grid_barrier(int* ctl, int which, int* flag) {
   bar_sync<NTHREADS>();
+  if (gridDim.x == 1) return *flag == 0;
   if (threadIdx.x == 0) {
     int* bar = ctl + DC_BAR + which;
     __threadfence();
@@ -111,19 +117,19 @@ __device__ __forceinline__ float warp_sum32(float (&v)[32], int lane) {
   return v[0];
 }
 
-// Logits of the units (EB experts, 8 tokens) that fall to this block, one unit
+// Logits of the units (EB experts, TB tokens) that fall to this block, one unit
 // at a time by its NW warps.  The layer multiplies with W_g in its own type, as
 // its training forward does; bf16 products are exact in fp32, a thread's chain
 // is a few terms long and the rest is a tree, so that a near-tie of two experts
 // is as narrow as fp32 allows.  red: NW * 32 floats of shared memory.
-template <typename WT, int EB, int NW>
-__device__ __forceinline__ void router_logits(const DecodeArgs& a, float* red) {
+template <typename WT, int EB, int TB, int NW>
+__device__ __noinline__ void router_logits(const DecodeArgs& a, float* red) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = a.T, D = a.D, E = a.E;
-  const int ntt = (T + 7) / 8, neb = (E + EB - 1) / EB;
+  const int ntt = (T + TB - 1) / TB, neb = (E + EB - 1) / EB;
   const WT* x = static_cast<const WT*>(a.x);
   for (int u = blockIdx.x; u < neb * ntt; u += gridDim.x) {
-    const int e0 = (u / ntt) * EB, t0 = (u % ntt) * 8, nt = min(8, T - t0), ne = min(EB, E - e0);
+    const int e0 = (u / ntt) * EB, t0 = (u % ntt) * TB, nt = min(TB, T - t0), ne = min(EB, E - e0);
     float s[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) s[i] = 0.f;
@@ -139,27 +145,29 @@ __device__ __forceinline__ void router_logits(const DecodeArgs& a, float* red) {
           for (int i = 0; i < 4; ++i) w[e][i] = to_f(from_f<bf16>(w[e][i]));
         }
       }
+      // absent tokens repeat the last one: a branch here would make the loads
+      // wait for one another
+      float v[TB][4];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t < nt) {
-          const WT* px = x + (long long)(t0 + t) * D + d;
-          float v[4];
-          if constexpr (sizeof(WT) == 2) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(px));
-            v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
-            v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
-          } else {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(px));
-            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-          }
-#pragma unroll
-          for (int e = 0; e < EB; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[e * 8 + t] = fmaf(w[e][i], v[i], s[e * 8 + t]);
+      for (int t = 0; t < TB; ++t) {
+        const WT* px = x + (long long)(t0 + min(t, nt - 1)) * D + d;
+        if constexpr (sizeof(WT) == 2) {
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(px));
+          v[t][0] = __uint_as_float(q.x << 16); v[t][1] = __uint_as_float(q.x & 0xffff0000u);
+          v[t][2] = __uint_as_float(q.y << 16); v[t][3] = __uint_as_float(q.y & 0xffff0000u);
+        } else {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(px));
+          v[t][0] = q.x; v[t][1] = q.y; v[t][2] = q.z; v[t][3] = q.w;
         }
       }
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int e = 0; e < EB; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[e * 8 + t] = fmaf(w[e][i], v[t][i], s[e * 8 + t]);
     }
-    if (EB * nt == 1) {
+    if (EB * TB == 1) {
       const float v = warp_sum(s[0]);
       if (lane == 0) red[warp * 32] = v;
     } else {
@@ -180,6 +188,13 @@ __device__ __forceinline__ void router_logits(const DecodeArgs& a, float* red) {
   }
 }
 
+template <typename WT, int NW>
+__device__ __forceinline__ void router(const DecodeArgs& a, float* red) {
+  if (a.T == 1) router_logits<WT, 1, 1, NW>(a, red);
+  else if (a.E * ((a.T + 7) / 8) > 2 * (int)gridDim.x) router_logits<WT, 4, 8, NW>(a, red);
+  else router_logits<WT, 1, 8, NW>(a, red);
+}
+
 // Selection keys as whole numbers in the order of the selection: a larger key
 // first, NaN after every number; 0 is left for what may not be chosen.  Equal
 // ones go to the smaller id.
@@ -189,24 +204,25 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One token's scores, kept groups, k experts and gates by one warp; a lane
-// holds the experts lane + 32 c, c < NC.  Each of the k picks is two
-// whole-number reductions: the largest key, then the smallest id that has it.
-// row: E floats of shared memory of the warp's own.
+// Token t's scores, kept groups, k experts and gates by one warp; a lane holds
+// the experts lane + 32 c, c < NC.  Each of the k picks is two whole-number
+// reductions: the largest key, then the smallest id that has it.  (Two or four
+// tokens side by side in a warp cost more in cold code than they save.)  row: E
+// floats of shared memory of the warp's own; mask: see select_all.
 template <int NC>
-__device__ __forceinline__ void select_token(const DecodeArgs& a, const float* logits, float* row,
-                                             short* idx, float* gate, uint32_t* mask, uint32_t bit,
-                                             int lane) {
+__device__ __noinline__ void select_token(const DecodeArgs& a, int t, float* row, short* idx,
+                                          float* gate, uint32_t* mask, int lane) {
   const int E = a.E, k = a.k;
   float s[NC];
   uint32_t key[NC];
-  float m = -FLT_MAX, z = 0.f;
+  const float* lg = a.logits + (long long)t * E;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int e = lane + 32 * c;
-    s[c] = e < E ? __ldcg(logits + e) : -INFINITY;
+    s[c] = e < E ? __ldcg(lg + e) : -INFINITY;
   }
   if (a.score == 0) {
+    float m = -FLT_MAX, z = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) m = fmaxf(m, s[c]);
     m = warp_max(m);
@@ -229,9 +245,9 @@ __device__ __forceinline__ void select_token(const DecodeArgs& a, const float* l
     key[c] = e < E ? order_key(kv) : 0u;
     if (e < E) row[e] = kv;
   }
+  __syncwarp();
   if (a.n_groups > 1) {
     const int NG = a.n_groups, per = E / NG;
-    __syncwarp();
     uint32_t gk = 0u;
     if (lane < NG) {
       float m1 = -INFINITY, m2 = -INFINITY;
@@ -261,6 +277,7 @@ __device__ __forceinline__ void select_token(const DecodeArgs& a, const float* l
     if (lane + 32 * c < E) row[lane + 32 * c] = s[c];
   __syncwarp();
   int pick = 0;
+#pragma unroll 1
   for (int j = 0; j < k; ++j) {
     uint32_t top = 0u;
     int at = 0x7fffffff;
@@ -277,9 +294,9 @@ __device__ __forceinline__ void select_token(const DecodeArgs& a, const float* l
   const float mine = lane < k ? row[pick] : 0.f;
   const float sum = warp_sum(mine);
   if (lane < k) {
-    idx[lane] = (short)pick;
-    gate[lane] = mine / sum;
-    atomicOr(mask + 2 * pick, bit);     // whole numbers: the order does not matter
+    idx[t * k + lane] = (short)pick;
+    gate[t * k + lane] = mine / sum;
+    atomicOr(mask + 2 * pick + (t >> 5), 1u << (t & 31));   // whole numbers: any order
   }
   __syncwarp();
 }
@@ -301,7 +318,7 @@ struct Routing {
 // Selection and the expert-major lists, by NW warps (every block for itself:
 // cheaper than another grid barrier).  An expert's tokens are a mask of at most
 // 64 bits, so that its count, its slots' order and the capacity's cut are
-// population counts.  TT: tokens of a tile; scratch: 768 + NW * E words.
+// population counts.  TT: tokens of a tile; scratch: 768 + NW E words.
 template <int NW>
 __device__ __forceinline__ void select_all(const DecodeArgs& a, const Routing& r, int TT,
                                            float* scratch, int* n_routed, int* n_tiles) {
@@ -313,15 +330,10 @@ __device__ __forceinline__ void select_all(const DecodeArgs& a, const Routing& r
   for (int i = tid; i < 512; i += NW * 32) mask[i] = 0u;
   __syncthreads();
   for (int t = warp; t < T; t += NW) {
-    const float* lg = a.logits + (long long)t * E;
-    short* ix = r.idx + t * k;
-    float* gt = r.gate + t * k;
-    uint32_t* mk = mask + (t >> 5);
-    const uint32_t bit = 1u << (t & 31);
-    if (E <= 32) select_token<1>(a, lg, row, ix, gt, mk, bit, lane);
-    else if (E <= 64) select_token<2>(a, lg, row, ix, gt, mk, bit, lane);
-    else if (E <= 128) select_token<4>(a, lg, row, ix, gt, mk, bit, lane);
-    else select_token<8>(a, lg, row, ix, gt, mk, bit, lane);
+    if (E <= 32) select_token<1>(a, t, row, r.idx, r.gate, mask, lane);
+    else if (E <= 64) select_token<2>(a, t, row, r.idx, r.gate, mask, lane);
+    else if (E <= 128) select_token<4>(a, t, row, r.idx, r.gate, mask, lane);
+    else select_token<8>(a, t, row, r.idx, r.gate, mask, lane);
   }
   __syncthreads();
   // expert tid's first slot and tiles: scans over the experts' kept counts
@@ -386,6 +398,7 @@ __device__ __forceinline__ void select_all(const DecodeArgs& a, const Routing& r
 
 // The last block out zeroes the barriers' counters for the next call.
 __device__ __forceinline__ void leave(int* ctl) {
+  if (gridDim.x == 1) return;
   if (atomicAdd(ctl + DC_EXIT, 1) == (int)gridDim.x - 1) {
     ctl[DC_BAR] = 0;
     ctl[DC_BAR + 1] = 0;

@@ -94,8 +94,11 @@ struct Part {
   int t0;                      // first tile
   int lo, hi;                  // items, counted from the first tile
 };
-__device__ __forceinline__ int share_of(int total, int b) {
-  return (int)((long long)total * b / (int)gridDim.x);
+// First item of block b's share: the blocks' shares are of equal weight bytes.
+__device__ __forceinline__ int share_of(int all_r, int K_r, int all_s, int K_s, int b) {
+  const long long bytes_r = (long long)all_r * K_r;
+  const long long at = (bytes_r + (long long)all_s * K_s) * b / (int)gridDim.x;
+  return at < bytes_r ? (int)(at / K_r) : all_r + (all_s > 0 ? (int)((at - bytes_r) / K_s) : 0);
 }
 template <bool UP>
 __device__ __forceinline__ Part make_part(const DecodeArgs& a, int n_routed, int n_tiles, bool routed) {
@@ -104,9 +107,11 @@ __device__ __forceinline__ Part make_part(const DecodeArgs& a, int n_routed, int
   const int width_r = UP ? a.F : a.D, width_s = UP ? a.Fs : a.D;
   p.rows = pair ? 8 : 16;
   const int per_r = (width_r + p.rows - 1) / p.rows, per_s = (width_s + p.rows - 1) / p.rows;
-  const int all_r = n_routed * per_r, all = all_r + (n_tiles - n_routed) * per_s;
-  const int lo = share_of(all, blockIdx.x), hi = share_of(all, blockIdx.x + 1);
-  p.K = UP ? a.D : (routed ? a.F : a.Fs);
+  const int K_r = UP ? a.D : a.F, K_s = UP ? a.D : a.Fs;
+  const int all_r = n_routed * per_r, all_s = (n_tiles - n_routed) * per_s;
+  const int lo = share_of(all_r, K_r, all_s, K_s, blockIdx.x);
+  const int hi = share_of(all_r, K_r, all_s, K_s, blockIdx.x + 1);
+  p.K = routed ? K_r : K_s;
   p.width = routed ? width_r : width_s;
   p.per = routed ? per_r : per_s;
   p.t0 = routed ? 0 : n_routed;
@@ -228,14 +233,15 @@ __device__ __forceinline__ int warps_per_item(int items, int K) {
   return best;
 }
 
-// The items of a part, by the multiplying warps.  `before` runs between the
-// first weight copies and the tiles' tokens.
-template <bool UP, typename Before>
-__device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, const Routing& rt,
-                                        int tt, int* row_at, char* rows, int rows_bytes, float* red,
-                                        uint32_t ring, const Before& before) {
+// The items of a part, by the multiplying warps.  Where `flag` is given, the grid
+// barrier before the down projection stands between the first weight copies and
+// the tiles' tokens.
+template <bool UP>
+__device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, const Routing& rt, int tt,
+                                        int* row_at, char* rows, int rows_bytes, float* red,
+                                     uint32_t ring, int* flag) {
   if (p.lo >= p.hi) {
-    before();
+    if (!UP && flag != nullptr) grid_barrier<CTHREADS>(a.ctl, 1, flag);
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -280,7 +286,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
   };
 #pragma unroll
   for (int u = 0; u < NS; ++u) put();
-  before();
+  if (!UP && flag != nullptr) grid_barrier<CTHREADS>(a.ctl, 1, flag);
 
   // what is being computed: item, its tile and block
   int i = p.lo + mine, it = i / p.per, ib = i % p.per, parity = 0, slot = 0;
@@ -377,7 +383,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
-decode_mma_kernel(const DecodeArgs a, const int tt) {
+decode_mma_kernel(const __grid_constant__ DecodeArgs a, const int tt) {
   extern __shared__ __align__(128) char sm[];
   __shared__ int flag, n_tiles, n_routed, scan[16];
   const Plan P = make_plan(a.T, a.k, a.E, a.Fs, tt);
@@ -389,16 +395,16 @@ decode_mma_kernel(const DecodeArgs a, const int tt) {
   float* red = reinterpret_cast<float*>(sm + P.off_red);
   char* rows = sm + P.off_rows;
 
-  if (tid == 0) flag = a.ctl[DC_MAGIC] == DECODE_MAGIC ? 0 : 2;
+  const int magic = tid == 0 ? __ldcg(a.ctl + DC_MAGIC) : 0;     // (looked at after the logits)
+
+  float* scratch = reinterpret_cast<float*>(sm);
+  router<bf16, WARPS>(a, scratch);
+  if (tid == 0) flag = magic == DECODE_MAGIC ? 0 : 2;
   __syncthreads();
   if (flag != 0) {   // the workspace was not initialised: the counters mean nothing
     if (tid == 0) a.ctl[DC_STATUS] = DEV_STATUS_INVALID_INDEX;
     return;
   }
-
-  float* scratch = reinterpret_cast<float*>(sm);
-  if (a.E * ((T + 7) / 8) > 2 * (int)gridDim.x) router_logits<bf16, 4, WARPS>(a, scratch);
-  else router_logits<bf16, 1, WARPS>(a, scratch);
   bool ok = grid_barrier<THREADS>(a.ctl, 0, &flag);
   if (ok) select_all<WARPS>(a, rt, tt, scratch, &n_routed, &n_tiles);
   const int nr = ok ? n_routed : 0, nt = ok ? n_tiles : 0;
@@ -407,18 +413,14 @@ decode_mma_kernel(const DecodeArgs a, const int tt) {
   const int warp = tid >> 5;
   if (warp < CW) {
     const uint32_t ring = smem_addr(sm) + warp * NS * STAGE;
-    auto none = [] {};
-    auto wait = [&] { ok = grid_barrier<CTHREADS>(a.ctl, 1, &flag) && ok; };
-    compute<true>(a, make_part<true>(a, nr, nt, true), rt, tt, row_at, rows, P.rows_bytes, red, ring,
-                  none);
-    if (a.Fs > 0)
-      compute<true>(a, make_part<true>(a, nr, nt, false), rt, tt, row_at + nr, rows, P.rows_bytes, red,
-                    ring, none);
-    compute<false>(a, make_part<false>(a, nr, nt, true), rt, tt, row_at, rows, P.rows_bytes, red, ring,
-                   wait);
-    if (a.Fs > 0)
-      compute<false>(a, make_part<false>(a, nr, nt, false), rt, tt, row_at + nr, rows, P.rows_bytes,
-                     red, ring, none);
+#pragma unroll 1
+    for (int shared = 0; shared < (a.Fs > 0 ? 2 : 1); ++shared)
+      compute<true>(a, make_part<true>(a, nr, nt, !shared), rt, tt, row_at + shared * nr, rows,
+                    P.rows_bytes, red, ring, nullptr);
+#pragma unroll 1
+    for (int shared = 0; shared < (a.Fs > 0 ? 2 : 1); ++shared)
+      compute<false>(a, make_part<false>(a, nr, nt, !shared), rt, tt, row_at + shared * nr, rows,
+                     P.rows_bytes, red, ring, shared ? nullptr : &flag);
     ok = grid_barrier<CTHREADS>(a.ctl, 2, &flag) && ok;
   }
   const long long R = (long long)T * k;
@@ -469,10 +471,10 @@ bool decode_mma_fits(const DecodeArgs& a) { return tile_tokens(a) > 0; }
 
 cudaError_t launch_decode_mma(const DecodeArgs& a, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  // a block per SM, or fewer where each would have less than 16 KB of weights
+  // a block per SM, or fewer where each would have less than 8 KB of weights
   const long long experts = (long long)a.T * a.k < a.E ? (long long)a.T * a.k : a.E;
   const long long bytes = (experts * a.F + a.Fs) * a.D * (a.act == 2 ? 3 : 2) * 2;
-  const long long blocks = (bytes + 16383) / 16384;
+  const long long blocks = (bytes + 8191) / 8192;
   return launch_cooperative(decode_mma_kernel, (int)(blocks < sms ? blocks : sms), THREADS,
                             attr_done, st, a, tile_tokens(a));
 }
