@@ -405,7 +405,7 @@ decode_mma_kernel(const __grid_constant__ DecodeArgs a, const int tt) {
     if (tid == 0) a.ctl[DC_STATUS] = DEV_STATUS_INVALID_INDEX;
     return;
   }
-  bool ok = grid_barrier<THREADS>(a.ctl, 0, &flag);
+  const bool ok = grid_barrier<THREADS>(a.ctl, 0, &flag);
   if (ok) select_all<WARPS>(a, rt, tt, scratch, &n_routed, &n_tiles);
   const int nr = ok ? n_routed : 0, nt = ok ? n_tiles : 0;
 
@@ -421,44 +421,49 @@ decode_mma_kernel(const __grid_constant__ DecodeArgs a, const int tt) {
     for (int shared = 0; shared < (a.Fs > 0 ? 2 : 1); ++shared)
       compute<false>(a, make_part<false>(a, nr, nt, !shared), rt, tt, row_at + shared * nr, rows,
                      P.rows_bytes, red, ring, shared ? nullptr : &flag);
-    ok = grid_barrier<CTHREADS>(a.ctl, 2, &flag) && ok;
+    grid_barrier<CTHREADS>(a.ctl, 2, &flag);
   }
-  const long long R = (long long)T * k;
-  if (ok && warp < CW) {
-    // y[t, d] = sum over j of gate (Y_e + b2), in j order, + the shared branch;
-    // eight assignments' reads at a time
-    for (int i = blockIdx.x * CTHREADS + tid; i < T * (D / 2); i += gridDim.x * CTHREADS) {
-      const int t = i / (D / 2), d = (i % (D / 2)) * 2;
-      float v0 = 0.f, v1 = 0.f;
-      for (int j0 = 0; j0 < k; j0 += 8) {
-        float2 h[8], b2[8];
+  __syncthreads();
+  if (flag == 0) {
+    // y[t, d] = sum over j of gate (Y_e + b2), + the shared branch: eight lanes
+    // take the assignments of four values of y, and a fixed tree adds them
+    const int quads = D / 4, j0 = tid & 7, terms = k + (a.Fs > 0 ? 1 : 0);
+    const int step = gridDim.x * (THREADS / 8);
+    for (int i0 = (blockIdx.x * THREADS + tid) / 8; i0 < T * quads; i0 += 2 * step) {
+      float4 v[2];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int s = j0 + u < k ? rt.slot[t * k + j0 + u] : -1;
-          h[u] = b2[u] = make_float2(0.f, 0.f);
-          if (s >= 0) {
-            h[u] = __ldcg(reinterpret_cast<const float2*>(a.ye + (long long)s * D + d));
-            if (a.b2 != nullptr)
-              b2[u] = *reinterpret_cast<const float2*>(
-                  a.b2 + (long long)rt.idx[t * k + j0 + u] * D + d);
+      for (int u = 0; u < 2; ++u) {
+        const int i = min(i0 + u * step, T * quads - 1), t = i / quads, d = (i % quads) * 4;
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int j = j0; j < terms; j += 8) {
+          const int s = j < k ? rt.slot[t * k + j] : T * k + t;
+          if (s < 0) continue;
+          float4 h = __ldcg(reinterpret_cast<const float4*>(a.ye + (long long)s * D + d));
+          if (a.b2 != nullptr) {           // (a layer with biases has no shared branch)
+            const float4 q = __ldg(reinterpret_cast<const float4*>(
+                a.b2 + (long long)rt.idx[t * k + j] * D + d));
+            h.x += q.x; h.y += q.y; h.z += q.z; h.w += q.w;
           }
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (j0 + u < k && rt.slot[t * k + j0 + u] >= 0) {
-            const float w = rt.gate[t * k + j0 + u];
-            v0 = fmaf(w, h[u].x + b2[u].x, v0);
-            v1 = fmaf(w, h[u].y + b2[u].y, v1);
-          }
+          const float w = j < k ? rt.gate[t * k + j] : 1.f;
+          v[u].x = fmaf(w, h.x, v[u].x); v[u].y = fmaf(w, h.y, v[u].y);
+          v[u].z = fmaf(w, h.z, v[u].z); v[u].w = fmaf(w, h.w, v[u].w);
         }
       }
-      if (a.Fs > 0) {
-        const float2 h = __ldcg(reinterpret_cast<const float2*>(a.ye + (R + t) * D + d));
-        v0 += h.x;
-        v1 += h.y;
+      // (the eight lanes of an output run through the loop together)
+      const uint32_t m8 = 0xffu << (tid & 24);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          v[u].x += __shfl_xor_sync(m8, v[u].x, o); v[u].y += __shfl_xor_sync(m8, v[u].y, o);
+          v[u].z += __shfl_xor_sync(m8, v[u].z, o); v[u].w += __shfl_xor_sync(m8, v[u].w, o);
+        }
+        const int i = i0 + u * step;
+        if (j0 == 0 && i < T * quads)
+          *reinterpret_cast<uint2*>(static_cast<bf16*>(a.y) + (long long)i * 4) =
+              make_uint2(pack_bf16(v[u].x, v[u].y), pack_bf16(v[u].z, v[u].w));
       }
-      reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.y) + (long long)t * D)[d / 2] =
-          pack_bf16(v0, v1);
     }
   }
   __syncthreads();
