@@ -44,8 +44,8 @@ class LayerNorm:
             raise ValueError(f"beta is on {beta.device}, gamma on {gamma.device}")
         self.gamma, self.beta, self.device = gamma, beta, gamma.device
         self.x_type, self.z_type, self.eps = _TORCH[x_dtype], _TORCH[z_dtype], float(eps)
-        self.workspace = None
-        self._cfg = {}
+        self.workspace = self.dgamma = self.dbeta = None
+        self._cfg, self._own = {}, {}
 
     def _config(self, T, delta):
         """The C configuration of T rows, its reference, and the backward
@@ -60,6 +60,14 @@ class LayerNorm:
                                     _TYPE[self.z_type], self.eps)
             c = self._cfg[key] = (cfg, ctypes.byref(cfg), B.moe_norm_workspace_size(cfg))
         return c
+
+    def _buffers(self, T, plain):
+        """Outputs of a call without statistics; one size at a time is kept."""
+        self._own.clear()
+        new = lambda dtype: torch.empty(T, self.D, dtype=dtype, device=self.device)  # noqa: E731
+        out = self._own[T, plain] = NormOut(None if plain else new(self.x_type), new(self.z_type),
+                                            None, None)
+        return out
 
     def _wrong(self, name, t, dtype, shape):
         """Raises for a tensor that is not contiguous `dtype` of `shape` on the
@@ -77,7 +85,10 @@ class LayerNorm:
     def forward(self, x, delta=None, stats=True, out=None, stream=None) -> NormOut:
         """h = x + delta (x itself without a delta), z = norm(h).  ``out``: a
         NormOut whose tensors are written instead of new ones; its h may be
-        ``x``.  stats=False leaves mean and rstd out (serving)."""
+        ``x``.  stats=False (serving) leaves mean and rstd out, and without
+        ``out`` writes h and z to buffers of this object, which its next such
+        call overwrites: allocating two tensors takes as long as launching the
+        kernel does."""
         shape = x.shape
         if len(shape) != 2 or shape[1] != self.D:
             raise ValueError(f"x must be [T, {self.D}], got {tuple(shape)}")
@@ -88,11 +99,13 @@ class LayerNorm:
                 raise ValueError(f"delta must be float32 or bfloat16, got {delta.dtype}")
             self._rows("delta", delta, delta.dtype, shape)
         if out is None:
-            out = NormOut(torch.empty_like(x) if delta is not None else None,
-                          torch.empty_like(x) if self.z_type is self.x_type else
-                          torch.empty_like(x, dtype=self.z_type),
-                          torch.empty(T, dtype=torch.float32, device=self.device) if stats else None,
-                          torch.empty(T, dtype=torch.float32, device=self.device) if stats else None)
+            if stats:
+                out = NormOut(torch.empty_like(x) if delta is not None else None,
+                              torch.empty_like(x, dtype=self.z_type),
+                              torch.empty(T, dtype=torch.float32, device=self.device),
+                              torch.empty(T, dtype=torch.float32, device=self.device))
+            else:
+                out = self._own.get((T, delta is None)) or self._buffers(T, delta is None)
         else:
             if (out.h is not None) != (delta is not None):
                 raise ValueError("out.h goes with a delta")
@@ -112,7 +125,10 @@ class LayerNorm:
     def backward(self, dz, h, mean, rstd, dres=None, out=None, stream=None) -> NormGrads:
         """Gradients at the stream h that ``forward`` normalised (its h, or its
         x without a delta); dres: the gradient reaching h past the norm.
-        ``out``: a NormGrads to write; its dx may be ``dz`` or ``dres``."""
+        ``out``: a NormGrads to write; its dx may be ``dz`` or ``dres``.  Without
+        it dx is new, and the parameters' gradients are written to ``dgamma``
+        and ``dbeta`` of this object (overwritten, never added to, as a layer's
+        own gradient buffers are)."""
         shape = h.shape
         if len(shape) != 2 or shape[1] != self.D:
             raise ValueError(f"h must be [T, {self.D}], got {tuple(shape)}")
@@ -124,8 +140,10 @@ class LayerNorm:
         if dres is not None:
             self._rows("dres", dres, torch.float32, shape)
         if out is None:
-            out = NormGrads(torch.empty_like(dz), torch.empty_like(self.gamma),
-                            None if self.beta is None else torch.empty_like(self.beta))
+            if self.dgamma is None:
+                self.dgamma = torch.empty_like(self.gamma)
+                self.dbeta = None if self.beta is None else torch.empty_like(self.beta)
+            out = NormGrads(torch.empty_like(dz), self.dgamma, self.dbeta)
         else:
             self._rows("out.dx", out.dx, torch.float32, shape)
             self._rows("out.dgamma", out.dgamma, torch.float32, (self.D,))

@@ -93,6 +93,23 @@ def test_forward_without_stats_and_shift():
     _check_forward(n, h, full, "f32", gamma, None)
 
 
+def test_forward_serving_buffers():
+    """Without statistics and ``out`` the outputs are the norm's own buffers; a
+    stream that is one of them is updated in place; sizes may alternate."""
+    gamma, beta = _params(96)
+    n = LayerNorm(gamma, beta, "bf16", "bf16")
+    for T in (3, 1, 3):
+        x, d = _stream(T, 96, "bf16", seed=T), _stream(T, 96, "bf16", seed=T + 7)
+        want = n.forward(x, d)
+        r = n.forward(x, d, stats=False)
+        assert torch.equal(r.h, want.h) and torch.equal(r.z, want.z)
+        nxt = n.forward(want.h, d)
+        again = n.forward(r.h, d, stats=False)
+        assert again.h is r.h and torch.equal(again.h, nxt.h) and torch.equal(again.z, nxt.z)
+        alone = n.forward(x, stats=False)
+        assert alone.h is None and torch.equal(alone.z, n.forward(x).z)
+
+
 def test_forward_in_place_stream():
     gamma, beta = _params(136)
     x, d = _stream(11, 136, "f32"), _stream(11, 136, "f32", seed=9)
@@ -172,9 +189,10 @@ def _check_backward(n, h, f, dz, dres, out):
                                  (3, 8191), (200, 8200), (2, 16384)])
 def test_backward(T, D, x):
     n, h, f, dz, dres = _backward_case(T, D, x)
-    out = n.backward(dz, h, f.mean, f.rstd, dres=dres)
+    out = NormGrads(*[t.clone() for t in n.backward(dz, h, f.mean, f.rstd, dres=dres)])
     _check_backward(n, h, f, dz, dres, out)
     again = n.backward(dz, h, f.mean, f.rstd, dres=dres)
+    assert again.dgamma is n.dgamma and again.dbeta is n.dbeta
     for a, b in zip(out, again):
         assert torch.equal(a, b)        # fixed-order sums: the same bits
 
