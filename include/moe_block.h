@@ -73,8 +73,12 @@ MOE_API moe_status moe_norm_backward(const moe_norm_config* cfg, const void* h, 
  * a weight.  MOE_BF16 layers route with a bf16 copy of w_gate's values, as
  * moe_forward does; products are summed in fp32, hidden activations stay fp32,
  * and y is rounded once.  idx [T,k] (int32) and gate [T,k] (fp32) receive the
- * routing, or are NULL.  T <= MOE_DECODE_MAX_TOKENS, D <= 2^20, F <= 2^19
- * (MOE_ERR_UNSUPPORTED beyond).  aux_alpha is not read.
+ * routing, or are NULL.  T <= MOE_DECODE_MAX_TOKENS, a token of x at most
+ * MOE_DECODE_MAX_ROW_BYTES, F and n_shared F <= MOE_DECODE_MAX_F
+ * (MOE_ERR_UNSUPPORTED beyond).  aux_alpha is not
+ * read.  The order of a token's sums goes with the call's split of the work:
+ * calls with the same tokens give the same bits, a token among other tokens may
+ * differ in the last bits before the rounding.
  *
  * The workspace holds the counters of the kernel's grid barriers: call
  * moe_decode_init once before its first use (and after a status other than
@@ -82,6 +86,8 @@ MOE_API moe_status moe_norm_backward(const moe_norm_config* cfg, const void* h, 
  * was made for (the size grows with T).  Calls that share a workspace must not
  * overlap on the GPU.  A call captures into a CUDA graph. */
 #define MOE_DECODE_MAX_TOKENS 64
+#define MOE_DECODE_MAX_ROW_BYTES 32768
+#define MOE_DECODE_MAX_F 8192
 MOE_API size_t moe_decode_workspace_size(const moe_config* cfg);
 MOE_API moe_status moe_decode_init(const moe_config* cfg, void* workspace, size_t workspace_bytes,
                                    void* stream);

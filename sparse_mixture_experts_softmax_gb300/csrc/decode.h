@@ -28,15 +28,11 @@ struct DecodeArgs {
   float* logits;               // [T, E]
   float* hidden;               // [T k, F], expert-major slots
   float* hidden_s;             // [T, Fs]
-  float* ye;                   // [T k + (Fs ? T : 0), D], decode_mma.cu only
+  float* ye;                   // [T k + (Fs ? T : 0), D]
 };
 
 // Writes the control words of a workspace that no call has used yet.
 cudaError_t launch_decode_init(int* ctl, cudaStream_t st);
 cudaError_t launch_decode(int dtype, const DecodeArgs& a, cudaStream_t st);
-// bf16 layers on the tensor cores, sms blocks at most.
-cudaError_t launch_decode_mma(const DecodeArgs& a, int sms, cudaStream_t st);
-// Whether the token tiles of such a layer fit the tensor-core kernel's shared memory.
-bool decode_mma_fits(const DecodeArgs& a);
 
 }  // namespace moe

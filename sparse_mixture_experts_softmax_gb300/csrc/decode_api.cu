@@ -15,8 +15,11 @@ namespace {
 moe_status check_decode(const moe_config* cfg) {
   RET_IF(validate_config(cfg));
   const moe_config& c = *cfg;
-  // offsets of activation rows are 32-bit inside the kernel
-  if (c.T > MOE_DECODE_MAX_TOKENS || c.D > (1 << 20) || c.F > (1 << 19)) return MOE_ERR_UNSUPPORTED;
+  // one token's row of the widest operand has to fit the kernel's shared memory
+  if (c.T > MOE_DECODE_MAX_TOKENS ||
+      (long long)c.D * (long long)esize(c.dtype) > MOE_DECODE_MAX_ROW_BYTES || c.F > MOE_DECODE_MAX_F ||
+      (long long)c.n_shared * c.F > MOE_DECODE_MAX_F)
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -33,8 +36,8 @@ DecodeLayout decode_layout(const moe_config& c) {
   o += align_up(R * c.F * 4);
   L.hidden_s = o;
   o += align_up(T * Fs * 4);
-  L.ye = o;      // (for every T: the size must not shrink as T grows)
-  if (c.dtype == MOE_BF16) o += align_up((R + (Fs ? T : 0)) * c.D * 4);
+  L.ye = o;
+  o += align_up((R + (Fs ? T : 0)) * c.D * 4);
   L.total = o;
   return L;
 }

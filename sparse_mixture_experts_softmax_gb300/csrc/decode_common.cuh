@@ -30,23 +30,6 @@ __device__ __forceinline__ unsigned long long now_ns() {
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
-  const unsigned long long t0 = now_ns();
-  while (!mbar_try(bar, parity))
-    if (now_ns() - t0 > WAIT_NS) return false;
-  return true;
-}
-
 // One of the kernel's grid barriers.  Each has a counter of its own, zero on
 // entry; the last block to leave the kernel zeroes them for the next call.
 // Returns false when the wait expired (uniform over the block).
@@ -81,26 +64,6 @@ __device__ __forceinline__ bool grid_barrier(int* ctl, int which, int* flag) {
   bar_sync<NTHREADS>();
   return *flag == 0;
 }
-
-// ---- arithmetic on pairs of fp32 values (one instruction for two lanes of a dot product)
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(uint32_t lo, uint32_t hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ float sum2(f32x2 v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return __uint_as_float(lo) + __uint_as_float(hi);
-}
-__device__ __forceinline__ f32x2 widen(uint32_t two_bf16) {
-  return pack2(two_bf16 << 16, two_bf16 & 0xffff0000u);
-}
-
 
 // Sums 32 values over the warp at once: lane l gets the whole sum of v[l].
 // (31 exchanges; one at a time they would take 160.)

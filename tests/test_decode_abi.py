@@ -41,7 +41,9 @@ def _call(L, c, w=None, x=A, y=A, idx=A, gate=A, ws=A, nbytes=1 << 40):
 
 
 @pytest.mark.parametrize("kw", [dict(T=65), dict(T=1 << 20), dict(D=(1 << 20) + 8),
-                                dict(F=(1 << 19) + 8), dict(k=9), dict(D=60), dict(E=12)])
+                                dict(F=(1 << 19) + 8), dict(k=9), dict(D=60), dict(E=12),
+                                dict(D=16392), dict(F=8200), dict(F=4104, n_shared=2),
+                                dict(D=8200, act="relu", dtype="f32")])
 def test_unsupported(L, kw):
     c = _cfg(**kw)
     assert B.moe_decode_workspace_size(c) == 0

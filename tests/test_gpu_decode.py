@@ -119,6 +119,11 @@ def test_decode(name, T):
          score="sigmoid"),
     dict(T=1, D=8, F=2048, E=8), dict(T=1, D=8192, F=8, E=8),
     dict(T=3, D=16384, F=24, E=8, n_shared=1),
+    # the widest rows the kernel takes, beside the longest lists
+    dict(T=64, D=16384, F=16, E=256, k=32), dict(T=64, D=16, F=8192, E=16, k=16),
+    dict(T=9, D=16, F=4096, E=8, n_shared=2),
+    dict(T=33, D=8192, F=16, E=8, k=3, dtype="f32"), dict(T=5, D=16, F=8192, E=8, dtype="f32"),
+    dict(T=64, D=7168, F=256, E=8, k=2),                # tiles of an odd number of tokens
 ], ids=lambda kw: "_".join(f"{k}{v}" for k, v in kw.items()))
 def test_decode_extremes(kw):
     wl = _wl(**kw)
