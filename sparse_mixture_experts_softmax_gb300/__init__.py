@@ -3,8 +3,8 @@
 The layer lives in the CUDA library ``libmoe_gb300.so`` behind the C ABI of
 ``include/moe.h``; ``binding`` is its thin ctypes binding and ``layer`` a small
 helper that owns the device buffers of one layer.  ``norm`` is the layer norm of
-the residual block around it and ``decode`` the layer for a few tokens
-(``include/moe_block.h``).
+the residual block around it, ``decode`` the layer for a few tokens
+(``include/moe_block.h``) and ``block`` the three together.
 """
 
 from .binding import (MoEError, make_config, make_grads, make_norm_config,  # noqa: F401

@@ -237,7 +237,7 @@ __device__ __forceinline__ void emit(const DecodeArgs& a, const Tile& tl, int bl
       if (f >= width) break;
       float v = h ? v1 : v0;
       if (a.b1 != nullptr) v += a.b1[(long long)tl.e * a.F + f];
-      __stcg(o + f, a.act == 1 ? gelu_tanh_f(v) : fmaxf(v, 0.f));
+      __stcg(o + f, a.act == 1 ? gelu_tanh_f(v) : (v < 0.f ? 0.f : v));     // a NaN stays one
     }
   } else {
     const long long row = (tl.e >= 0 ? 0 : (long long)a.T * a.k) + tl.start + tok;

@@ -20,7 +20,9 @@ class MoEDecoder:
     """w_gate [E,D] fp32; w1, w3 [E,F,D], w2 [E,D,F] and the shared branch ws1,
     ws3, ws2 in the layer's type (float32 or bfloat16); b1 [E,F], b2 [E,D],
     logit_bias [E], corr_bias [E] fp32 or None.  The tensors are used in place,
-    so the decoder follows a layer that is still being trained."""
+    so the decoder follows a layer that is still being trained.  Calls run on the
+    current stream; those of one decoder share its buffers and must not overlap
+    on the GPU."""
 
     def __init__(self, w_gate, w1, w2, w3=None, b1=None, b2=None, k=1, act="relu",
                  score="softmax", n_groups=1, topk_groups=1, group_score="top2_sum",
@@ -86,7 +88,7 @@ class MoEDecoder:
                               self.workspace.data_ptr(), self.workspace.numel())
         return c
 
-    def decode(self, x, y=None, stream=None):
+    def decode(self, x, y=None):
         """y [T, D] of the tokens x [T, D] (the layer's type, 0 <= T <=
         max_tokens).  Without ``y`` the result is written to a buffer of the
         decoder, which the next call overwrites; ``idx`` and ``gate`` [T, k]
@@ -109,17 +111,17 @@ class MoEDecoder:
                                  f"{self.device}")
             yp = y.data_ptr()
         status = B.lib().moe_decode(c[1], self._weights_ref, x.data_ptr(), yp, c[6], c[7], c[8],
-                                    c[9], B._stream_on(stream, self.device))
+                                    c[9], B._stream_on(None, self.device))
         if status != B.MOE_OK:
             B._check("moe_decode", status)
         self.idx, self.gate = c[3], c[4]
         return y
 
-    def status(self, stream=None) -> int:
+    def status(self) -> int:
         """Device status since the last reset (0, or a MOE_ERR_* code; see
-        moe_decode_status).  Waits for the stream."""
-        return B.moe_decode_status(self.cfg, self.workspace, B._stream_on(stream, self.device))
+        moe_decode_status).  Waits for the current stream."""
+        return B.moe_decode_status(self.cfg, self.workspace, B._stream_on(None, self.device))
 
-    def reset(self, stream=None):
+    def reset(self):
         """Makes the workspace ready again after a status other than 0."""
-        B.moe_decode_init(self.cfg, self.workspace, B._stream_on(stream, self.device))
+        B.moe_decode_init(self.cfg, self.workspace, B._stream_on(None, self.device))

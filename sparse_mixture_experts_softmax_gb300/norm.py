@@ -33,39 +33,50 @@ class NormGrads(NamedTuple):
 
 class LayerNorm:
     """gamma, beta (or None): fp32 [D] on the GPU, used in place.  x_dtype is
-    the residual stream's type, z_dtype the following layer's input type."""
+    the residual stream's type, z_dtype the following layer's input type.  Calls
+    run on the current stream; those of one object share its buffers, so they
+    must not overlap on the GPU (several streams: order them, or give ``out`` and
+    use an object each)."""
 
     def __init__(self, gamma, beta=None, x_dtype="f32", z_dtype="f32", eps=1e-5):
         self.D = int(gamma.numel())
         for name, p in (("gamma", gamma), ("beta", beta)):
-            if p is not None and (p.dtype != torch.float32 or tuple(p.shape) != (self.D,)):
-                raise ValueError(f"{name} must be float32 of shape [{self.D}]")
+            if p is not None and (p.dtype != torch.float32 or tuple(p.shape) != (self.D,) or
+                                  not p.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous float32 of shape [{self.D}]")
         if beta is not None and beta.device != gamma.device:
             raise ValueError(f"beta is on {beta.device}, gamma on {gamma.device}")
         self.gamma, self.beta, self.device = gamma, beta, gamma.device
         self.x_type, self.z_type, self.eps = _TORCH[x_dtype], _TORCH[z_dtype], float(eps)
         self.workspace = self.dgamma = self.dbeta = None
-        self._cfg, self._own = {}, {}
+        self._plans, self._own = {}, {}
+        self._gamma_ptr = gamma.data_ptr()
+        self._beta_ptr = None if beta is None else beta.data_ptr()
 
-    def _config(self, T, delta):
-        """The C configuration of T rows, its reference, and the backward
-        pass's workspace size (the last configurations are kept: a decoding
-        program passes the same T over and over)."""
-        key = (T, delta)
-        c = self._cfg.get(key)
-        if c is None:
-            if len(self._cfg) >= 256:
-                self._cfg.clear()
-            cfg = B.moe_norm_config(T, self.D, _TYPE[self.x_type], _TYPE[delta],
-                                    _TYPE[self.z_type], self.eps)
-            c = self._cfg[key] = (cfg, ctypes.byref(cfg), B.moe_norm_workspace_size(cfg))
-        return c
+    def _plan(self, shape, delta):
+        """What a call on rows of `shape` passes besides its tensors: the C
+        configuration, its reference, the backward pass's workspace size, and a
+        tensor like its statistics.  The last ones are kept: a program passes
+        the same shapes over and over, and a call costs as much host time as a
+        small kernel runs."""
+        if len(shape) != 2 or shape[1] != self.D:
+            raise ValueError(f"the rows must be [T, {self.D}], got {tuple(shape)}")
+        if delta is not None and delta not in _TYPE:
+            raise ValueError(f"delta must be float32 or bfloat16, got {delta}")
+        if len(self._plans) >= 64:
+            self._plans.clear()
+        cfg = B.moe_norm_config(shape[0], self.D, _TYPE[self.x_type], _TYPE[delta or torch.float32],
+                                _TYPE[self.z_type], self.eps)
+        p = self._plans[shape, delta] = (
+            cfg, ctypes.byref(cfg), B.moe_norm_workspace_size(cfg),
+            torch.empty(shape[0], dtype=torch.float32, device=self.device))
+        return p
 
-    def _buffers(self, T, plain):
+    def _buffers(self, shape, plain):
         """Outputs of a call without statistics; one size at a time is kept."""
         self._own.clear()
-        new = lambda dtype: torch.empty(T, self.D, dtype=dtype, device=self.device)  # noqa: E731
-        out = self._own[T, plain] = NormOut(None if plain else new(self.x_type), new(self.z_type),
+        new = lambda dtype: torch.empty(shape, dtype=dtype, device=self.device)  # noqa: E731
+        out = self._own[shape, plain] = NormOut(None if plain else new(self.x_type), new(self.z_type),
                                             None, None)
         return out
 
@@ -78,11 +89,11 @@ class LayerNorm:
                          f"{t.dtype} {tuple(t.shape)}")
 
     def _rows(self, name, t, dtype, shape):
-        if (t.dtype != dtype or t.shape != shape or t.device != self.device or
+        if (t.dtype is not dtype or t.shape != shape or t.device != self.device or
                 not t.is_contiguous()):
             self._wrong(name, t, dtype, shape)
 
-    def forward(self, x, delta=None, stats=True, out=None, stream=None) -> NormOut:
+    def forward(self, x, delta=None, stats=True, out=None) -> NormOut:
         """h = x + delta (x itself without a delta), z = norm(h).  ``out``: a
         NormOut whose tensors are written instead of new ones; its h may be
         ``x``.  stats=False (serving) leaves mean and rstd out, and without
@@ -90,23 +101,15 @@ class LayerNorm:
         call overwrites: allocating two tensors takes as long as launching the
         kernel does."""
         shape = x.shape
-        if len(shape) != 2 or shape[1] != self.D:
-            raise ValueError(f"x must be [T, {self.D}], got {tuple(shape)}")
-        T = shape[0]
-        self._rows("x", x, self.x_type, shape)
-        if delta is not None:
-            if delta.dtype not in _TYPE:
-                raise ValueError(f"delta must be float32 or bfloat16, got {delta.dtype}")
-            self._rows("delta", delta, delta.dtype, shape)
-        if out is None:
-            if stats:
-                out = NormOut(torch.empty_like(x) if delta is not None else None,
-                              torch.empty_like(x, dtype=self.z_type),
-                              torch.empty(T, dtype=torch.float32, device=self.device),
-                              torch.empty(T, dtype=torch.float32, device=self.device))
-            else:
-                out = self._own.get((T, delta is None)) or self._buffers(T, delta is None)
-        else:
+        kind = None if delta is None else delta.dtype
+        plan = self._plans.get((shape, kind)) or self._plan(shape, kind)
+        if x.dtype is not self.x_type or x.device != self.device or not x.is_contiguous():
+            self._wrong("x", x, self.x_type, shape)
+        if delta is not None and (delta.shape != shape or delta.device != self.device or
+                                  not delta.is_contiguous()):
+            self._wrong("delta", delta, kind, shape)
+        if out is not None:
+            T = shape[0]
             if (out.h is not None) != (delta is not None):
                 raise ValueError("out.h goes with a delta")
             if out.h is not None:
@@ -115,14 +118,24 @@ class LayerNorm:
             for name, t in (("out.mean", out.mean), ("out.rstd", out.rstd)):
                 if t is not None:
                     self._rows(name, t, torch.float32, (T,))
-        cfg = self._config(T, delta.dtype if delta is not None else torch.float32)
-        B._check("moe_norm_forward", B.lib().moe_norm_forward(
-            cfg[1], x.data_ptr(), None if delta is None else delta.data_ptr(),
-            self.gamma.data_ptr(), B._ptr(self.beta), None if delta is None else out.h.data_ptr(),
-            out.z.data_ptr(), B._ptr(out.mean), B._ptr(out.rstd), B._stream_on(stream, self.device)))
+        elif stats:
+            like = torch.empty_like
+            out = NormOut(None if delta is None else like(x),
+                          like(x) if self.z_type is self.x_type else like(x, dtype=self.z_type),
+                          like(plan[3]), like(plan[3]))
+        else:
+            out = self._own.get((shape, delta is None)) or self._buffers(shape, delta is None)
+        h, z, mean, rstd = out
+        status = B.lib().moe_norm_forward(
+            plan[1], x.data_ptr(), None if delta is None else delta.data_ptr(), self._gamma_ptr,
+            self._beta_ptr, None if h is None else h.data_ptr(), z.data_ptr(),
+            None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
+            B._stream_on(None, self.device))
+        if status != B.MOE_OK:
+            B._check("moe_norm_forward", status)
         return out
 
-    def backward(self, dz, h, mean, rstd, dres=None, out=None, stream=None) -> NormGrads:
+    def backward(self, dz, h, mean, rstd, dres=None, out=None) -> NormGrads:
         """Gradients at the stream h that ``forward`` normalised (its h, or its
         x without a delta); dres: the gradient reaching h past the norm.
         ``out``: a NormGrads to write; its dx may be ``dz`` or ``dres``.  Without
@@ -130,31 +143,31 @@ class LayerNorm:
         and ``dbeta`` of this object (overwritten, never added to, as a layer's
         own gradient buffers are)."""
         shape = h.shape
-        if len(shape) != 2 or shape[1] != self.D:
-            raise ValueError(f"h must be [T, {self.D}], got {tuple(shape)}")
-        T = shape[0]
+        plan = self._plans.get((shape, None)) or self._plan(shape, None)
+        T, f32 = shape[0], torch.float32
         self._rows("h", h, self.x_type, shape)
-        self._rows("dz", dz, torch.float32, shape)
-        self._rows("mean", mean, torch.float32, (T,))
-        self._rows("rstd", rstd, torch.float32, (T,))
+        self._rows("dz", dz, f32, shape)
+        self._rows("mean", mean, f32, (T,))
+        self._rows("rstd", rstd, f32, (T,))
         if dres is not None:
-            self._rows("dres", dres, torch.float32, shape)
+            self._rows("dres", dres, f32, shape)
         if out is None:
             if self.dgamma is None:
                 self.dgamma = torch.empty_like(self.gamma)
                 self.dbeta = None if self.beta is None else torch.empty_like(self.beta)
             out = NormGrads(torch.empty_like(dz), self.dgamma, self.dbeta)
         else:
-            self._rows("out.dx", out.dx, torch.float32, shape)
-            self._rows("out.dgamma", out.dgamma, torch.float32, (self.D,))
+            self._rows("out.dx", out.dx, f32, shape)
+            self._rows("out.dgamma", out.dgamma, f32, (self.D,))
             if out.dbeta is not None:
-                self._rows("out.dbeta", out.dbeta, torch.float32, (self.D,))
-        cfg = self._config(T, torch.float32)
-        if self.workspace is None or self.workspace.numel() < cfg[2]:
-            self.workspace = torch.empty(cfg[2], dtype=torch.uint8, device=h.device)
-        B._check("moe_norm_backward", B.lib().moe_norm_backward(
-            cfg[1], h.data_ptr(), dz.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            self.gamma.data_ptr(), B._ptr(dres), out.dx.data_ptr(), out.dgamma.data_ptr(),
-            B._ptr(out.dbeta), self.workspace.data_ptr(), self.workspace.numel(),
-            B._stream_on(stream, self.device)))
+                self._rows("out.dbeta", out.dbeta, f32, (self.D,))
+        if self.workspace is None or self.workspace.numel() < plan[2]:
+            self.workspace = torch.empty(plan[2], dtype=torch.uint8, device=self.device)
+        status = B.lib().moe_norm_backward(
+            plan[1], h.data_ptr(), dz.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+            self._gamma_ptr, None if dres is None else dres.data_ptr(), out.dx.data_ptr(),
+            out.dgamma.data_ptr(), None if out.dbeta is None else out.dbeta.data_ptr(),
+            self.workspace.data_ptr(), self.workspace.numel(), B._stream_on(None, self.device))
+        if status != B.MOE_OK:
+            B._check("moe_norm_backward", status)
         return out

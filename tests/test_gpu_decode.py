@@ -198,6 +198,24 @@ def test_decode_a_bad_token_stays_alone():
     assert d.status() == 0
 
 
+@pytest.mark.parametrize("act,dtype", [("relu", "f32"), ("relu", "bf16"), ("gelu_tanh", "f32")])
+def test_decode_a_nan_passes_the_activation(act, dtype):
+    """A NaN hidden value reaches y (ReLU does not turn it into a zero), in the
+    tokens of its expert only."""
+    wl = _wl(T=12, D=64, F=32, E=8, k=1, act=act, dtype=dtype, has_bias=True)
+    inp = _inputs(wl, seed=12)
+    d = _decoder(wl, inp)
+    x = device_x(wl, inp)
+    clean = d.decode(x).clone()
+    e = int(d.idx[0, 0])
+    inp["b1"][e, 5] = float("nan")
+    d = _decoder(wl, inp)
+    y = d.decode(x)
+    hit = d.idx[:, 0] == e
+    assert torch.isnan(y[hit]).all()
+    assert torch.equal(y[~hit], clean[~hit])
+
+
 def test_decode_token_counts_share_a_decoder():
     wl = _wl(T=64, D=328, F=72, E=16, k=3, n_shared=1)
     inp = _inputs(wl, seed=8)
