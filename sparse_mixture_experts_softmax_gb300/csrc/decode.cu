@@ -219,10 +219,11 @@ __device__ __forceinline__ uint4 load_rows(uint32_t at) {
   return v;
 }
 
-// One output pair of an item: rows r and r + 8 of the 16, token `tok` of the tile.
+// One output pair of an item: rows r and r + 8 of the 16, token `tok` of the
+// tile; b0, b1: the rows' biases (up projections of layers that have them).
 template <bool UP>
 __device__ __forceinline__ void emit(const DecodeArgs& a, const Tile& tl, int block, int r, int tok,
-                                     float v0, float v1) {
+                                     float v0, float v1, float b0, float b1) {
   if (tok >= tl.n) return;
   if constexpr (UP) {
     const int width = tl.e >= 0 ? a.F : a.Fs;
@@ -235,8 +236,7 @@ __device__ __forceinline__ void emit(const DecodeArgs& a, const Tile& tl, int bl
     for (int h = 0; h < 2; ++h) {
       const int f = block * 16 + h * 8 + r;
       if (f >= width) break;
-      float v = h ? v1 : v0;
-      if (a.b1 != nullptr) v += a.b1[(long long)tl.e * a.F + f];
+      const float v = h ? v1 + b1 : v0 + b0;
       __stcg(o + f, a.act == 1 ? gelu_tanh_f(v) : (v < 0.f ? 0.f : v));     // a NaN stays one
     }
   } else {
@@ -487,6 +487,10 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
       const Tile tl = rt.tiles[p.t0 + it];
       Products<WT, UP> sum;
       sum.begin(rows + row_at[it], pitch, tl.n, lane);
+      // the biases of the item's rows, one a lane, on their way from here on
+      float bias = 0.f;
+      if (UP && a.b1 != nullptr && lane < 16 && ib * 16 + lane < p.width)
+        bias = __ldg(a.b1 + (long long)tl.e * a.F + ib * 16 + lane);
       for (int s = 0; s < steps; ++s) {
         asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
         __syncwarp();
@@ -496,8 +500,10 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
         put();
         slot = slot + 1 == NS ? 0 : slot + 1;
       }
-      auto out = [&](int row, int tok, float v0, float v1) {
-        emit<UP>(a, tl, ib, row, tok, v0, v1);
+      auto out = [&](int row, int tok, float v0, float v1) {       // by whole warps
+        const float b0 = UP ? __shfl_sync(0xffffffffu, bias, row) : 0.f;
+        const float b1 = UP ? __shfl_sync(0xffffffffu, bias, row + 8) : 0.f;
+        emit<UP>(a, tl, ib, row, tok, v0, v1, b0, b1);
       };
       if (KS == 1) {
         sum.each(lane, out);

@@ -259,7 +259,8 @@ __device__ __noinline__ void select_token(const DecodeArgs& a, int t, float* row
   if (lane < k) {
     idx[t * k + lane] = (short)pick;
     gate[t * k + lane] = mine / sum;
-    atomicOr(mask + 2 * pick + (t >> 5), 1u << (t & 31));   // whole numbers: any order
+    if (mask != nullptr)
+      atomicOr(mask + 2 * pick + (t >> 5), 1u << (t & 31));   // whole numbers: any order
   }
   __syncwarp();
 }
@@ -290,6 +291,31 @@ __device__ __forceinline__ void select_all(const DecodeArgs& a, const Routing& r
   uint32_t* mask = reinterpret_cast<uint32_t*>(scratch);      // [256][2]
   int* base_of = reinterpret_cast<int*>(scratch) + 512;       // [256]
   float* row = scratch + 768 + warp * E;
+  if (T == 1) {
+    // one token: its picks are the lists (an expert keeps at least one row), and
+    // the two barriers and the scans below would cost as much as the picking
+    if (warp == 0) {
+      if (E <= 64) select_token<2>(a, 0, row, r.idx, r.gate, nullptr, lane);
+      else if (E <= 128) select_token<4>(a, 0, row, r.idx, r.gate, nullptr, lane);
+      else select_token<8>(a, 0, row, r.idx, r.gate, nullptr, lane);
+      if (lane < k) {
+        r.tiles[lane] = Tile{r.idx[lane], 1, lane};
+        r.tok[lane] = 0;
+        r.slot[lane] = (short)lane;
+        if (blockIdx.x == 0) {
+          if (a.idx != nullptr) a.idx[lane] = r.idx[lane];
+          if (a.gate != nullptr) a.gate[lane] = r.gate[lane];
+        }
+      }
+      if (lane == 0) {
+        *n_routed = k;
+        *n_tiles = k + (a.Fs > 0 ? 1 : 0);
+        if (a.Fs > 0) r.tiles[k] = Tile{(short)-1, 1, 0};
+      }
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = tid; i < 512; i += NW * 32) mask[i] = 0u;
   __syncthreads();
   for (int t = warp; t < T; t += NW) {
