@@ -30,22 +30,24 @@ __device__ __forceinline__ unsigned long long now_ns() {
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-// One of the kernel's grid barriers.  Each has a counter of its own, zero on
-// entry; the last block to leave the kernel zeroes them for the next call.
-// Returns false when the wait expired (uniform over the block).
-// The first NTHREADS threads of the block take part.
+// A barrier of the block's first NTHREADS threads.
 template <int NTHREADS>
 __device__ __forceinline__ void bar_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(NTHREADS) : "memory");
 }
+// One of the kernel's grid barriers, for the first NTHREADS threads of every
+// block.  Each has a counter of its own, zero on entry; the last block to leave
+// the kernel zeroes them for the next call.  Returns false when the wait expired
+// (uniform over those threads).
 template <int NTHREADS>
 __device__ __forceinline__ bool grid_barrier(int* ctl, int which, int* flag) {
   bar_sync<NTHREADS>();
   if (gridDim.x == 1) return *flag == 0;
   if (threadIdx.x == 0) {
     int* bar = ctl + DC_BAR + which;
-    __threadfence();
-    atomicAdd(bar, 1);
+    // release and acquire on the counter order the block's accesses (the block's
+    // barrier carries them to and from this thread); a full fence costs more
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(bar) : "memory");
     int seen = 0;
     unsigned long long t0 = 0;
     while (true) {
@@ -59,7 +61,6 @@ __device__ __forceinline__ bool grid_barrier(int* ctl, int which, int* flag) {
         break;
       }
     }
-    __threadfence();
   }
   bar_sync<NTHREADS>();
   return *flag == 0;
