@@ -116,11 +116,14 @@ struct Part {
   int t0;                      // first tile
   int lo, hi;                  // items, counted from the first tile
 };
-// First item of block b's share: the blocks' shares are of equal weight bytes.
-__device__ __forceinline__ int share_of(int all_r, int K_r, int all_s, int K_s, int b) {
-  const long long bytes_r = (long long)all_r * K_r;
-  const long long at = (bytes_r + (long long)all_s * K_s) * b / (int)gridDim.x;
-  return at < bytes_r ? (int)(at / K_r) : all_r + (all_s > 0 ? (int)((at - bytes_r) / K_s) : 0);
+// First item of block b's share: the blocks' shares are of equal weight bytes, a
+// shared item counting `weight` routed ones.  One 32-bit division: the whole
+// block waits for it.
+__device__ __forceinline__ int share_of(int all_r, int all_s, int weight, int b) {
+  const int units = all_r + all_s * weight, q = units / (int)gridDim.x;
+  const int at = q * b + min(b, units - q * (int)gridDim.x);
+  if (at <= all_r) return at;
+  return all_r + (weight == 1 ? at - all_r : (at - all_r) / weight);
 }
 template <typename WT, bool UP>
 __device__ __forceinline__ Part make_part(const DecodeArgs& a, int n_routed, int n_tiles, bool routed) {
@@ -131,8 +134,9 @@ __device__ __forceinline__ Part make_part(const DecodeArgs& a, int n_routed, int
   const int per_r = (width_r + p.rows - 1) / p.rows, per_s = (width_s + p.rows - 1) / p.rows;
   const int K_r = UP ? a.D : a.F, K_s = UP ? a.D : a.Fs;
   const int all_r = n_routed * per_r, all_s = (n_tiles - n_routed) * per_s;
-  const int lo = share_of(all_r, K_r, all_s, K_s, blockIdx.x);
-  const int hi = share_of(all_r, K_r, all_s, K_s, blockIdx.x + 1);
+  const int weight = UP || a.Fs == 0 ? 1 : a.n_shared;         // Fs = n_shared F
+  const int lo = share_of(all_r, all_s, weight, blockIdx.x);
+  const int hi = share_of(all_r, all_s, weight, blockIdx.x + 1);
   p.K = routed ? K_r : K_s;
   p.width = routed ? width_r : width_s;
   p.per = routed ? per_r : per_s;
@@ -396,12 +400,15 @@ template <bool UP> struct Products<float, UP> {
 // block's share, an item shared by several warps counting one more for adding
 // their parts.
 __device__ __forceinline__ int warps_per_item(int items, int stages) {
+  static_assert(CW == 8, "three halvings");
   int best = 1, cost = 0x7fffffff;
-  for (int ks = 1; ks <= CW; ks *= 2) {
-    const int c = (items + CW / ks - 1) / (CW / ks) * ((stages + ks - 1) / ks * 4 + (ks > 1 ? 1 : 0));
+#pragma unroll 1
+  for (int l = 0; l <= 3; ++l) {
+    const int c = ((items + (CW >> l) - 1) >> (3 - l)) *
+                  (((stages + (1 << l) - 1) >> l) * 4 + (l > 0 ? 1 : 0));
     if (c < cost) {
       cost = c;
-      best = ks;
+      best = 1 << l;
     }
   }
   return best;
@@ -421,13 +428,15 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
   constexpr int ES = (int)sizeof(WT), SV = PIECE / ES;         // values of a row in a stage
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int K = p.K, stages = (K + SV - 1) / SV;
-  const int KS = warps_per_item(p.hi - p.lo, stages), groups = CW / KS;
-  const int mine = warp / KS, ks = warp % KS, steps = (stages + KS - 1) / KS;
+  const int KS = warps_per_item(p.hi - p.lo, stages), groups = CW >> (__ffs(KS) - 1);
+  const int lg = __ffs(KS) - 1, mine = warp >> lg, ks = warp & (KS - 1);
+  const int steps = (stages + KS - 1) >> lg;
   const int pitch = row_pitch<WT>(K), size = part_floats<WT>(tt);
   const long long item_step = (long long)groups * p.rows * K * ES;
 
   // the next stage to be copied: item, its tile and block, step; rows 0..7 of it
-  int li = p.lo + mine, lt = li / p.per, lb = li % p.per, ls = 0, put_slot = 0;
+  int li = p.lo + mine, lt = li / p.per, lb = li - lt * p.per, ls = 0, put_slot = 0;
+  int it = lt, ib = lb;        // (where the computing starts, too)
   const char* lp = li < p.hi ? item_rows<WT>(p, rt.tiles, lt, lb) : nullptr;
   auto put = [&] {
     const int v0 = (ls * KS + ks) * SV;
@@ -465,10 +474,11 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
   if (!UP && flag != nullptr) grid_barrier<CTHREADS>(a.ctl, 1, flag);
 
   // what is being computed: item, its tile and block
-  int i = p.lo + mine, it = i / p.per, ib = i % p.per, parity = 0, slot = 0;
+  int i = p.lo + mine, parity = 0, slot = 0;
+  int tile = p.lo / p.per;
   for (int b_lo = p.lo; b_lo < p.hi;) {
     // the tokens of as many of the next tiles as there is room for
-    int t = b_lo / p.per, used = 0;
+    int t = tile, used = 0;
     bar_sync<CTHREADS>();      // the last ones are no longer read
     const int first = t;
     for (; t * p.per < p.hi; ++t) {
@@ -481,6 +491,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
     }
     const int b_hi = min(p.hi, t * p.per);
     b_lo = b_hi;
+    tile = t;
     bar_sync<CTHREADS>();
 
     while (i < b_hi) {

@@ -14,7 +14,7 @@ struct DecodeArgs {
   int T, D, F, E, k;
   int act;                     // 0 relu, 1 gelu_tanh, 2 swiglu
   int score, n_groups, topk_groups, group_score;
-  int Fs;                      // hidden width of the shared branch, or 0
+  int n_shared, Fs;            // shared experts; hidden width n_shared F of their branch, or 0
   int cap;                     // rows an expert keeps, INT_MAX for no limit
   const void* x;               // [T, D] in the layer's type
   const float* w_gate;

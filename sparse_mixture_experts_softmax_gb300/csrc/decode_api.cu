@@ -91,6 +91,7 @@ moe_status moe_decode(const moe_config* cfg, const moe_weights* w, const void* x
   a.T = c.T; a.D = c.D; a.F = c.F; a.E = c.E; a.k = c.k;
   a.act = c.act; a.score = c.score;
   a.n_groups = c.n_groups; a.topk_groups = c.topk_groups; a.group_score = c.group_score;
+  a.n_shared = c.n_shared;
   a.Fs = c.n_shared * c.F;
   a.cap = expert_capacity_rows(c.capacity_factor, c.T, c.k, c.E);
   a.x = x;

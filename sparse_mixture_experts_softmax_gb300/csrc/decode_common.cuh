@@ -228,10 +228,11 @@ __device__ __noinline__ void select_token(const DecodeArgs& a, int t, float* row
       keep |= 1u << g;
       if (lane == g) gk = 0u;
     }
+    const float inv = 1.0f / (float)per;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int e = lane + 32 * c;
-      if (e < E && !((keep >> (e / per)) & 1u)) key[c] = 0u;
+      const int e = lane + 32 * c, g = (int)(((float)e + 0.5f) * inv);   // e / per, exact below 2^8
+      if (e < E && !((keep >> g) & 1u)) key[c] = 0u;
     }
     __syncwarp();
   }
