@@ -538,7 +538,7 @@ template <typename WT>
 __global__ void __launch_bounds__(THREADS, 1)
 decode_kernel(const __grid_constant__ DecodeArgs a, const int tt) {
   extern __shared__ __align__(128) char sm[];
-  __shared__ int flag, n_tiles, n_routed, scan[16];
+  __shared__ int flag, n_tiles, n_routed, scan[8];
   const Plan P = make_plan<WT>(a.T, a.k, a.E, a.Fs, tt);
   const int tid = threadIdx.x;
   const int T = a.T, D = a.D, k = a.k;

@@ -168,6 +168,10 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_value(uint32_t k) {     // of a number's key
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
 // Token t's scores, kept groups, k experts and gates by one warp; a lane holds
 // the experts lane + 32 c, c < NC.  Each of the k picks is two whole-number
 // reductions: the largest key, then the smallest id that has it.  (Two or four
@@ -177,19 +181,20 @@ template <int NC>
 __device__ __noinline__ void select_token(const DecodeArgs& a, int t, float* row, short* idx,
                                           float* gate, uint32_t* mask, int lane) {
   const int E = a.E, k = a.k;
-  float s[NC];
+  float s[NC], cb[NC];
   uint32_t key[NC];
   const float* lg = a.logits + (long long)t * E;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int e = lane + 32 * c;
     s[c] = e < E ? __ldcg(lg + e) : -INFINITY;
+    cb[c] = a.corr_bias != nullptr && e < E ? __ldg(a.corr_bias + e) : 0.f;
   }
   if (a.score == 0) {
     float m = -FLT_MAX, z = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) m = fmaxf(m, s[c]);
-    m = warp_max(m);
+    m = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       s[c] = lane + 32 * c < E ? expf(s[c] - m) : 0.f;
@@ -205,7 +210,7 @@ __device__ __noinline__ void select_token(const DecodeArgs& a, int t, float* row
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int e = lane + 32 * c;
-    const float kv = (a.corr_bias != nullptr && e < E) ? s[c] + a.corr_bias[e] : s[c];
+    const float kv = a.corr_bias != nullptr ? s[c] + cb[c] : s[c];
     key[c] = e < E ? order_key(kv) : 0u;
     if (e < E) row[e] = kv;
   }
@@ -215,9 +220,15 @@ __device__ __noinline__ void select_token(const DecodeArgs& a, int t, float* row
     uint32_t gk = 0u;
     if (lane < NG) {
       float m1 = -INFINITY, m2 = -INFINITY;
-      for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        const float v = row[e];
-        if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
+      for (int e0 = 0; e0 < per; e0 += 8) {
+        float v[8];            // eight reads at a time, not one after the other
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = e0 + i < per ? row[lane * per + e0 + i] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          m2 = v[i] > m1 ? m1 : (v[i] > m2 ? v[i] : m2);
+          m1 = v[i] > m1 ? v[i] : m1;
+        }
       }
       gk = order_key((per == 1 || a.group_score == 1) ? m1 : m1 + m2);
     }
@@ -278,7 +289,7 @@ struct Routing {
   short* tok;         // [R] slot -> token; slots are expert-major, tokens ascending
   short* slot;        // [T, k] -> slot, or -1 (dropped by the capacity)
   Tile* tiles;        // token tiles of the chosen experts, then of the shared branch
-  int* scan;          // 2 * 8 words of scratch
+  int* scan;          // 8 words of scratch
 };
 
 // Selection and the expert-major lists, by NW warps (every block for itself:
@@ -327,37 +338,31 @@ __device__ __forceinline__ void select_all(const DecodeArgs& a, const Routing& r
     else select_token<8>(a, t, row, r.idx, r.gate, mask, lane);
   }
   __syncthreads();
-  // expert tid's first slot and tiles: scans over the experts' kept counts
-  int mine = 0, mt = 0, incl = 0, incl_t = 0;
+  // expert tid's first slot and tile: one scan over the experts' kept counts (at
+  // most 2048 in all) and, 16 bits up, their tiles
+  int mine = 0, both = 0, incl = 0;
   if (warp < 8) {
     mine = min(__popc(mask[2 * tid]) + __popc(mask[2 * tid + 1]), a.cap);
-    mt = (mine + TT - 1) / TT;
-    incl = mine;
-    incl_t = mt;
+    both = mine + ((mine + TT - 1) / TT << 16);
+    incl = both;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_t, o);
-      if (lane >= o) {
-        incl += u;
-        incl_t += v;
-      }
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
     }
-    if (lane == 31) {
-      r.scan[warp] = incl;
-      r.scan[8 + warp] = incl_t;
-    }
+    if (lane == 31) r.scan[warp] = incl;
   }
   __syncthreads();
   if (warp < 8) {
-    int base = incl - mine, tile = incl_t - mt, total_t = 0;
+    int before = incl - both, total_t = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      if (w < warp) {
-        base += r.scan[w];
-        tile += r.scan[8 + w];
-      }
-      total_t += r.scan[8 + w];
+      const int v = r.scan[w];
+      if (w < warp) before += v;
+      total_t += v >> 16;
     }
+    const int base = before & 0xffff;
+    int tile = before >> 16;
     base_of[tid] = base;
     for (int i = 0; i < mine; i += TT)
       r.tiles[tile++] = Tile{(short)tid, (short)min(TT, mine - i), base + i};
