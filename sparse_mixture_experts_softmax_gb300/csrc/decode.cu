@@ -264,7 +264,14 @@ template <typename WT, bool UP> struct Products;
 template <bool UP> struct Products<bf16, UP> {
   uint32_t at0, at1;           // the lane's token rows of the two token tiles
   int plane, n;
-  float acc[2][2][4];          // token tiles of 8, chains of dependent products
+  // token tiles of 8 by chains of dependent products: the two steps of a block,
+  // and for hidden activations their two parts
+  static constexpr int CH = UP ? 2 : 4;
+  float acc[2][CH][4];
+  __device__ __forceinline__ float total(int t8, int c) const {
+    return UP ? acc[t8][0][c] + acc[t8][1][c]
+              : (acc[t8][0][c] + acc[t8][1][c]) + (acc[t8][CH - 2][c] + acc[t8][CH - 1][c]);
+  }
   __device__ __forceinline__ void begin(const char* rows, int pitch, int tokens, int lane) {
     const uint32_t at = smem_addr(rows) + (lane & 3) * 16;
     n = tokens;
@@ -272,7 +279,9 @@ template <bool UP> struct Products<bf16, UP> {
     at0 = at + min(lane >> 2, n - 1) * pitch;
     at1 = at + min(8 + (lane >> 2), n - 1) * pitch;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[0][0][c] = acc[0][1][c] = acc[1][0][c] = acc[1][1][c] = 0.f;
+    for (int h = 0; h < CH; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[0][h][c] = acc[1][h][c] = 0.f;
   }
   __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
     const int g = lane >> 2, blocks = min(PIECE / 64, (left + 31) / 32);
@@ -288,10 +297,10 @@ template <bool UP> struct Products<bf16, UP> {
       };
       const uint32_t off = (v0 + u * 32) * 2;
       products(acc[0][0], acc[0][1], at0 + off);
-      if (!UP) products(acc[0][0], acc[0][1], at0 + plane + off);
+      if (!UP) products(acc[0][CH - 2], acc[0][CH - 1], at0 + plane + off);
       if (n > 8) {
         products(acc[1][0], acc[1][1], at1 + off);
-        if (!UP) products(acc[1][0], acc[1][1], at1 + plane + off);
+        if (!UP) products(acc[1][CH - 2], acc[1][CH - 1], at1 + plane + off);
       }
     }
   }
@@ -303,16 +312,14 @@ template <bool UP> struct Products<bf16, UP> {
       if (t8 == 0 || n > 8)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          out(lane >> 2, t8 * 8 + (lane & 3) * 2 + c, acc[t8][0][c] + acc[t8][1][c],
-              acc[t8][0][c + 2] + acc[t8][1][c + 2]);
+          out(lane >> 2, t8 * 8 + (lane & 3) * 2 + c, total(t8, c), total(t8, c + 2));
   }
   __device__ __forceinline__ void store(float* buf, int lane) const {
 #pragma unroll
     for (int t8 = 0; t8 < 2; ++t8)
       if (t8 == 0 || n > 8)
-        *reinterpret_cast<float4*>(buf + t8 * 128 + lane * 4) = make_float4(
-            acc[t8][0][0] + acc[t8][1][0], acc[t8][0][1] + acc[t8][1][1],
-            acc[t8][0][2] + acc[t8][1][2], acc[t8][0][3] + acc[t8][1][3]);
+        *reinterpret_cast<float4*>(buf + t8 * 128 + lane * 4) =
+            make_float4(total(t8, 0), total(t8, 1), total(t8, 2), total(t8, 3));
   }
   // Sums of KS warps' stored results, o = me, me + lanes, ..
   template <typename Out>
