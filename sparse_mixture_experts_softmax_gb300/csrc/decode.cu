@@ -33,8 +33,8 @@
 // multiply on the CUDA cores: a lane holds 4 values of K and the sums of all 16
 // rows, so that a token's values are read once for 16 rows.
 //
-// Measured: 64 tokens of the large layer (6.1 GB of weights) 0.95 ms, 6.4 TB/s of
-// the 6.79 of a copy; one token (403 MB) 78 us, 5.1 TB/s, the rest being the three
+// Measured: 64 tokens of the large layer (6.2 GB of weights) 0.95 ms, 6.5 TB/s of
+// the 6.79 of a copy; one token (403 MB) 76 us, 5.3 TB/s, the rest being the three
 // barriers, the selection and the launch.  Left behind (64 tokens): a multiply-add
 // per weight and token on the CUDA cores 4.04 ms; rows from HBM straight to
 // registers, 64 bytes of a row to a load, 1.71 ms, with L2 prefetches ahead of
