@@ -163,6 +163,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// The first of the two bf16 parts of v: the nearest bf16 value, but the largest
+// one for a finite v beyond it; an infinity is a part of its own (with 0).
+__device__ __forceinline__ float bf16_part(float v) {
+  const float h = __bfloat162float(__float2bfloat16_rn(v));
+  return isinf(h) ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : h;
+}
 // A tile's token rows into shared memory (two planes for hidden activations of a
 // bf16 layer, whose rows have zeros from K to the next multiple of 32).
 template <typename WT, bool UP>
@@ -199,10 +205,9 @@ __device__ __forceinline__ void load_tile(const DecodeArgs& a, const Routing& rt
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float u0 = v[2 * j], u1 = v[2 * j + 1];
-          hi[j] = pack_bf16(u0, u1);
-          lo[j] = pack_bf16(u0 - __uint_as_float(hi[j] << 16),
-                            u1 - __uint_as_float(hi[j] & 0xffff0000u));
+          const float h0 = bf16_part(v[2 * j]), h1 = bf16_part(v[2 * j + 1]);
+          hi[j] = pack_bf16(h0, h1);
+          lo[j] = pack_bf16(isinf(h0) ? 0.f : v[2 * j] - h0, isinf(h1) ? 0.f : v[2 * j + 1] - h1);
         }
         *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(to + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);

@@ -298,3 +298,23 @@ def test_decode_weights_past_32_bit_offsets():
         want = want + 0.5 * (x.double() @ w1[e].double().t()).clamp(min=0) @ w2[e].double().t()
     tol = 2.0 ** -8 * want.abs() + _f32_tol(D, F) * want.abs().max()
     assert ((y.double() - want).abs() <= tol).all()
+
+
+def test_largest_hidden_values():
+    """bf16 layers: a hidden value beyond the largest bf16 stays itself, and an
+    infinite one gives infinities, not NaN."""
+    E, F, D = 8, 32, 64
+    w1, w2 = torch.zeros(E, F, D), torch.zeros(E, D, F)
+    x = torch.zeros(2, D)
+    x[0, 0], x[0, 1], x[1, 2] = 2.0 ** 127, 2.0 ** 119, 2.0 ** 127
+    w1[0, 0, 0], w1[0, 0, 1], w1[0, 1, 2] = 1.9921875, 1.5, 4.0
+    w2[0, :, 0], w2[0, 0::2, 1], w2[0, 1::2, 1] = 2.0 ** -10, 1.0, -1.0
+    lb = torch.zeros(E, device="cuda")
+    lb[0] = 200.0                                     # expert 0 with gate 1
+    c = lambda t: t.bfloat16().cuda()  # noqa: E731
+    d = MoEDecoder(torch.zeros(E, D, device="cuda"), c(w1), c(w2), k=1, act="relu", logit_bias=lb,
+                   max_tokens=2)
+    y = d.decode(c(x)).double().cpu()
+    h = 2.0 ** 127 * 1.9921875 + 1.5 * 2.0 ** 119     # fits fp32, rounds past bf16
+    assert ((y[0] - 2.0 ** -10 * h).abs() <= 2.0 ** -8 * 2.0 ** -10 * h).all()
+    assert (y[1, 0::2] == math.inf).all() and (y[1, 1::2] == -math.inf).all()
