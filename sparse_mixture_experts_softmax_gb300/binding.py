@@ -232,9 +232,9 @@ def _stream_on(stream, device) -> int:
     one, or the device's current stream.  The current stream is read as a plain
     address (0.1 us; building torch's Stream object takes 3 us, as long as a
     kernel of a few tokens)."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, the kernels run on a GPU")
     if stream is None:
-        if device.type != "cuda":
-            return 0
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

@@ -19,10 +19,11 @@ _DTYPE = {torch.float32: "f32", torch.bfloat16: "bf16"}
 class MoEDecoder:
     """w_gate [E,D] fp32; w1, w3 [E,F,D], w2 [E,D,F] and the shared branch ws1,
     ws3, ws2 in the layer's type (float32 or bfloat16); b1 [E,F], b2 [E,D],
-    logit_bias [E], corr_bias [E] fp32 or None.  The tensors are used in place,
-    so the decoder follows a layer that is still being trained.  Calls run on the
-    current stream; those of one decoder share its buffers and must not overlap
-    on the GPU."""
+    logit_bias [E], corr_bias [E] fp32 or None.  The tensors are used in place (in
+    the storage that they have when the decoder is made), so the decoder follows
+    a layer that is still being trained.  Calls run on the current stream; those
+    of one decoder share its buffers and must not overlap on the GPU, nor with
+    the decoder's making, which clears its workspace on the current stream."""
 
     def __init__(self, w_gate, w1, w2, w3=None, b1=None, b2=None, k=1, act="relu",
                  score="softmax", n_groups=1, topk_groups=1, group_score="top2_sum",
@@ -61,8 +62,8 @@ class MoEDecoder:
             T, D, F, E, k, act=act, score=score, n_groups=n_groups, topk_groups=topk_groups,
             group_score=group_score, dtype=_DTYPE[dt], has_bias=b1 is not None,
             n_shared=n_shared, capacity_factor=capacity_factor)
-        # the weights stay alive as long as the decoder does
-        self._hold = [t for t, _, _ in want.values()]
+        # that storage stays alive as long as the decoder does, even if a parameter's is replaced
+        self._hold = [t.detach() for t, _, _ in want.values() if t is not None]
         self._weights = B.make_weights(w_gate, w1, w2, w3, b1, b2, logit_bias, corr_bias, ws1,
                                        ws3, ws2)
         self._weights_ref = ctypes.byref(self._weights)

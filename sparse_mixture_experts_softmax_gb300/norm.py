@@ -32,7 +32,8 @@ class NormGrads(NamedTuple):
 
 
 class LayerNorm:
-    """gamma, beta (or None): fp32 [D] on the GPU, used in place.  x_dtype is
+    """gamma, beta (or None): fp32 [D] on the GPU, used in place (the storage that
+    they have when the object is made).  x_dtype is
     the residual stream's type, z_dtype the following layer's input type.  Calls
     run on the current stream; those of one object share its buffers, so they
     must not overlap on the GPU (several streams: order them, or give ``out`` and
@@ -46,7 +47,9 @@ class LayerNorm:
                 raise ValueError(f"{name} must be contiguous float32 of shape [{self.D}]")
         if beta is not None and beta.device != gamma.device:
             raise ValueError(f"beta is on {beta.device}, gamma on {gamma.device}")
-        self.gamma, self.beta, self.device = gamma, beta, gamma.device
+        # (detached: they keep that storage even if a parameter's is replaced)
+        self.gamma, self.beta = gamma.detach(), None if beta is None else beta.detach()
+        self.device = gamma.device
         self.x_type, self.z_type, self.eps = _TORCH[x_dtype], _TORCH[z_dtype], float(eps)
         self.workspace = self.dgamma = self.dbeta = None
         self._plans, self._own = {}, {}
@@ -55,8 +58,7 @@ class LayerNorm:
 
     def _plan(self, shape, delta):
         """What a call on rows of `shape` passes besides its tensors: the C
-        configuration, its reference, the backward pass's workspace size, and a
-        tensor like its statistics.  The last ones are kept: a program passes
+        configuration, its reference, and a tensor like its statistics.  The last ones are kept: a program passes
         the same shapes over and over, and a call costs as much host time as a
         small kernel runs."""
         if len(shape) != 2 or shape[1] != self.D:
@@ -68,16 +70,17 @@ class LayerNorm:
         cfg = B.moe_norm_config(shape[0], self.D, _TYPE[self.x_type], _TYPE[delta or torch.float32],
                                 _TYPE[self.z_type], self.eps)
         p = self._plans[shape, delta] = (
-            cfg, ctypes.byref(cfg), B.moe_norm_workspace_size(cfg),
+            cfg, ctypes.byref(cfg),
             torch.empty(shape[0], dtype=torch.float32, device=self.device))
         return p
 
     def _buffers(self, shape, plain):
-        """Outputs of a call without statistics; one size at a time is kept."""
-        self._own.clear()
+        """Outputs of a call without statistics.  Those of few rows stay for
+        good: a captured graph writes to them as long as it lives."""
         new = lambda dtype: torch.empty(shape, dtype=dtype, device=self.device)  # noqa: E731
-        out = self._own[shape, plain] = NormOut(None if plain else new(self.x_type), new(self.z_type),
-                                            None, None)
+        out = NormOut(None if plain else new(self.x_type), new(self.z_type), None, None)
+        if shape[0] <= B.MOE_DECODE_MAX_TOKENS:
+            self._own[shape, plain] = out
         return out
 
     def _wrong(self, name, t, dtype, shape):
@@ -97,9 +100,9 @@ class LayerNorm:
         """h = x + delta (x itself without a delta), z = norm(h).  ``out``: a
         NormOut whose tensors are written instead of new ones; its h may be
         ``x``.  stats=False (serving) leaves mean and rstd out, and without
-        ``out`` writes h and z to buffers of this object, which its next such
-        call overwrites: allocating two tensors takes as long as launching the
-        kernel does."""
+        ``out`` writes h and z of up to 64 rows to buffers of this object, which
+        its next such call overwrites: allocating two tensors takes as long as
+        launching the kernel does."""
         shape = x.shape
         kind = None if delta is None else delta.dtype
         plan = self._plans.get((shape, kind)) or self._plan(shape, kind)
@@ -122,7 +125,7 @@ class LayerNorm:
             like = torch.empty_like
             out = NormOut(None if delta is None else like(x),
                           like(x) if self.z_type is self.x_type else like(x, dtype=self.z_type),
-                          like(plan[3]), like(plan[3]))
+                          like(plan[2]), like(plan[2]))
         else:
             out = self._own.get((shape, delta is None)) or self._buffers(shape, delta is None)
         h, z, mean, rstd = out
@@ -161,8 +164,10 @@ class LayerNorm:
             self._rows("out.dgamma", out.dgamma, f32, (self.D,))
             if out.dbeta is not None:
                 self._rows("out.dbeta", out.dbeta, f32, (self.D,))
-        if self.workspace is None or self.workspace.numel() < plan[2]:
-            self.workspace = torch.empty(plan[2], dtype=torch.uint8, device=self.device)
+        if self.workspace is None:
+            # for any number of rows, so that it is never replaced under a graph that uses it
+            most = B.moe_norm_workspace_size(B.make_norm_config(2**31 - 1, self.D))
+            self.workspace = torch.empty(most, dtype=torch.uint8, device=self.device)
         status = B.lib().moe_norm_backward(
             plan[1], h.data_ptr(), dz.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
             self._gamma_ptr, None if dres is None else dres.data_ptr(), out.dx.data_ptr(),

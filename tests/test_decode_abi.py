@@ -127,3 +127,10 @@ def test_python_refusals(L):
         d.decode(t(2, D), y=t(3, D))
     with pytest.raises(ValueError):
         d.decode(t(2, D), y=t(2, D, dt=torch.float32))
+
+
+def test_python_refuses_host_tensors(L):
+    t = lambda *s: torch.zeros(*s)  # noqa: E731
+    d = MoEDecoder(t(8, 32), t(8, 16, 32), t(8, 32, 16), k=2, max_tokens=4)
+    with pytest.raises(ValueError, match="GPU"):
+        d.decode(t(2, 32))

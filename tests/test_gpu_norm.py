@@ -286,3 +286,42 @@ def test_more_than_2_31_elements():
     tail = slice(T - 4, T)
     _check_forward(n, h[tail].contiguous(), NormOut(None, r.z[tail], r.mean[tail], r.rstd[tail]),
                    "bf16", gamma, beta)
+
+
+def test_graphs_keep_their_buffers():
+    """A graph of a few rows, or of a small backward pass, still writes to memory
+    of the norm's own after calls of other sizes."""
+    gamma, beta = _params(96)
+    n = LayerNorm(gamma, beta)
+    x, dz = _stream(1, 96, "f32"), _stream(1, 96, "f32", seed=3)
+    want = n.forward(x)
+    n.forward(x, stats=False)
+    grads = n.backward(dz, x, want.mean, want.rstd)
+    dx, dgamma = grads.dx.clone(), grads.dgamma.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = n.forward(x, stats=False)
+        b = n.backward(dz, x, want.mean, want.rstd, out=grads)
+    held = n.workspace.data_ptr(), r.z.data_ptr()
+    for T in (2, 65, 5000):
+        big = _stream(T, 96, "f32", seed=T)
+        s = n.forward(big)
+        assert torch.equal(n.forward(big, stats=False).z, s.z)
+        n.backward(big, big, s.mean, s.rstd)
+    assert held == (n.workspace.data_ptr(), n.forward(x, stats=False).z.data_ptr())
+    others = [torch.full((1, 96), 7.0, device="cuda") for _ in range(64)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r.z, want.z) and torch.equal(b.dx, dx) and torch.equal(b.dgamma, dgamma)
+    assert all(bool((o == 7.0).all()) for o in others)
+
+
+def test_parameter_storage_is_kept():
+    """Replacing a parameter's storage neither frees nor changes what the norm reads."""
+    gamma, beta = _params(64)
+    p = torch.nn.Parameter(gamma.clone())
+    n, x = LayerNorm(p, beta), _stream(5, 64, "f32")
+    want = LayerNorm(gamma, beta).forward(x).z
+    p.data = torch.zeros_like(gamma)
+    assert torch.equal(n.forward(x).z, want)

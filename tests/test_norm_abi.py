@@ -131,3 +131,19 @@ def test_python_refusals(L):
         n.backward(x.bfloat16(), x, torch.zeros(3), torch.zeros(3))
     with pytest.raises(ValueError):
         n.backward(x, x, torch.zeros(3), torch.zeros(3), dres=torch.zeros(3, 15))
+
+
+def test_workspace_of_any_rows(L):
+    """The workspace for the most rows holds every smaller call's."""
+    for D in (1, 7, 64, 4096, 8191, 16384):
+        most = B.moe_norm_workspace_size(_cfg(T=2**31 - 1, D=D))
+        sizes = [B.moe_norm_workspace_size(_cfg(T=T, D=D)) for T in (0, 1, 17, 303, 4096, 1 << 20)]
+        assert 0 < max(sizes) <= most and sizes == sorted(sizes)
+
+
+def test_python_refuses_host_tensors(L):
+    n, x = LayerNorm(torch.ones(16)), torch.zeros(3, 16)
+    with pytest.raises(ValueError, match="GPU"):
+        n.forward(x)
+    with pytest.raises(ValueError, match="GPU"):
+        n.backward(x, x, torch.zeros(3), torch.zeros(3))
