@@ -273,9 +273,13 @@ template <bool UP> struct Products<bf16, UP> {
   // and for hidden activations their two parts
   static constexpr int CH = UP ? 2 : 4;
   float acc[2][CH][4];
+  // A sum over the first parts that is not finite is the result: the second
+  // parts, zeros or of the other sign, would make a NaN of an infinite weight's
+  // or an overflowing product's infinity, and they overflow only where it does.
   __device__ __forceinline__ float total(int t8, int c) const {
-    return UP ? acc[t8][0][c] + acc[t8][1][c]
-              : (acc[t8][0][c] + acc[t8][1][c]) + (acc[t8][CH - 2][c] + acc[t8][CH - 1][c]);
+    const float first = acc[t8][0][c] + acc[t8][1][c];
+    if (UP) return first;
+    return isfinite(first) ? first + (acc[t8][CH - 2][c] + acc[t8][CH - 1][c]) : first;
   }
   __device__ __forceinline__ void begin(const char* rows, int pitch, int tokens, int lane) {
     const uint32_t at = smem_addr(rows) + (lane & 3) * 16;

@@ -318,3 +318,33 @@ def test_largest_hidden_values():
     h = 2.0 ** 127 * 1.9921875 + 1.5 * 2.0 ** 119     # fits fp32, rounds past bf16
     assert ((y[0] - 2.0 ** -10 * h).abs() <= 2.0 ** -8 * 2.0 ** -10 * h).all()
     assert (y[1, 0::2] == math.inf).all() and (y[1, 1::2] == -math.inf).all()
+
+
+@pytest.mark.parametrize("F", [32, 2048])          # one warp an item, and several
+def test_infinite_down_weights(F):
+    """bf16 layers: an infinite W2 value times a hidden value is an infinity of its
+    sign, and so is a product past fp32's range, whatever the second part of the
+    hidden value is (zero, of the same sign, of the other sign)."""
+    E, D = 8, 64
+    w1, w2 = torch.zeros(E, F, D), torch.zeros(E, D, F)
+    h = [2.0, 1 + 2.0 ** -9, 1 + 1.5 * 2.0 ** -8, 2048 * (1 + 1.5 * 2.0 ** -8)]
+    x = torch.zeros(4, D)
+    for t, v in enumerate(h):                         # token t: hidden value 0 of expert 0 is h[t]
+        first = float(torch.tensor(v).bfloat16())
+        x[t, 2 * t], x[t, 2 * t + 1] = first, v - first
+        w1[0, 0, 2 * t] = w1[0, 0, 2 * t + 1] = 1.0
+    w2[0, 1, 0], w2[0, 2, 0], w2[0, 3, 0], w2[0, 4, 0] = math.inf, -math.inf, 3e38, -3e38
+    w2[0, 5, 0] = 1.0
+    lb = torch.zeros(E, device="cuda")
+    lb[0] = 200.0                                     # expert 0 with gate 1
+    c = lambda t: t.bfloat16().cuda()  # noqa: E731
+    d = MoEDecoder(torch.zeros(E, D, device="cuda"), c(w1), c(w2), k=1, act="relu", logit_bias=lb,
+                   max_tokens=4)
+    for T in (4, 1):
+        y = d.decode(c(x[4 - T:])).double().cpu()
+        assert (y[:, 1] == math.inf).all() and (y[:, 2] == -math.inf).all()
+        assert y[-1, 3] == math.inf and y[-1, 4] == -math.inf
+        want = torch.tensor(h[4 - T:], dtype=torch.float64)
+        assert ((y[:, 5] - want).abs() <= 2.0 ** -8 * want).all()
+        assert not y[:, 0].any() and not y[:, 6:].any()
+    assert d.status() == 0
