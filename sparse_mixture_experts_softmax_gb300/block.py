@@ -35,20 +35,28 @@ class MoEBlock:
         want = torch.bfloat16 if layer.dtype == "bf16" else torch.float32
         if norm.z_type != want:
             raise ValueError(f"the norm writes {norm.z_type}, the layer reads {want}")
+        if norm.device != layer.w_gate.device:
+            raise ValueError(f"the norm is on {norm.device}, the layer on {layer.w_gate.device}")
         self.norm, self.layer = norm, layer
         self._decoder: Optional[MoEDecoder] = None
 
     def forward(self, h, delta=None):
         """(state, y) of the layer's T tokens: state.h is the stream h + delta
         (h itself without a delta), y [T, D] fp32 the layer's output."""
+        if h.shape[0] != self.layer.cfg.T:
+            raise ValueError(f"the layer was made for {self.layer.cfg.T} tokens, got {tuple(h.shape)}")
         r = self.norm.forward(h, delta)
         return BlockState(h if r.h is None else r.h, r.z, r.mean, r.rstd), self.layer.forward(r.z)
 
     def backward(self, state: BlockState, dout):
-        """Gradient [T, D] fp32 at state.h (and so at the delta) from dout, the
-        one at state.h + y.  The layer's and the norm's parameter gradients are
+        """Gradient [T, D] fp32 at state.h (and so at the delta) from dout (fp32),
+        the one at state.h + y.  The layer's and the norm's parameter gradients are
         left in their buffers.  The layer's workspace must still hold the state
         of this block's forward."""
+        # before the layer's launches, which take plain addresses
+        shape = (self.layer.cfg.T, self.norm.D)
+        self.norm._rows("dout", dout, torch.float32, shape)
+        self.norm._rows("state.z", state.z, self.norm.z_type, shape)
         dz = torch.empty_like(dout)
         self.layer.backward(state.z, dout, dz)
         return self.norm.backward(dz, state.h, state.mean, state.rstd, dres=dout).dx
