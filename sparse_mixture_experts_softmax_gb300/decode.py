@@ -25,6 +25,14 @@ class MoEDecoder:
     of one decoder share its buffers and must not overlap on the GPU, nor with
     the decoder's making, which clears its workspace on the current stream."""
 
+    # calls pass addresses and configurations made from these once
+    _FIXED = frozenset(("workspace", "cfg", "device", "dtype", "D", "k", "max_tokens"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} is fixed when the decoder is made")
+        self.__dict__[name] = value
+
     def __init__(self, w_gate, w1, w2, w3=None, b1=None, b2=None, k=1, act="relu",
                  score="softmax", n_groups=1, topk_groups=1, group_score="top2_sum",
                  logit_bias=None, corr_bias=None, n_shared=0, ws1=None, ws3=None, ws2=None,
@@ -115,7 +123,7 @@ class MoEDecoder:
                                     c[9], B._stream_on(None, self.device))
         if status != B.MOE_OK:
             B._check("moe_decode", status)
-        self.idx, self.gate = c[3], c[4]
+        self.__dict__.update(idx=c[3], gate=c[4])      # (without __setattr__'s look-up)
         return y
 
     def status(self) -> int:

@@ -37,7 +37,16 @@ class LayerNorm:
     the residual stream's type, z_dtype the following layer's input type.  Calls
     run on the current stream; those of one object share its buffers, so they
     must not overlap on the GPU (several streams: order them, or give ``out`` and
-    use an object each)."""
+    use an object each).  gamma and beta change in place only."""
+
+    # calls pass configurations made from these once, and check neither parameter again
+    _FIXED = frozenset(("gamma", "beta", "D", "device", "x_type", "z_type", "eps"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} is fixed when the norm is made (gamma and beta change "
+                                 "in place)")
+        self.__dict__[name] = value
 
     def __init__(self, gamma, beta=None, x_dtype="f32", z_dtype="f32", eps=1e-5):
         self.D = int(gamma.numel())
@@ -53,8 +62,6 @@ class LayerNorm:
         self.x_type, self.z_type, self.eps = _TORCH[x_dtype], _TORCH[z_dtype], float(eps)
         self.workspace = self.dgamma = self.dbeta = None
         self._plans, self._own = {}, {}
-        self._gamma_ptr = gamma.data_ptr()
-        self._beta_ptr = None if beta is None else beta.data_ptr()
 
     def _plan(self, shape, delta):
         """What a call on rows of `shape` passes besides its tensors: the C
@@ -130,8 +137,9 @@ class LayerNorm:
             out = self._own.get((shape, delta is None)) or self._buffers(shape, delta is None)
         h, z, mean, rstd = out
         status = B.lib().moe_norm_forward(
-            plan[1], x.data_ptr(), None if delta is None else delta.data_ptr(), self._gamma_ptr,
-            self._beta_ptr, None if h is None else h.data_ptr(), z.data_ptr(),
+            plan[1], x.data_ptr(), None if delta is None else delta.data_ptr(),
+            self.gamma.data_ptr(), None if self.beta is None else self.beta.data_ptr(),
+            None if h is None else h.data_ptr(), z.data_ptr(),
             None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
             B._stream_on(None, self.device))
         if status != B.MOE_OK:
@@ -170,7 +178,7 @@ class LayerNorm:
             self.workspace = torch.empty(most, dtype=torch.uint8, device=self.device)
         status = B.lib().moe_norm_backward(
             plan[1], h.data_ptr(), dz.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            self._gamma_ptr, None if dres is None else dres.data_ptr(), out.dx.data_ptr(),
+            self.gamma.data_ptr(), None if dres is None else dres.data_ptr(), out.dx.data_ptr(),
             out.dgamma.data_ptr(), None if out.dbeta is None else out.dbeta.data_ptr(),
             self.workspace.data_ptr(), self.workspace.numel(), B._stream_on(None, self.device))
         if status != B.MOE_OK:

@@ -134,3 +134,12 @@ def test_python_refuses_host_tensors(L):
     d = MoEDecoder(t(8, 32), t(8, 16, 32), t(8, 32, 16), k=2, max_tokens=4)
     with pytest.raises(ValueError, match="GPU"):
         d.decode(t(2, 32))
+
+
+def test_what_a_decoder_is_made_of_stays(L):
+    """Calls pass addresses taken once: a replaced workspace would be freed under them."""
+    t = lambda *s: torch.zeros(*s)  # noqa: E731
+    d = MoEDecoder(t(8, 32), t(8, 16, 32), t(8, 32, 16), k=2, max_tokens=4)
+    for name in ("workspace", "cfg", "device", "dtype", "D", "k", "max_tokens"):
+        with pytest.raises(AttributeError, match=name):
+            setattr(d, name, None)

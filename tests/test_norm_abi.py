@@ -147,3 +147,17 @@ def test_python_refuses_host_tensors(L):
         n.forward(x)
     with pytest.raises(ValueError, match="GPU"):
         n.backward(x, x, torch.zeros(3), torch.zeros(3))
+
+
+def test_what_a_norm_is_made_of_stays(L):
+    """Calls pass addresses and configurations taken once: replacing what they were
+    taken from would leave them at freed memory or with the old values."""
+    n = LayerNorm(torch.ones(16), torch.zeros(16))
+    n.beta = n.beta             # (as ``n.beta += t`` ends)
+    for name, value in (("gamma", torch.ones(16)), ("beta", None), ("D", 8), ("eps", 1e-6),
+                        ("x_type", torch.bfloat16), ("z_type", torch.bfloat16),
+                        ("device", torch.device("meta"))):
+        with pytest.raises(AttributeError, match=name):
+            setattr(n, name, value)
+    n.gamma *= 2                # in place is how they are trained
+    assert float(n.gamma[0]) == 2.0
