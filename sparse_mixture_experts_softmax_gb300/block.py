@@ -61,28 +61,43 @@ class MoEBlock:
         self.layer.backward(state.z, dout, dz)
         return self.norm.backward(dz, state.h, state.mean, state.rstd, dres=dout).dx
 
+    def _served(self):
+        """The layer's tensors that serving reads, by the decoder's names for them
+        and the layer's own."""
+        la, lp = self.layer, "_lp" if self.layer.dtype == "bf16" else ""
+        own = dict(w_gate="w_gate", w1="w1" + lp, w3="w3" + lp, w2="w2" + lp, b1="b1", b2="b2",
+                   logit_bias="logit_bias", corr_bias="corr_bias", ws1="ws1" + lp, ws3="ws3" + lp,
+                   ws2="ws2" + lp)
+        return {name: (attr, getattr(la, attr)) for name, attr in own.items()}
+
     @property
     def decoder(self) -> MoEDecoder:
         """The few-token form of the layer, on the weights it trains (made on
-        the first use, which is outside of any graph capture)."""
+        the first use, which is outside of any graph capture).  It reads the
+        storage that they had then: once a tensor of the layer has been replaced,
+        rather than changed in place, this raises; make a new block."""
         d = self._decoder
         if d is None:
-            la, c = self.layer, self.layer.cfg
-            lp = la.dtype == "bf16"
-            pick = lambda name: getattr(la, name + "_lp" if lp else name)  # noqa: E731
+            c = self.layer.cfg
             name_of = lambda table, v: next(k for k, i in table.items() if i == v)  # noqa: E731
+            served = self._served()
             d = self._decoder = MoEDecoder(
-                la.w_gate, pick("w1"), pick("w2"), w3=pick("w3"), b1=la.b1, b2=la.b2, k=c.k,
-                act=name_of(B.ACT, c.act), score=name_of(B.SCORE, c.score), n_groups=c.n_groups,
-                topk_groups=c.topk_groups, group_score=name_of(B.GROUP_SCORE, c.group_score),
-                logit_bias=la.logit_bias, corr_bias=la.corr_bias, n_shared=c.n_shared,
-                ws1=pick("ws1"), ws3=pick("ws3"), ws2=pick("ws2"),
+                **{name: t for name, (_, t) in served.items()}, k=c.k, act=name_of(B.ACT, c.act),
+                score=name_of(B.SCORE, c.score), n_groups=c.n_groups, topk_groups=c.topk_groups,
+                group_score=name_of(B.GROUP_SCORE, c.group_score), n_shared=c.n_shared,
                 capacity_factor=c.capacity_factor)
+            self._read = [(attr, None if t is None else t.data_ptr()) for attr, t in served.values()]
+            return d
+        for attr, at in self._read:
+            t = getattr(self.layer, attr)
+            if (None if t is None else t.data_ptr()) != at:
+                raise ValueError(f"the layer's {attr} was replaced after the decoder was made")
         return d
 
     def decode(self, h, delta=None):
         """(h', y) for a few tokens: h' = h + delta (h without one) and y [T, D] in
         the layer's type, the next block's delta.  Both are buffers of this
         block, which its next call overwrites."""
+        d = self.decoder
         r = self.norm.forward(h, delta, stats=False)
-        return h if r.h is None else r.h, self.decoder.decode(r.z)
+        return h if r.h is None else r.h, d.decode(r.z)

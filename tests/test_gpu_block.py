@@ -111,3 +111,29 @@ def test_example_runs():
     losses, err = mod.main(6)
     assert losses[-1] < losses[0]
     assert err <= 2 * 3 * 2.0 ** -8        # two blocks
+
+
+@pytest.mark.parametrize("how", ["attribute", "data"])
+def test_block_does_not_serve_replaced_weights(how):
+    """The decoder reads the storage that the layer's tensors had when it was made:
+    weights trained in place are served, others are refused, not ignored."""
+    wl, inp, block = _block("grouped_cb", 16, 6, "bf16")
+    h0 = torch.randn(4, wl.D, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    y = block.decode(h0)[1].clone()
+    block.layer.w2_lp.mul_(2)
+    assert torch.equal(block.decode(h0)[1], 2 * y)
+    for name in ("w2_lp", "corr_bias"):
+        old = getattr(block.layer, name)
+        if how == "attribute":
+            setattr(block.layer, name, old.clone())
+        else:
+            keep, old.data = old.data, old.clone()
+        with pytest.raises(ValueError, match=name):
+            block.decode(h0)
+        if how == "attribute":
+            setattr(block.layer, name, old)
+        else:
+            old.data = keep
+    assert torch.equal(block.decode(h0)[1], 2 * y)
+    again = MoEBlock(block.norm, block.layer)
+    assert torch.equal(again.decode(h0)[1], 2 * y)
