@@ -227,13 +227,23 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _stream_on(stream, device) -> int:
-    """The raw stream for a call on `device` (a CUDA torch.device): the given
-    one, or the device's current stream.  The current stream is read as a plain
-    address (0.1 us; building torch's Stream object takes 3 us, as long as a
-    kernel of a few tokens)."""
+def _on_current(device):
+    """Raises unless `device` (a torch.device) is the current GPU, where the
+    library launches: with tensors of another one a kernel would run on the wrong
+    GPU, on addresses that mean nothing there."""
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}, the kernels run on a GPU")
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()} (torch.cuda.device selects another)")
+
+
+def _stream_on(stream, device) -> int:
+    """The raw stream for a call on `device` (a CUDA torch.device, and the current
+    one): the given one, or the device's current stream.  The current stream is
+    read as a plain address (0.1 us; building torch's Stream object takes 3 us, as
+    long as a kernel of a few tokens)."""
+    _on_current(device)
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -505,7 +515,8 @@ def make_norm_config(T, D, x_type="f32", delta_type="f32", z_type="f32",
 def moe_norm_forward(cfg, x, delta, gamma, beta, h, z, mean=None, rstd=None, stream=None):
     _check("moe_norm_forward",
            lib().moe_norm_forward(ctypes.byref(cfg), _ptr(x), _ptr(delta), _ptr(gamma), _ptr(beta),
-                                  _ptr(h), _ptr(z), _ptr(mean), _ptr(rstd), _stream(stream)))
+                                  _ptr(h), _ptr(z), _ptr(mean), _ptr(rstd),
+                                  _stream_on(stream, x.device)))
 
 
 def moe_norm_workspace_size(cfg) -> int:
@@ -517,7 +528,8 @@ def moe_norm_backward(cfg, h, dz, mean, rstd, gamma, dres, dx, dgamma, dbeta, wo
     _check("moe_norm_backward",
            lib().moe_norm_backward(ctypes.byref(cfg), _ptr(h), _ptr(dz), _ptr(mean), _ptr(rstd),
                                    _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-                                   _ptr(workspace), workspace.numel(), _stream(stream)))
+                                   _ptr(workspace), workspace.numel(),
+                                   _stream_on(stream, h.device)))
 
 
 # ---- the layer for a few tokens (include/moe_block.h)
@@ -531,18 +543,20 @@ def moe_decode_workspace_size(cfg) -> int:
 
 def moe_decode_init(cfg, workspace, stream=None):
     _check("moe_decode_init", lib().moe_decode_init(ctypes.byref(cfg), _ptr(workspace),
-                                                    workspace.numel(), _stream(stream)))
+                                                    workspace.numel(),
+                                                    _stream_on(stream, workspace.device)))
 
 
 def moe_decode(cfg, weights, x, y, workspace, idx=None, gate=None, stream=None):
     _check("moe_decode",
            lib().moe_decode(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(y), _ptr(idx),
-                            _ptr(gate), _ptr(workspace), workspace.numel(), _stream(stream)))
+                            _ptr(gate), _ptr(workspace), workspace.numel(),
+                            _stream_on(stream, x.device)))
 
 
 def moe_decode_status(cfg, workspace, stream=None) -> int:
     out = ctypes.c_int32(0)
     _check("moe_decode_status",
            lib().moe_decode_status(ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
-                                   ctypes.addressof(out), _stream(stream)))
+                                   ctypes.addressof(out), _stream_on(stream, workspace.device)))
     return int(out.value)

@@ -21,9 +21,10 @@ class MoEDecoder:
     ws3, ws2 in the layer's type (float32 or bfloat16); b1 [E,F], b2 [E,D],
     logit_bias [E], corr_bias [E] fp32 or None.  The tensors are used in place (in
     the storage that they have when the decoder is made), so the decoder follows
-    a layer that is still being trained.  Calls run on the current stream; those
-    of one decoder share its buffers and must not overlap on the GPU, nor with
-    the decoder's making, which clears its workspace on the current stream."""
+    a layer that is still being trained.  Calls run on the current stream of
+    their GPU, which has to be the current one; those of one decoder share its
+    buffers and must not overlap on the GPU, nor with the decoder's making, which
+    clears its workspace on the current stream."""
 
     # calls pass addresses and configurations made from these once
     _FIXED = frozenset(("workspace", "cfg", "device", "dtype", "D", "k", "max_tokens"))

@@ -2,7 +2,8 @@
 
 Allocates (through torch) the fp32 master parameters, the bf16 working copies,
 the gradient buffers and the workspace, and calls the C ABI.  It computes
-nothing itself.
+nothing itself.  Calls run on the current stream of the layer's GPU, which has
+to be the current one.
 """
 
 from __future__ import annotations
@@ -66,6 +67,7 @@ class MoELayer:
 
     # expert weights in the compute dtype (bf16 copies for bf16 layers)
     def weights(self) -> B.moe_weights:
+        B._on_current(self.w_gate.device)
         lp = self.dtype == "bf16"
         return B.make_weights(self.w_gate, self.w1_lp if lp else self.w1,
                               self.w2_lp if lp else self.w2, self.w3_lp if lp else self.w3,
@@ -74,6 +76,7 @@ class MoELayer:
                               self.ws2_lp if lp else self.ws2)
 
     def params(self) -> B.moe_params:
+        B._on_current(self.w_gate.device)
         return B.make_params(self.w_gate, self.w1, self.w2, self.grads, w3=self.w3, b1=self.b1,
                              b2=self.b2, w1_lp=self.w1_lp, w3_lp=self.w3_lp, w2_lp=self.w2_lp,
                              logit_bias=self.logit_bias, corr_bias=self.corr_bias,

@@ -33,11 +33,11 @@ class NormGrads(NamedTuple):
 
 class LayerNorm:
     """gamma, beta (or None): fp32 [D] on the GPU, used in place (the storage that
-    they have when the object is made).  x_dtype is
-    the residual stream's type, z_dtype the following layer's input type.  Calls
-    run on the current stream; those of one object share its buffers, so they
-    must not overlap on the GPU (several streams: order them, or give ``out`` and
-    use an object each).  gamma and beta change in place only."""
+    they have when the object is made); they change in place only.  x_dtype is the
+    residual stream's type, z_dtype the following layer's input type.  Calls run on
+    the current stream of their GPU, which has to be the current one; those of one
+    object share its buffers, so they must not overlap on the GPU (several streams:
+    order them, or give ``out`` and use an object each)."""
 
     # calls pass configurations made from these once, and check neither parameter again
     _FIXED = frozenset(("gamma", "beta", "D", "device", "x_type", "z_type", "eps"))
