@@ -24,7 +24,8 @@ class MoEDecoder:
     a layer that is still being trained.  Calls run on the current stream of
     their GPU, which has to be the current one; those of one decoder share its
     buffers and must not overlap on the GPU, nor with the decoder's making, which
-    clears its workspace on the current stream."""
+    clears its workspace on the current stream (and so cannot be part of a graph
+    capture: the workspace would be cleared by the graph's replays only)."""
 
     # calls pass addresses and configurations made from these once
     _FIXED = frozenset(("workspace", "cfg", "device", "dtype", "D", "k", "max_tokens"))
@@ -65,6 +66,8 @@ class MoEDecoder:
                                  f"{t.dtype} {tuple(t.shape)}")
             if t.device != w1.device:
                 raise ValueError(f"{name} is on {t.device}, w1 on {w1.device}")
+        if w1.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise ValueError("a decoder cannot be made while its stream is being captured")
         self.device, self.dtype, self.D, self.k = w1.device, dt, D, int(k)
         self.max_tokens = int(max_tokens)
         self._make = lambda T: B.make_config(

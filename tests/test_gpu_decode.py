@@ -348,3 +348,23 @@ def test_infinite_down_weights(F):
         assert ((y[:, 5] - want).abs() <= 2.0 ** -8 * want).all()
         assert not y[:, 0].any() and not y[:, 6:].any()
     assert d.status() == 0
+
+
+def test_a_decoder_is_not_made_in_a_capture():
+    """Its workspace would be cleared by the graph's replays only."""
+    wl = _wl(T=2)
+    inp = _inputs(wl, seed=13)
+    x = device_x(wl, inp)
+    d = _decoder(wl, inp)
+    want = d.decode(x).clone()
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    weights = [inp[n].cuda() for n in ("w_gate", "w1_bf16", "w2_bf16", "w3_bf16")]
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captur"):
+            MoEDecoder(weights[0], weights[1], weights[2], w3=weights[3], k=wl.k, act=wl.act)
+        d.decode(x, y=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
