@@ -368,3 +368,24 @@ def test_a_decoder_is_not_made_in_a_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_an_expired_grid_barrier_ends_in_order(which):
+    """A barrier's counter that starts one low never fills: every block's wait runs
+    out (2 s), the call ends, the status says so, and a reset restores the decoder."""
+    wl = _wl(T=6, D=256, F=136, E=16, k=3, n_shared=1)
+    inp = _inputs(wl, seed=14)
+    d = _decoder(wl, inp)
+    x = device_x(wl, inp)
+    want = d.decode(x).clone()
+    assert d.status() == 0
+    counters = d.workspace[:256].view(torch.int32)
+    assert counters[32:35].tolist() == [0, 0, 0]     # ready for the next call
+    counters[32 + which] = -1
+    d.decode(x)
+    assert d.status() == B.MOE_ERR_TIMEOUT
+    assert counters[32:35].tolist() == [0, 0, 0]
+    d.reset()
+    assert torch.equal(d.decode(x), want)
+    assert d.status() == 0
