@@ -668,11 +668,13 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   const int sms = sm_count(), tt = tile_tokens<WT>(a);
   if (sms <= 0) return cudaErrorUnknown;
   if (tt <= 0) return cudaErrorInvalidValue;    // (past the entry point's limits)
-  // a block per SM, or fewer where each would have less than 8 KB of weights, or
-  // one block, whose barriers are its own, for up to 64 KB
+  // a block per SM, or fewer where each would have less than 8 KB of weights (the
+  // kernel's time hardly goes with it: 4 KB, 16 KB and a block on every SM are
+  // within 0.2 us of 13.4 at 96 KB of weights, of 13.6 at 390 KB, of 14.4 at
+  // 780 KB; one block alone takes 0.3 us more than four at 32 KB, 23 us at 390 KB)
   const long long experts = (long long)a.T * a.k < a.E ? (long long)a.T * a.k : a.E;
   const long long bytes = (experts * a.F + a.Fs) * a.D * (a.act == 2 ? 3 : 2) * (int)sizeof(WT);
-  const long long blocks = bytes <= 65536 ? 1 : (bytes + 8191) / 8192;
+  const long long blocks = (bytes + 8191) / 8192;
   return launch_cooperative(decode_kernel<WT>, (int)(blocks < sms ? blocks : sms), THREADS,
                             attr_done, st, a, tt);
 }
