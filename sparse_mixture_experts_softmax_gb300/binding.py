@@ -14,6 +14,7 @@ import os
 from typing import Optional
 
 import torch
+from torch import _C
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_gb300.so")
 
@@ -233,9 +234,9 @@ def _on_current(device):
     GPU, on addresses that mean nothing there."""
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}, the kernels run on a GPU")
-    if device.index != torch._C._cuda_getDevice():
+    if device.index != _C._cuda_getDevice():
         raise ValueError(f"the tensors are on {device}, the current device is "
-                         f"cuda:{torch._C._cuda_getDevice()} (torch.cuda.device selects another)")
+                         f"cuda:{_C._cuda_getDevice()} (torch.cuda.device selects another)")
 
 
 def _stream_on(stream, device) -> int:
@@ -243,9 +244,11 @@ def _stream_on(stream, device) -> int:
     one): the given one, or the device's current stream.  The current stream is
     read as a plain address (0.1 us; building torch's Stream object takes 3 us, as
     long as a kernel of a few tokens)."""
-    _on_current(device)
+    index = device.index
+    if index is None or index != _C._cuda_getDevice():
+        _on_current(device)              # raises (a CPU's device has no index)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

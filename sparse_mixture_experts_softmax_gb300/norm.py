@@ -39,7 +39,7 @@ class LayerNorm:
     object share its buffers, so they must not overlap on the GPU (several streams:
     order them, or give ``out`` and use an object each)."""
 
-    # calls pass configurations made from these once, and check neither parameter again
+    # calls pass addresses and configurations made from these once
     _FIXED = frozenset(("gamma", "beta", "D", "device", "x_type", "z_type", "eps"))
 
     def __setattr__(self, name, value):
@@ -58,6 +58,10 @@ class LayerNorm:
             raise ValueError(f"beta is on {beta.device}, gamma on {gamma.device}")
         # (detached: they keep that storage even if a parameter's is replaced)
         self.gamma, self.beta = gamma.detach(), None if beta is None else beta.detach()
+        # what the addresses below are of, whatever becomes of the attributes' storage
+        self._held = gamma.detach(), None if beta is None else beta.detach()
+        self._gamma_ptr = gamma.data_ptr()
+        self._beta_ptr = None if beta is None else beta.data_ptr()
         self.device = gamma.device
         self.x_type, self.z_type, self.eps = _TORCH[x_dtype], _TORCH[z_dtype], float(eps)
         self.workspace = self.dgamma = self.dbeta = None
@@ -137,9 +141,8 @@ class LayerNorm:
             out = self._own.get((shape, delta is None)) or self._buffers(shape, delta is None)
         h, z, mean, rstd = out
         status = B.lib().moe_norm_forward(
-            plan[1], x.data_ptr(), None if delta is None else delta.data_ptr(),
-            self.gamma.data_ptr(), None if self.beta is None else self.beta.data_ptr(),
-            None if h is None else h.data_ptr(), z.data_ptr(),
+            plan[1], x.data_ptr(), None if delta is None else delta.data_ptr(), self._gamma_ptr,
+            self._beta_ptr, None if h is None else h.data_ptr(), z.data_ptr(),
             None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
             B._stream_on(None, self.device))
         if status != B.MOE_OK:
@@ -178,7 +181,7 @@ class LayerNorm:
             self.workspace = torch.empty(most, dtype=torch.uint8, device=self.device)
         status = B.lib().moe_norm_backward(
             plan[1], h.data_ptr(), dz.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            self.gamma.data_ptr(), None if dres is None else dres.data_ptr(), out.dx.data_ptr(),
+            self._gamma_ptr, None if dres is None else dres.data_ptr(), out.dx.data_ptr(),
             out.dgamma.data_ptr(), None if out.dbeta is None else out.dbeta.data_ptr(),
             self.workspace.data_ptr(), self.workspace.numel(), B._stream_on(None, self.device))
         if status != B.MOE_OK:

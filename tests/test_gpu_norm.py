@@ -325,3 +325,13 @@ def test_parameter_storage_is_kept():
     want = LayerNorm(gamma, beta).forward(x).z
     p.data = torch.zeros_like(gamma)
     assert torch.equal(n.forward(x).z, want)
+
+
+def test_the_norms_own_parameters_keep_their_storage():
+    """So does replacing the storage of the norm's own attribute."""
+    gamma, beta = _params(64)
+    n, x = LayerNorm(gamma.clone(), beta), _stream(5, 64, "f32")
+    want = n.forward(x).z
+    n.gamma.data = torch.zeros_like(gamma)
+    others = [torch.zeros(64, device="cuda") for _ in range(16)]     # where a freed one would be
+    assert torch.equal(n.forward(x).z, want) and len(others) == 16
