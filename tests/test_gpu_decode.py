@@ -389,3 +389,25 @@ def test_an_expired_grid_barrier_ends_in_order(which):
     d.reset()
     assert torch.equal(d.decode(x), want)
     assert d.status() == 0
+
+
+def test_direct_bindings():
+    """The binding's functions, as a program without the class calls them."""
+    wl = _wl(T=5, D=136, F=72, E=16, k=3)
+    inp = _inputs(wl, seed=15)
+    d = _decoder(wl, inp)
+    x = device_x(wl, inp)
+    want = d.decode(x)
+    w = [inp[n].cuda() for n in ("w_gate", "w1_bf16", "w2_bf16", "w3_bf16")]
+    cfg = B.make_config(5, 136, 72, 16, 3, act="swiglu", score=wl.score, dtype="bf16",
+                        has_bias=False)
+    weights = B.make_weights(w[0], w[1], w[2], w3=w[3])
+    ws = torch.empty(B.moe_decode_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    y, idx, gate = torch.empty_like(x), torch.empty_like(d.idx), torch.empty_like(d.gate)
+    B.moe_decode_init(cfg, ws)
+    B.moe_decode(cfg, weights, x, y, ws, idx=idx, gate=gate)
+    assert B.moe_last_launch_count() == 1
+    assert torch.equal(y, want) and torch.equal(idx, d.idx) and torch.equal(gate, d.gate)
+    y.zero_()
+    B.moe_decode(cfg, weights, x, y, ws)              # the routing is optional
+    assert torch.equal(y, want) and B.moe_decode_status(cfg, ws) == 0

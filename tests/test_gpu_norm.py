@@ -335,3 +335,30 @@ def test_the_norms_own_parameters_keep_their_storage():
     n.gamma.data = torch.zeros_like(gamma)
     others = [torch.zeros(64, device="cuda") for _ in range(16)]     # where a freed one would be
     assert torch.equal(n.forward(x).z, want) and len(others) == 16
+
+
+def test_direct_bindings():
+    """The binding's functions, as a program without the class calls them."""
+    T, D = 21, 264
+    gamma, beta = _params(D)
+    h, d = _stream(T, D, "bf16"), _stream(T, D, "f32", seed=2, offset=0.0)
+    n = LayerNorm(gamma, beta, "bf16", "bf16")
+    want = n.forward(h, d)
+    cfg = B.make_norm_config(T, D, x_type="bf16", delta_type="f32", z_type="bf16")
+    got = NormOut(*[torch.empty_like(t) for t in want])
+    B.moe_norm_forward(cfg, h, d, gamma, beta, got.h, got.z, got.mean, got.rstd)
+    assert B.moe_last_launch_count() == 1
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    dz, dres = _stream(T, D, "f32", seed=4), _stream(T, D, "f32", seed=5)
+    want = n.backward(dz, got.h, got.mean, got.rstd, dres=dres)
+    out = NormGrads(*[torch.empty_like(t) for t in want])
+    ws = torch.empty(B.moe_norm_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    B.moe_norm_backward(cfg, got.h, dz, got.mean, got.rstd, gamma, dres, out.dx, out.dgamma,
+                        out.dbeta, ws, stream=s)
+    assert B.moe_last_launch_count() == 2
+    s.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
