@@ -68,11 +68,15 @@ MOE_API moe_status moe_norm_backward(const moe_norm_config* cfg, const void* h, 
 
 /* The layer of moe.h for a few tokens: the same configuration, weights and
  * routing as moe_forward (scores, groups, correction bias, shared branch and
- * capacity included), as one cooperative kernel that reads each chosen expert's
- * weights once.  x [T,D] and y [T,D] are in cfg.dtype; y must not overlap x or
+ * capacity included), as one cooperative kernel.  It reads a chosen expert's
+ * weights once for each tile of the expert's tokens (and the shared branch's once
+ * for each tile of all tokens): once for up to 16 tokens of a bf16 layer and 4 of
+ * an fp32 one, for fewer where rows are wide (9 at D = 4096, 5 at F = 4096, 2 at
+ * F = 8192).  x [T,D] and y [T,D] are in cfg.dtype; y must not overlap x or
  * a weight.  MOE_BF16 layers route with a bf16 copy of w_gate's values, as
- * moe_forward does; products are summed in fp32, hidden activations stay fp32,
- * and y is rounded once.  idx [T,k] (int32) and gate [T,k] (fp32) receive the
+ * moe_forward does; products are summed in fp32; hidden activations are fp32, of
+ * which a MOE_BF16 layer's down projection takes 16 bits, as two bf16 parts; y is
+ * rounded once.  An infinite weight gives infinities as in moe_forward.  idx [T,k] (int32) and gate [T,k] (fp32) receive the
  * routing, or are NULL.  T <= MOE_DECODE_MAX_TOKENS, a token of x at most
  * MOE_DECODE_MAX_ROW_BYTES, F and n_shared F <= MOE_DECODE_MAX_F
  * (MOE_ERR_UNSUPPORTED beyond).  aux_alpha is not

@@ -2,8 +2,11 @@
 // MLPs, shared branch, combine.
 //
 // A call of T tokens reads the weights of the at most min(E, T k) experts that
-// its tokens choose, once; for T up to some tens that is all that bounds it (a
-// multiply-add per weight and token against 2 or 4 bytes of HBM traffic).  So the
+// its tokens choose; for T up to some tens that is all that bounds it (a
+// multiply-add per weight and token against 2 or 4 bytes of HBM traffic), as long
+// as an expert's tokens fit one tile: every further tile reads its weights again
+// (8 experts, k = 2, D = 4096, 64 tokens: 437 us at F = 4096 with tiles of 5, 1570
+// at F = 8192 with tiles of 2, where the bytes alone would take 119 and 237).  So the
 // kernel is a streaming one: a cooperative grid of one block per SM, with three
 // grid barriers between the steps that depend on one another across blocks:
 //   1  logits = x W_g^T

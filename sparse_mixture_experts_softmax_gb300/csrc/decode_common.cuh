@@ -1,4 +1,4 @@
-// What the two kernels of the few-token MoE layer share: bounded waits, the grid
+// The routing half of the few-token MoE layer's kernel: bounded waits, the grid
 // barrier, the router's logits and the selection.
 //
 // A block runs most of this once and from a cold instruction cache, where the
@@ -8,8 +8,6 @@
 #pragma once
 
 #include <float.h>
-
-#include <type_traits>
 
 #include "common.cuh"
 #include "decode.h"

@@ -184,7 +184,14 @@ __device__ __forceinline__ void copy4(uint32_t dst, const T* src) {
 // costs spills or the second block of an SM.  65536 x 4096, bf16 stream with a
 // residual gradient: 559 us, 6.72 TB/s (the copy rate is 6.79); 631 us with loads
 // at the row's turn, 662 us with gamma in registers, 870 us with one block an SM.
-// W = 1 (D no multiple of 8) loads at the row's turn.
+// W = 1 (D no multiple of 8) loads at the row's turn: 5003 x 1023 fp32 with a
+// residual gradient 37 us, 3 times its bytes' time.  Above D = 8192 a block of
+// 1024 threads keeps 16 values a thread and spills: 8192 x 16384 557 us (bf16) and
+// 572 us (fp32), 2.0 and 1.8 times their bytes'.
+// dres joins before the row's correction, which rounds once more at its size
+// (65536 x 4096: 2.8e-7 from the values in 64 bits, an fp32 form that adds it last
+// 1.8e-7): kept back it would need eight more registers a thread, or its place in
+// shared memory while the next row should be loading.
 template <typename XT, int W, int V, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1024 / MAXT)
 norm_bwd_kernel(NormBwd a, int stages) {
@@ -321,6 +328,10 @@ norm_cols_kernel(const float* __restrict__ part, int nparts, int D, float* __res
   if (threadIdx.x == 0 && col < D) (w == 0 ? dgamma : dbeta)[col] = sum;
 }
 
+// SMs of the part that the library is built for.  A constant, so that the backward
+// pass's workspace and the order of its sums do not go with the device.
+constexpr int SMS = 152;
+
 // Threads per row and pieces per thread: the fewest threads that hold the row.
 struct Shape {
   int W, V, tpr, rows;   // values a piece, pieces a thread, threads a row, rows a block
@@ -351,7 +362,7 @@ static BwdShape bwd_shape(long long T, int D) {
   s.tpr = 32;
   while (s.tpr * s.W * s.V < D && s.tpr < 1024) s.tpr *= 2;
   s.rows = s.tpr < 512 ? 512 / s.tpr : 1;
-  const long long need = (T + s.rows - 1) / s.rows, most = 152LL * (s.tpr > 512 ? 1 : 2);
+  const long long need = (T + s.rows - 1) / s.rows, most = (long long)SMS * (s.tpr > 512 ? 1 : 2);
   s.blocks = (int)(need < most ? need : most);
   return s;
 }
@@ -359,9 +370,11 @@ int norm_bwd_blocks(long long T, int D) { return bwd_shape(T, D).blocks; }
 
 template <typename XT, typename ZT>
 static cudaError_t fwd_t(const NormFwd& a, cudaStream_t st) {
-  // few rows: one piece a thread, for the shortest chain; many: two, for
-  // fewer threads a row
-  const Shape s = norm_shape(a.D, a.T < 304 && a.D <= 8192 ? 1 : 2);
+  // few rows (less than two an SM): one piece a thread, for the shortest chain;
+  // many: two, for fewer threads a row.  One against two pieces, us, bf16: 1 row of
+  // 1024 2.1 / 2.5, of 4096 2.6 / 2.8, of 8192 3.3 / 3.4 (of 256 1.95 / 1.8); 4864
+  // rows of 4096 34.4 / 31.8, of 8192 72.0 / 70.2 (of 1024 9.9 / 10.2)
+  const Shape s = norm_shape(a.D, a.T < 2 * SMS && a.D <= 8192 ? 1 : 2);
   const dim3 grid((unsigned)((a.T + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
   if (s.W == 1) return launch_pdl(norm_fwd_kernel<XT, ZT, 1, 8>, grid, block, 0, st, a);
   if (s.V == 1) return launch_pdl(norm_fwd_kernel<XT, ZT, 8, 1>, grid, block, 0, st, a);
