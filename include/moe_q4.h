@@ -1,0 +1,77 @@
+/*
+ * moe_q4.h -- C ABI of 4-bit expert weights, for serving the MoE layer of moe.h:
+ *
+ *   - moe_q4_quantize / moe_q4_dequantize: weights to 4 bits with a scale for
+ *     each group of inputs, and back;
+ *   - moe_q4_product: the matrix product grouped by expert over ragged rows,
+ *     from one row (a matrix-vector product) to a batch of prompts.
+ *
+ * A 4-bit matrix of E experts, N outputs and K inputs is
+ *   codes  [E, N, K/2] bytes: 32-bit words of eight inputs each; input i of a
+ *          word's eight is in its four bits from 4 (i/2) + 16 (i%2) on;
+ *   scales [E, ceil(K/group), N] bf16: one for `group` inputs of an output, the
+ *          last group of an output ending with its inputs,
+ * and stands for the weights  w = (code - 8) scale,  code 0 to 15, rounded to bf16.
+ * Scales of up to five significant bits, such as moe_q4_quantize writes, make that
+ * rounding exact.  N is a multiple of 8, K of 32, and group is 32, 64 or 128.
+ *
+ * The conventions of moe.h hold: device pointers, 16-byte aligned, dense
+ * row-major tensors, caller-owned memory, work enqueued on `stream`, arguments
+ * checked on the host before the first launch, no floating-point atomics (the
+ * same inputs give the same bits), no host synchronisation, no allocation.
+ */
+#ifndef MOE_Q4_GB300_H
+#define MOE_Q4_GB300_H
+
+#include "moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+  const void* codes;
+  const void* scales;
+} moe_q4_matrix;
+
+/* codes and scales of w [E, N, K] (w_type: MOE_F32 or MOE_BF16).  Per group of an
+ * output, with a = max |w|:  scale is the smallest bf16 value of five significant
+ * bits that is not below a / 7, and  code = 8 + the whole number nearest to
+ * w / scale, ties to even (8 where a is 0).  Codes are 1 to 15.  A group with an
+ * infinity or a NaN gets a NaN scale, so that all of it reads as NaN. */
+MOE_API moe_status moe_q4_quantize(int32_t E, int32_t N, int32_t K, int32_t group, int32_t w_type,
+                                   const void* w, void* codes, void* scales, void* stream);
+
+/* w [E, N, K] (w_type: MOE_F32 or MOE_BF16) of a matrix: bf16 values, widened to
+ * fp32 where asked.  Codes of 0 (-8) are read too. */
+MOE_API moe_status moe_q4_dequantize(int32_t E, int32_t N, int32_t K, int32_t group, int32_t w_type,
+                                     const moe_q4_matrix* m, void* w, void* stream);
+
+#define MOE_Q4_ACT_NONE 3
+#define MOE_Q4_MAX_EXPERTS 256
+typedef struct {
+  int32_t R;           /* rows of x and c                                       */
+  int32_t E, N, K;     /* experts, outputs, inputs                              */
+  int32_t group;
+  int32_t act;         /* MOE_ACT_* or MOE_Q4_ACT_NONE                          */
+} moe_q4_product_config;
+
+/* c[r] = act(W_e x[r] + bias_e) for the rows offsets[e] <= r < offsets[e+1] of
+ * expert e, or, with MOE_ACT_SWIGLU,  c[r] = SiLU(W_e x[r]) * (W3_e x[r]).
+ * x [R, K] and c [R, N] are bf16; products are summed and act is taken in fp32,
+ * and c is rounded once.  w and w3 (NULL unless act is MOE_ACT_SWIGLU) are 4-bit
+ * matrices; bias [E, N] fp32 or NULL (NULL with MOE_ACT_SWIGLU).  offsets [E+1]
+ * (int32) lie on the device; values that decrease or leave [0, R] are clamped.
+ * Rows outside of every segment are not read and left as they are in c.  c must
+ * not overlap an input.  E <= MOE_Q4_MAX_EXPERTS, R K and R N < 2^40.
+ * dev_status (int32, device) receives MOE_ERR_TIMEOUT where a bounded device-side
+ * wait expired (c is then invalid), and is left as it is otherwise. */
+MOE_API moe_status moe_q4_product(const moe_q4_product_config* cfg, const int32_t* offsets,
+                                  const void* x, const moe_q4_matrix* w, const moe_q4_matrix* w3,
+                                  const float* bias, void* c, int32_t* dev_status, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_Q4_GB300_H */

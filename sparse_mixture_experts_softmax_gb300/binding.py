@@ -74,6 +74,14 @@ class moe_norm_config(ctypes.Structure):
                 ("z_type", c_int32), ("eps", c_float)]
 
 
+class moe_q4_matrix(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
+
+
+class moe_q4_product_config(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("R", "E", "N", "K", "group", "act")]
+
+
 class MoEError(RuntimeError):
     def __init__(self, fn: str, status: int, text: str):
         super().__init__(f"{fn}: {text} (status {status})")
@@ -187,8 +195,12 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_decode_init.argtypes = [P(moe_config), c_void_p, c_size_t, c_void_p]
     L.moe_decode.argtypes = [P(moe_config), P(moe_weights)] + [c_void_p] * 5 + [c_size_t, c_void_p]
     L.moe_decode_status.argtypes = [P(moe_config), c_void_p, c_size_t, c_void_p, c_void_p]
+    L.moe_q4_quantize.argtypes = [c_int32] * 5 + [c_void_p] * 4
+    L.moe_q4_dequantize.argtypes = [c_int32] * 5 + [P(moe_q4_matrix), c_void_p, c_void_p]
+    L.moe_q4_product.argtypes = [P(moe_q4_product_config), c_void_p, c_void_p, P(moe_q4_matrix),
+                                 P(moe_q4_matrix)] + [c_void_p] * 4
     for fn in ("moe_norm_forward", "moe_norm_backward", "moe_decode_init", "moe_decode",
-               "moe_decode_status"):
+               "moe_decode_status", "moe_q4_quantize", "moe_q4_dequantize", "moe_q4_product"):
         getattr(L, fn).restype = c_int32
     for fn in ("moe_ep_buffer_offsets", "moe_ep_get_routing", "moe_ep_route",
                "moe_ep_expert_forward",
@@ -563,3 +575,34 @@ def moe_decode_status(cfg, workspace, stream=None) -> int:
            lib().moe_decode_status(ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
                                    ctypes.addressof(out), _stream_on(stream, workspace.device)))
     return int(out.value)
+
+
+# ---- 4-bit expert weights (include/moe_q4.h)
+
+MOE_Q4_ACT_NONE = 3
+MOE_Q4_MAX_EXPERTS = 256
+Q4_ACT = dict(ACT, none=MOE_Q4_ACT_NONE)
+Q4_GROUPS = (32, 64, 128)
+
+
+def make_q4_matrix(codes, scales) -> moe_q4_matrix:
+    return moe_q4_matrix(_ptr(codes), _ptr(scales))
+
+
+def moe_q4_quantize(E, N, K, group, w_type, w, codes, scales, stream=None):
+    _check("moe_q4_quantize",
+           lib().moe_q4_quantize(int(E), int(N), int(K), int(group), DTYPE[w_type], _ptr(w),
+                                 _ptr(codes), _ptr(scales), _stream_on(stream, w.device)))
+
+
+def moe_q4_dequantize(E, N, K, group, w_type, matrix, w, stream=None):
+    _check("moe_q4_dequantize",
+           lib().moe_q4_dequantize(int(E), int(N), int(K), int(group), DTYPE[w_type],
+                                   ctypes.byref(matrix), _ptr(w), _stream_on(stream, w.device)))
+
+
+def moe_q4_product(cfg, offsets, x, w, w3, bias, c, dev_status, stream=None):
+    _check("moe_q4_product",
+           lib().moe_q4_product(ctypes.byref(cfg), _ptr(offsets), _ptr(x), ctypes.byref(w),
+                                None if w3 is None else ctypes.byref(w3), _ptr(bias), _ptr(c),
+                                _ptr(dev_status), _stream_on(stream, x.device)))

@@ -1,0 +1,185 @@
+"""4-bit expert weights, on top of the ctypes binding (``include/moe_q4.h``).
+
+``quantize`` makes a ``Q4Matrix`` of an expert matrix; ``Q4Product`` multiplies the
+rows of each expert with one.  Nothing is computed here: outputs are allocated
+through torch and the C ABI is called, on the current stream of the tensors' GPU,
+which has to be the current one.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import binding as B
+
+_TYPE = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+def _want(name, t, dtype, shape, device):
+    """Raises unless t is contiguous `dtype` of `shape` on `device`."""
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+class Q4Matrix:
+    """A 4-bit matrix [E, N, K] (N outputs, K inputs of each of E experts):
+
+    codes   uint8 [E, N, K / 2], 32-bit words of eight inputs each, input i of a word's
+            eight in its four bits from 4 (i // 2) + 16 (i % 2) on;
+    scales  bfloat16 [E, ceil(K / group), N];
+
+    it stands for the weights (code - 8) scale, rounded to bfloat16.  The tensors are
+    used in place (in the storage that they have when the object is made) and change in
+    place only."""
+
+    __slots__ = ("codes", "scales", "group", "E", "N", "K", "device", "_held")
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):
+            raise AttributeError(f"{name} is fixed when the matrix is made")
+        object.__setattr__(self, name, value)
+
+    def __init__(self, codes, scales, group):
+        if group not in B.Q4_GROUPS:
+            raise ValueError(f"group must be one of {B.Q4_GROUPS}, got {group}")
+        if codes.dim() != 3:
+            raise ValueError(f"codes must be [E, N, K / 2], got {tuple(codes.shape)}")
+        E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+        if E < 1 or N < 1 or K < 1 or N % 8 or K % 32:
+            raise ValueError(f"N must be a multiple of 8 and K of 32, got {(E, N, K)}")
+        _want("codes", codes, torch.uint8, (E, N, K // 2), codes.device)
+        _want("scales", scales, torch.bfloat16, (E, -(-K // group), N), codes.device)
+        self.codes, self.scales, self.group = codes.detach(), scales.detach(), int(group)
+        self.E, self.N, self.K, self.device = E, N, K, codes.device
+        # what c_matrix() has handed out addresses of, whatever becomes of the attributes' storage
+        self._held = codes.detach(), scales.detach()
+
+    @property
+    def shape(self):
+        return (self.E, self.N, self.K)
+
+    def c_matrix(self) -> B.moe_q4_matrix:
+        return B.make_q4_matrix(*self._held)
+
+    def dequantize(self, dtype=torch.bfloat16, out=None):
+        """The weights [E, N, K] (bfloat16 values, in float32 where asked)."""
+        if out is None:
+            out = torch.empty(self.shape, dtype=dtype, device=self.device)
+        if out.dtype not in _TYPE:
+            raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
+        _want("out", out, out.dtype, self.shape, self.device)
+        B.moe_q4_dequantize(self.E, self.N, self.K, self.group, _TYPE[out.dtype], self.c_matrix(), out)
+        return out
+
+
+def quantize(w, group=64, out=None) -> Q4Matrix:
+    """The 4-bit matrix of w [E, N, K] or [N, K] (then E is 1), float32 or bfloat16.  A
+    group's scale is the smallest value of five significant bits that is not below
+    max |w| / 7, its codes 8 + the nearest whole numbers to w / scale.  ``out``: a
+    matrix of that shape and group that is rewritten (what was made with it follows)."""
+    if w.dtype not in _TYPE:
+        raise ValueError(f"w must be float32 or bfloat16, got {w.dtype}")
+    if group not in B.Q4_GROUPS:
+        raise ValueError(f"group must be one of {B.Q4_GROUPS}, got {group}")
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    if w.dim() != 3 or w.numel() == 0 or w.shape[1] % 8 or w.shape[2] % 32:
+        raise ValueError("w must be [E, N, K] with N a multiple of 8 and K of 32, got "
+                         f"{tuple(w.shape)}")
+    E, N, K = w.shape
+    _want("w", w, w.dtype, (E, N, K), w.device)
+    if out is None:
+        out = Q4Matrix(torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device),
+                       torch.empty(E, -(-K // group), N, dtype=torch.bfloat16, device=w.device), group)
+    elif out.shape != (E, N, K) or out.group != group or out.device != w.device:
+        raise ValueError(f"out is {out.shape} with groups of {out.group} on {out.device}, w asks "
+                         f"for {(E, N, K)} with groups of {group} on {w.device}")
+    B.moe_q4_quantize(E, N, K, group, _TYPE[w.dtype], w.detach(), *out._held)
+    return out
+
+
+class Q4Product:
+    """c[r] = act(W_e x[r] + bias_e) for the rows r of each expert e, or with act
+    "swiglu"  SiLU(W_e x[r]) * (W3_e x[r]):  w (and w3) are Q4Matrix [E, N, K], bias is
+    float32 [E, N] or None, act "none", "relu", "gelu_tanh" or "swiglu".  The tensors are
+    used in place, in the storage that they have when the object is made.  Calls of one
+    object share nothing but the status word, so they may overlap on the GPU; the first
+    one has to come after the object's making, which clears that word on the current
+    stream (and so cannot be part of a graph capture)."""
+
+    _FIXED = frozenset(("shape", "device", "dev_status"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"{name} is fixed when the product is made")
+        self.__dict__[name] = value
+
+    def __init__(self, w, w3=None, bias=None, act="none"):
+        if act not in B.Q4_ACT:
+            raise ValueError(f"act must be one of {sorted(B.Q4_ACT)}, got {act!r}")
+        if (w3 is not None) != (act == "swiglu"):
+            raise ValueError("w3 goes with swiglu, and only with it")
+        if w.E > B.MOE_Q4_MAX_EXPERTS:
+            raise ValueError(f"{w.E} experts: at most {B.MOE_Q4_MAX_EXPERTS}")
+        if w3 is not None and (w3.shape != w.shape or w3.group != w.group or w3.device != w.device):
+            raise ValueError(f"w3 is {w3.shape} with groups of {w3.group} on {w3.device}, w "
+                             f"{w.shape} with groups of {w.group} on {w.device}")
+        if bias is not None:
+            if w3 is not None:
+                raise ValueError("a swiglu product has no bias")
+            _want("bias", bias, torch.float32, (w.E, w.N), w.device)
+        if w.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise ValueError("a product cannot be made while its stream is being captured")
+        self.shape, self.device = w.shape, w.device
+        self._held = w._held, None if w3 is None else w3._held, None if bias is None else bias.detach()
+        self._w = w.c_matrix()
+        self._w3 = None if w3 is None else w3.c_matrix()
+        self._refs = ctypes.byref(self._w), None if w3 is None else ctypes.byref(self._w3)
+        self._bias = None if bias is None else bias.data_ptr()
+        self._make = lambda R: B.moe_q4_product_config(R, w.E, w.N, w.K, w.group, B.Q4_ACT[act])  # noqa: E731
+        self._calls = {}
+        self.dev_status = torch.zeros(4, dtype=torch.int32, device=w.device)
+        self._status = self.dev_status.data_ptr()
+
+    def forward(self, x, offsets, out=None):
+        """c [R, N] bfloat16 of the rows x [R, K] bfloat16.  The rows of expert e are
+        offsets[e] to offsets[e + 1] - 1 (int32 [E + 1], on the GPU); values that decrease
+        or leave 0 .. R are clamped.  Rows outside of every expert's are not read and are
+        left as they are in ``out`` (undefined without one)."""
+        E, N, K = self.shape
+        shape = x.shape
+        if (len(shape) != 2 or shape[1] != K or x.dtype is not torch.bfloat16 or
+                x.device != self.device or not x.is_contiguous()):
+            raise ValueError(f"x must be contiguous bfloat16 [R, {K}] on {self.device}, got {x.dtype} "
+                             f"{tuple(shape)} on {x.device}")
+        if (offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or
+                offsets.device != self.device or not offsets.is_contiguous()):
+            raise ValueError(f"offsets must be contiguous int32 [{E + 1}] on {self.device}, got "
+                             f"{offsets.dtype} {tuple(offsets.shape)} on {offsets.device}")
+        R = shape[0]
+        if out is None:
+            out = torch.empty((R, N), dtype=torch.bfloat16, device=self.device)
+        else:
+            _want("out", out, torch.bfloat16, (R, N), self.device)
+        c = self._calls.get(R)
+        if c is None:
+            if len(self._calls) >= 64:
+                self._calls.clear()
+            cfg = self._make(R)
+            c = self._calls[R] = cfg, ctypes.byref(cfg)
+        status = B.lib().moe_q4_product(c[1], offsets.data_ptr(), x.data_ptr(), self._refs[0],
+                                        self._refs[1], self._bias, out.data_ptr(), self._status,
+                                        B._stream_on(None, self.device))
+        if status != B.MOE_OK:
+            B._check("moe_q4_product", status)
+        return out
+
+    def status(self) -> int:
+        """0, or MOE_ERR_TIMEOUT when a bounded device-side wait of a call expired (its
+        output is invalid) since the object was made.  Waits for the current stream."""
+        return int(self.dev_status[0])

@@ -1,0 +1,193 @@
+"""4-bit expert weights without a GPU: the packed layout's plain form, refusals of the
+entry points (host checks) and of the Python classes, and the structs' layout."""
+
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_mixture_experts_softmax_gb300 import binding as B
+from sparse_mixture_experts_softmax_gb300.build import INCLUDE, LIB, build_library
+from sparse_mixture_experts_softmax_gb300.q4 import Q4Matrix, Q4Product, quantize
+from tests import q4_cases as C
+
+A = 0x7f0000000000          # a fake aligned address: host checks never follow it
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(LIB):
+        build_library()
+    return B.lib()
+
+
+def test_layout_of_a_word():
+    codes = np.arange(8).reshape(1, 1, 8)
+    assert C.pack(codes).reshape(-1).tolist() == [0 | 2 << 4, 4 | 6 << 4, 1 | 3 << 4, 5 | 7 << 4]
+    rng = np.random.default_rng(0)
+    codes = rng.integers(0, 16, (2, 8, 96))
+    assert np.array_equal(C.unpack(C.pack(codes)), codes)
+
+
+@pytest.mark.parametrize("group", B.Q4_GROUPS)
+def test_quantize_definition(group):
+    w = np.random.default_rng(1).normal(0, 1, (2, 8, 160)).astype(np.float32).astype(np.float64)
+    codes, scales = C.quantize(w, group)
+    assert codes.min() >= 1 and codes.max() <= 15
+    of = np.repeat(scales, group, axis=1)[:, :160].transpose(0, 2, 1)
+    assert (np.abs(w - (codes - 8) * of) <= of / 2).all()
+    assert np.array_equal((codes - 8) * of, C.weights(codes, scales, group))     # exact in bf16
+    amax = np.stack([np.abs(w[..., g:g + group]).max(-1) for g in range(0, 160, group)], 1)
+    assert (scales >= amax / 7).all() and (scales < amax / 7 * (1 + 2.0 ** -4)).all()
+
+
+def _cfg(**kw):
+    base = dict(R=4, E=3, N=16, K=64, group=32, act=B.MOE_Q4_ACT_NONE)
+    base.update(kw)
+    return B.moe_q4_product_config(*[base[n] for n, _ in B.moe_q4_product_config._fields_])
+
+
+def _m(codes=A, scales=A):
+    return ctypes.byref(B.moe_q4_matrix(codes, scales))
+
+
+def _call(L, cfg, off=A, x=A, w=True, w3=None, bias=None, c=A, status=A):
+    return L.moe_q4_product(None if cfg is None else ctypes.byref(cfg), off, x,
+                            _m() if w is True else w, w3, bias, c, status, None)
+
+
+@pytest.mark.parametrize("kw", [dict(N=12), dict(K=48), dict(group=16), dict(group=0), dict(group=48),
+                                dict(E=257), dict(N=1 << 28, K=1 << 12), dict(E=256, N=1 << 23),
+                                dict(R=2**31 - 1, K=1 << 12), dict(R=2**31 - 1, N=1 << 12)])
+def test_product_unsupported(L, kw):
+    assert _call(L, _cfg(**kw)) == B.MOE_ERR_UNSUPPORTED
+
+
+def test_product_invalid(L):
+    bad = B.MOE_ERR_INVALID_ARG
+    assert _call(L, None) == bad
+    for kw in (dict(R=-1), dict(E=0), dict(N=0), dict(K=0), dict(N=-8), dict(act=-1), dict(act=4)):
+        assert _call(L, _cfg(**kw)) == bad
+    for kw in (dict(off=None), dict(x=None), dict(w=None), dict(c=None), dict(status=None),
+               dict(w=_m(codes=None)), dict(w=_m(scales=None)), dict(w3=_m())):
+        assert _call(L, _cfg(), **kw) == bad
+    swiglu = _cfg(act=B.ACT["swiglu"])
+    assert _call(L, swiglu) == bad
+    assert _call(L, swiglu, w3=_m(codes=None)) == bad
+    assert _call(L, swiglu, w3=_m(), bias=A) == bad
+
+
+def test_product_alignment(L):
+    for kw in (dict(off=A + 4), dict(x=A + 8), dict(c=A + 2), dict(status=A + 4), dict(bias=A + 4),
+               dict(w=_m(codes=A + 4)), dict(w=_m(scales=A + 2))):
+        assert _call(L, _cfg(), **kw) == B.MOE_ERR_ALIGNMENT
+    assert _call(L, _cfg(act=B.ACT["swiglu"]), w3=_m(scales=A + 8)) == B.MOE_ERR_ALIGNMENT
+
+
+def test_pack_refusals(L):
+    for fn in (lambda E, N, K, G, t, w, c, s: L.moe_q4_quantize(E, N, K, G, t, w, c, s, None),
+               lambda E, N, K, G, t, w, c, s: L.moe_q4_dequantize(E, N, K, G, t, _m(c, s), w, None)):
+        for args, want in [((0, 8, 32, 32, 0), 1), ((1, -8, 32, 32, 0), 1), ((1, 8, 0, 32, 0), 1),
+                           ((1, 8, 32, 32, 2), 1), ((1, 8, 32, 32, -1), 1), ((1, 12, 32, 32, 0), 2),
+                           ((1, 8, 40, 32, 0), 2), ((1, 8, 32, 40, 0), 2), ((1 << 20, 1 << 12, 32, 32, 0), 2),
+                           ((1 << 10, 1 << 15, 1 << 16, 32, 0), 2)]:
+            assert fn(*args, A, A, A) == want, args
+        ok = (1, 8, 32, 32, 1)
+        for i in range(3):
+            ptrs = [A, A, A]
+            ptrs[i] = None
+            assert fn(*ok, *ptrs) == B.MOE_ERR_INVALID_ARG
+            ptrs[i] = A + 8
+            assert fn(*ok, *ptrs) == B.MOE_ERR_ALIGNMENT
+    assert L.moe_q4_dequantize(1, 8, 32, 32, 1, None, A, None) == B.MOE_ERR_INVALID_ARG
+
+
+def test_struct_layout(tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    structs = {n: getattr(B, n) for n in dir(B) if n.startswith("moe_q4_") and
+               isinstance(getattr(B, n), type) and issubclass(getattr(B, n), ctypes.Structure)}
+    assert structs
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "moe_q4.h"', 'int main(void) {']
+    for name, cls in structs.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    lines += ['printf("%d\\n%d\\n", MOE_Q4_ACT_NONE, MOE_Q4_MAX_EXPERTS);', 'return 0; }']
+    (tmp_path / "p.c").write_text("\n".join(lines))
+    subprocess.run([cc, "-I", INCLUDE, str(tmp_path / "p.c"), "-o", str(tmp_path / "p")], check=True)
+    got = [int(v) for v in subprocess.run([str(tmp_path / "p")], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    want = []
+    for cls in structs.values():
+        want.append(ctypes.sizeof(cls))
+        want += [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want + [B.MOE_Q4_ACT_NONE, B.MOE_Q4_MAX_EXPERTS]
+
+
+# ---- the Python classes
+
+def _matrix(E=2, N=16, K=64, group=32):
+    return Q4Matrix(torch.zeros(E, N, K // 2, dtype=torch.uint8),
+                    torch.zeros(E, -(-K // group), N, dtype=torch.bfloat16), group)
+
+
+def test_matrix_refusals():
+    m = _matrix()
+    assert m.shape == (2, 16, 64) and m.device.type == "cpu"
+    codes, scales = m.codes, m.scales
+    for c, s, g in [(codes, scales, 48), (codes[0], scales, 32), (codes.int(), scales, 32),
+                    (codes, scales.float(), 32), (codes, scales, 64), (codes[:, :, :24], scales, 32),
+                    (codes[:, :12].contiguous(), scales, 32), (codes.transpose(0, 1), scales, 32),
+                    (codes, scales.transpose(1, 2).contiguous().transpose(1, 2), 32),
+                    (codes[:0], scales[:0], 32), (codes.to("meta"), scales, 32)]:
+        with pytest.raises(ValueError):
+            Q4Matrix(c, s, g)
+    with pytest.raises(AttributeError):
+        m.codes = codes
+    with pytest.raises(AttributeError):
+        m.group = 64
+
+
+def test_quantize_refusals():
+    for w, kw in [(torch.zeros(8, 32, dtype=torch.float16), {}), (torch.zeros(8, 40), {}),
+                  (torch.zeros(12, 32), {}), (torch.zeros(32), {}), (torch.zeros(0, 8, 32), {}),
+                  (torch.zeros(8, 32), dict(group=16)), (torch.zeros(32, 8).t(), {}),
+                  (torch.zeros(8, 32), dict(out=_matrix())),
+                  (torch.zeros(2, 16, 64), dict(group=64, out=_matrix()))]:
+        with pytest.raises(ValueError):
+            quantize(w, **kw)
+    with pytest.raises(ValueError, match="GPU"):        # a CPU tensor never reaches the library
+        quantize(torch.zeros(8, 32))
+    with pytest.raises(ValueError, match="GPU"):
+        _matrix().dequantize()
+    with pytest.raises(ValueError):
+        _matrix().dequantize(torch.float16)
+    with pytest.raises(ValueError):
+        _matrix().dequantize(out=torch.zeros(2, 16, 32))
+
+
+def test_product_class_refusals():
+    m = _matrix()
+    for args, kw in [((m,), dict(act="silu")), ((m, m), dict(act="none")), ((m,), dict(act="swiglu")),
+                     ((m, _matrix(N=24)), dict(act="swiglu")), ((m, _matrix(group=64)), dict(act="swiglu")),
+                     ((_matrix(E=257),), {}), ((m, m), dict(act="swiglu", bias=torch.zeros(2, 16))),
+                     ((m,), dict(bias=torch.zeros(2, 8))), ((m,), dict(bias=torch.zeros(2, 16).double()))]:
+        with pytest.raises(ValueError):
+            Q4Product(*args, **kw)
+    p = Q4Product(m, bias=torch.zeros(2, 16), act="relu")
+    x, off = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for xx, oo, out in [(x.float(), off, None), (x[:, :32], off, None), (x, off[:2], None),
+                        (x, off.long(), None), (x[0], off, None), (x, off, torch.zeros(4, 16)),
+                        (x, off, torch.zeros(5, 16, dtype=torch.bfloat16)),
+                        (torch.zeros(4, 128, dtype=torch.bfloat16)[:, ::2], off, None)]:
+        with pytest.raises(ValueError):
+            p.forward(xx, oo, out)
+    with pytest.raises(ValueError, match="GPU"):
+        p.forward(x, off)
+    with pytest.raises(AttributeError):
+        p.shape = (1, 2, 3)
