@@ -4,7 +4,9 @@
  *   - moe_q4_quantize / moe_q4_dequantize: weights to 4 bits with a scale for
  *     each group of inputs, and back;
  *   - moe_q4_product: the matrix product grouped by expert over ragged rows,
- *     from one row (a matrix-vector product) to a batch of prompts.
+ *     from one row (a matrix-vector product) to a batch of prompts;
+ *   - moe_q4_decode: moe_decode (moe_block.h) on 4-bit expert weights;
+ *   - moe_q4_forward: moe_forward on 4-bit expert weights.
  *
  * A 4-bit matrix of E experts, N outputs and K inputs is
  *   codes  [E, N, K/2] bytes: 32-bit words of eight inputs each; input i of a
@@ -69,6 +71,37 @@ typedef struct {
 MOE_API moe_status moe_q4_product(const moe_q4_product_config* cfg, const int32_t* offsets,
                                   const void* x, const moe_q4_matrix* w, const moe_q4_matrix* w3,
                                   const float* bias, void* c, int32_t* dev_status, void* stream);
+
+/* The weights of a layer whose expert matrices are 4-bit ones: as in moe_weights
+ * (w1, w3 and ws1, ws3 [E, F, D] and [1, n_shared F, D], w2 and ws2 [E, D, F] and
+ * [1, D, n_shared F]), w3 and the shared branch's being ignored where the layer has
+ * none.  The layer's cfg.dtype is MOE_BF16, D and F multiples of 32
+ * (MOE_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  const float* w_gate;
+  moe_q4_matrix w1, w3, w2;
+  const float *b1, *b2, *logit_bias, *corr_bias;
+  moe_q4_matrix ws1, ws3, ws2;
+  int32_t group;
+} moe_q4_weights;
+
+/* moe_decode with those weights: the same arguments, limits, workspace
+ * (moe_decode_workspace_size, moe_decode_init, moe_decode_status) and precision. */
+MOE_API moe_status moe_q4_decode(const moe_config* cfg, const moe_q4_weights* w, const void* x,
+                                 void* y, int32_t* idx, float* gate, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* moe_forward with those weights, for any T, in a workspace of its own (its size
+ * grows with T: one made for the most tokens serves every call): x [T, D] bf16,
+ * y [T, D] fp32, which must not overlap x or a weight.  Hidden activations and the experts' outputs are rounded to
+ * bf16, as in moe_forward.  moe_q4_status reads the last call's device status: 0,
+ * or MOE_ERR_TIMEOUT when a bounded device-side wait expired (y is then invalid).
+ * It synchronises `stream`. */
+MOE_API size_t moe_q4_workspace_size(const moe_config* cfg);
+MOE_API moe_status moe_q4_forward(const moe_config* cfg, const moe_q4_weights* w, const void* x,
+                                  float* y, void* workspace, size_t workspace_bytes, void* stream);
+MOE_API moe_status moe_q4_status(const moe_config* cfg, const void* workspace,
+                                 size_t workspace_bytes, int32_t* status_host, void* stream);
 
 #ifdef __cplusplus
 }

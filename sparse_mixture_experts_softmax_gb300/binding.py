@@ -82,6 +82,12 @@ class moe_q4_product_config(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in ("R", "E", "N", "K", "group", "act")]
 
 
+class moe_q4_weights(ctypes.Structure):
+    _fields_ = [("w_gate", c_void_p)] + [(n, moe_q4_matrix) for n in ("w1", "w3", "w2")] + \
+        [(n, c_void_p) for n in ("b1", "b2", "logit_bias", "corr_bias")] + \
+        [(n, moe_q4_matrix) for n in ("ws1", "ws3", "ws2")] + [("group", c_int32)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, fn: str, status: int, text: str):
         super().__init__(f"{fn}: {text} (status {status})")
@@ -199,8 +205,16 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_q4_dequantize.argtypes = [c_int32] * 5 + [P(moe_q4_matrix), c_void_p, c_void_p]
     L.moe_q4_product.argtypes = [P(moe_q4_product_config), c_void_p, c_void_p, P(moe_q4_matrix),
                                  P(moe_q4_matrix)] + [c_void_p] * 4
+    L.moe_q4_decode.argtypes = [P(moe_config), P(moe_q4_weights)] + [c_void_p] * 5 + [c_size_t,
+                                                                                      c_void_p]
+    L.moe_q4_workspace_size.argtypes = [P(moe_config)]
+    L.moe_q4_workspace_size.restype = c_size_t
+    L.moe_q4_forward.argtypes = [P(moe_config), P(moe_q4_weights)] + [c_void_p] * 3 + [c_size_t,
+                                                                                       c_void_p]
+    L.moe_q4_status.argtypes = [P(moe_config), c_void_p, c_size_t, c_void_p, c_void_p]
     for fn in ("moe_norm_forward", "moe_norm_backward", "moe_decode_init", "moe_decode",
-               "moe_decode_status", "moe_q4_quantize", "moe_q4_dequantize", "moe_q4_product"):
+               "moe_decode_status", "moe_q4_quantize", "moe_q4_dequantize", "moe_q4_product",
+               "moe_q4_decode", "moe_q4_forward", "moe_q4_status"):
         getattr(L, fn).restype = c_int32
     for fn in ("moe_ep_buffer_offsets", "moe_ep_get_routing", "moe_ep_route",
                "moe_ep_expert_forward",
@@ -606,3 +620,36 @@ def moe_q4_product(cfg, offsets, x, w, w3, bias, c, dev_status, stream=None):
            lib().moe_q4_product(ctypes.byref(cfg), _ptr(offsets), _ptr(x), ctypes.byref(w),
                                 None if w3 is None else ctypes.byref(w3), _ptr(bias), _ptr(c),
                                 _ptr(dev_status), _stream_on(stream, x.device)))
+
+
+def make_q4_weights(w_gate, group, w1, w2, w3=None, b1=None, b2=None, logit_bias=None,
+                    corr_bias=None, ws1=None, ws3=None, ws2=None) -> moe_q4_weights:
+    """w1, w2, w3, ws1, ws3, ws2: moe_q4_matrix or None."""
+    m = lambda q: moe_q4_matrix() if q is None else q  # noqa: E731
+    return moe_q4_weights(_ptr(w_gate), m(w1), m(w3), m(w2), _ptr(b1), _ptr(b2), _ptr(logit_bias),
+                          _ptr(corr_bias), m(ws1), m(ws3), m(ws2), int(group))
+
+
+def moe_q4_decode(cfg, weights, x, y, workspace, idx=None, gate=None, stream=None):
+    _check("moe_q4_decode",
+           lib().moe_q4_decode(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(y), _ptr(idx),
+                               _ptr(gate), _ptr(workspace), workspace.numel(),
+                               _stream_on(stream, x.device)))
+
+
+def moe_q4_workspace_size(cfg) -> int:
+    return int(lib().moe_q4_workspace_size(ctypes.byref(cfg)))
+
+
+def moe_q4_forward(cfg, weights, x, y, workspace, stream=None):
+    _check("moe_q4_forward",
+           lib().moe_q4_forward(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(y),
+                                _ptr(workspace), workspace.numel(), _stream_on(stream, x.device)))
+
+
+def moe_q4_status(cfg, workspace, stream=None) -> int:
+    out = ctypes.c_int32(0)
+    _check("moe_q4_status",
+           lib().moe_q4_status(ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
+                               ctypes.addressof(out), _stream_on(stream, workspace.device)))
+    return int(out.value)

@@ -5,7 +5,8 @@ The sum h' + y is left to whoever comes next: a following block takes ``y`` as
 its ``delta`` and adds it inside its own norm, so a stack of blocks never makes a
 pass over the stream for it.  ``MoEBlock`` owns nothing but the pieces it is
 given (``norm.LayerNorm``, ``layer.MoELayer`` and, for serving,
-``decode.MoEDecoder``) and computes nothing itself.
+``decode.MoEDecoder``) and computes nothing itself.  ``Q4Block`` is the block on 4-bit
+expert weights, for serving.
 """
 
 from __future__ import annotations
@@ -18,6 +19,7 @@ from . import binding as B
 from .decode import MoEDecoder
 from .layer import MoELayer
 from .norm import LayerNorm
+from .q4_layer import Q4Layer
 
 
 class BlockState(NamedTuple):
@@ -101,3 +103,30 @@ class MoEBlock:
         d = self.decoder
         r = self.norm.forward(h, delta, stats=False)
         return h if r.h is None else r.h, d.decode(r.z)
+
+
+class Q4Block:
+    """The block around a layer of 4-bit expert weights: prompts by ``forward``, a few
+    tokens by ``decode``, (h', y) from both as from a MoEBlock."""
+
+    def __init__(self, norm: LayerNorm, layer: Q4Layer):
+        if norm.D != layer.D:
+            raise ValueError(f"the norm has {norm.D} channels, the layer {layer.D}")
+        if norm.z_type != torch.bfloat16:
+            raise ValueError(f"the norm writes {norm.z_type}, the layer reads bfloat16")
+        if norm.device != layer.device:
+            raise ValueError(f"the norm is on {norm.device}, the layer on {layer.device}")
+        self.norm, self.layer = norm, layer
+
+    def forward(self, h, delta=None):
+        """h' = h + delta (h without one) and y [T, D] fp32, for up to the layer's
+        max_tokens rows.  h' of up to 64 rows is a buffer of this block, which its next
+        call overwrites."""
+        r = self.norm.forward(h, delta, stats=False)
+        return h if r.h is None else r.h, self.layer.forward(r.z)
+
+    def decode(self, h, delta=None):
+        """The same for a few tokens; y is in bf16.  Both are buffers of this block,
+        which its next call overwrites."""
+        r = self.norm.forward(h, delta, stats=False)
+        return h if r.h is None else r.h, self.layer.decode(r.z)

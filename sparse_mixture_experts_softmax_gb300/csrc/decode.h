@@ -21,6 +21,9 @@ struct DecodeArgs {
   const void *w1, *w3, *w2;
   const float *b1, *b2, *logit_bias, *corr_bias;
   const void *ws1, *ws3, *ws2;
+  // 4-bit weights: scales beside the codes above, log2 of a group's inputs
+  const void *s1, *s3, *s2, *ss1, *ss3, *ss2;
+  int log_g;
   void* y;                     // [T, D] in the layer's type
   int* idx;                    // [T, k] or nullptr
   float* gate;                 // [T, k] or nullptr
@@ -33,6 +36,7 @@ struct DecodeArgs {
 
 // Writes the control words of a workspace that no call has used yet.
 cudaError_t launch_decode_init(int* ctl, cudaStream_t st);
-cudaError_t launch_decode(int dtype, const DecodeArgs& a, cudaStream_t st);
+enum { DECODE_F32 = 0, DECODE_BF16 = 1, DECODE_Q4 = 2 };       // kinds of expert weights
+cudaError_t launch_decode(int kind, const DecodeArgs& a, cudaStream_t st);
 
 }  // namespace moe

@@ -22,7 +22,7 @@ cudaError_t launch_q4_dequantize(int type, const Q4Shape& s, const void* codes, 
 struct Q4Product {
   int R, E, N, K, G;
   int act;                     // 0 relu, 1 gelu_tanh, 2 swiglu, 3 none
-  const int* offsets;          // [E + 1]
+  const int* offsets;          // [E + 1], or nullptr: one segment of R rows
   const void* x;               // [R, K] bf16
   const void *codes, *scales, *codes3, *scales3;
   const float* bias;           // [E, N] or nullptr

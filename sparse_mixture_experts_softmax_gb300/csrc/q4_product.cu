@@ -22,9 +22,9 @@ __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4Product p) {
   const int r = blockIdx.x / blocks_n, n0 = (blockIdx.x % blocks_n) * 64 + warp * 8;
   pdl_begin();
   if (threadIdx.x == 0) {
-    int prev = min(max(p.offsets[0], 0), p.R);
-    expert = -1;
-    for (int e = 0; e < p.E; ++e) {
+    int prev = p.offsets ? min(max(p.offsets[0], 0), p.R) : 0;
+    expert = p.offsets ? -1 : 0;
+    for (int e = 0; p.offsets && e < p.E; ++e) {
       const int hi = min(max(p.offsets[e + 1], prev), p.R);
       if (r >= prev && r < hi) { expert = e; break; }
       prev = hi;

@@ -12,6 +12,7 @@ import ctypes
 import torch
 
 from . import binding as B
+from .q4 import Q4Matrix
 
 _DTYPE = {torch.float32: "f32", torch.bfloat16: "bf16"}
 
@@ -19,7 +20,9 @@ _DTYPE = {torch.float32: "f32", torch.bfloat16: "bf16"}
 class MoEDecoder:
     """w_gate [E,D] fp32; w1, w3 [E,F,D], w2 [E,D,F] and the shared branch ws1,
     ws3, ws2 in the layer's type (float32 or bfloat16); b1 [E,F], b2 [E,D],
-    logit_bias [E], corr_bias [E] fp32 or None.  The tensors are used in place (in
+    logit_bias [E], corr_bias [E] fp32 or None.  Or all of w1, w3, w2, ws1, ws3, ws2 as
+    Q4Matrix ([1, n_shared F, D] and [1, D, n_shared F] for the shared branch), of one
+    group, in a bfloat16 layer (``moe_q4_decode``).  The tensors are used in place (in
     the storage that they have when the decoder is made), so the decoder follows
     a layer that is still being trained.  Calls run on the current stream of
     their GPU, which has to be the current one; those of one decoder share its
@@ -39,9 +42,10 @@ class MoEDecoder:
                  score="softmax", n_groups=1, topk_groups=1, group_score="top2_sum",
                  logit_bias=None, corr_bias=None, n_shared=0, ws1=None, ws3=None, ws2=None,
                  capacity_factor=0.0, max_tokens=B.MOE_DECODE_MAX_TOKENS):
-        if w1.dtype not in _DTYPE:
-            raise ValueError(f"w1 must be float32 or bfloat16, got {w1.dtype}")
-        if w1.dim() != 3:
+        q4 = isinstance(w1, Q4Matrix)
+        if not q4 and w1.dtype not in _DTYPE:
+            raise ValueError(f"w1 must be float32, bfloat16 or a Q4Matrix, got {w1.dtype}")
+        if len(w1.shape) != 3:
             raise ValueError(f"w1 must be [E, F, D], got {tuple(w1.shape)}")
         E, F, D = w1.shape
         Fs = int(n_shared) * F
@@ -51,19 +55,28 @@ class MoEDecoder:
             raise ValueError("b1 and b2 come together")
         if not 1 <= max_tokens <= B.MOE_DECODE_MAX_TOKENS:
             raise ValueError(f"max_tokens must be 1 to {B.MOE_DECODE_MAX_TOKENS}")
-        f32, dt = torch.float32, w1.dtype
+        f32, dt = torch.float32, torch.bfloat16 if q4 else w1.dtype
+        one = (1,) if q4 else ()
         want = dict(w_gate=(w_gate, f32, (E, D)), w1=(w1, dt, (E, F, D)), w2=(w2, dt, (E, D, F)),
                     w3=(w3, dt, (E, F, D)), b1=(b1, f32, (E, F)), b2=(b2, f32, (E, D)),
                     logit_bias=(logit_bias, f32, (E,)), corr_bias=(corr_bias, f32, (E,)),
-                    ws1=(ws1, dt, (Fs, D)), ws3=(ws3, dt, (Fs, D)), ws2=(ws2, dt, (D, Fs)))
+                    ws1=(ws1, dt, one + (Fs, D)), ws3=(ws3, dt, one + (Fs, D)),
+                    ws2=(ws2, dt, one + (D, Fs)))
+        matrices = {}
         for name, (t, dtype, shape) in want.items():
             if name.startswith("ws") and (t is not None) != (n_shared > 0):
                 raise ValueError("ws1, ws3 and ws2 go with n_shared > 0")
             if t is None:
                 continue
-            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            if q4 and dtype is dt:
+                if not isinstance(t, Q4Matrix) or t.shape != shape or t.group != w1.group:
+                    raise ValueError(f"{name} must be a Q4Matrix of shape {shape} with groups of "
+                                     f"{w1.group}, like w1")
+                matrices[name] = t
+            elif (isinstance(t, Q4Matrix) or t.dtype != dtype or tuple(t.shape) != shape or
+                  not t.is_contiguous()):
                 raise ValueError(f"{name} must be contiguous {dtype} of shape {shape}, got "
-                                 f"{t.dtype} {tuple(t.shape)}")
+                                 f"{getattr(t, 'dtype', 'a Q4Matrix')} {tuple(t.shape)}")
             if t.device != w1.device:
                 raise ValueError(f"{name} is on {t.device}, w1 on {w1.device}")
         if w1.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
@@ -75,9 +88,17 @@ class MoEDecoder:
             group_score=group_score, dtype=_DTYPE[dt], has_bias=b1 is not None,
             n_shared=n_shared, capacity_factor=capacity_factor)
         # that storage stays alive as long as the decoder does, even if a parameter's is replaced
-        self._hold = [t.detach() for t, _, _ in want.values() if t is not None]
-        self._weights = B.make_weights(w_gate, w1, w2, w3, b1, b2, logit_bias, corr_bias, ws1,
-                                       ws3, ws2)
+        self._hold = [t._held if isinstance(t, Q4Matrix) else t.detach()
+                      for t, _, _ in want.values() if t is not None]
+        if q4:
+            self._entry = "moe_q4_decode"
+            self._weights = B.make_q4_weights(w_gate, w1.group, b1=b1, b2=b2, logit_bias=logit_bias,
+                                              corr_bias=corr_bias,
+                                              **{n: m.c_matrix() for n, m in matrices.items()})
+        else:
+            self._entry = "moe_decode"
+            self._weights = B.make_weights(w_gate, w1, w2, w3, b1, b2, logit_bias, corr_bias, ws1,
+                                           ws3, ws2)
         self._weights_ref = ctypes.byref(self._weights)
         self._calls = {}
         self.cfg = self._make(self.max_tokens)
@@ -123,10 +144,10 @@ class MoEDecoder:
                 raise ValueError(f"y must be contiguous {self.dtype} {tuple(shape)} on "
                                  f"{self.device}")
             yp = y.data_ptr()
-        status = B.lib().moe_decode(c[1], self._weights_ref, x.data_ptr(), yp, c[6], c[7], c[8],
-                                    c[9], B._stream_on(None, self.device))
+        status = getattr(B.lib(), self._entry)(c[1], self._weights_ref, x.data_ptr(), yp, c[6],
+                                               c[7], c[8], c[9], B._stream_on(None, self.device))
         if status != B.MOE_OK:
-            B._check("moe_decode", status)
+            B._check(self._entry, status)
         self.__dict__.update(idx=c[3], gate=c[4])      # (without __setattr__'s look-up)
         return y
 
