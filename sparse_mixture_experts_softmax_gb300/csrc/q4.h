@@ -30,5 +30,7 @@ struct Q4Product {
   int* status;
 };
 cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st);
+// The kernel for many rows (q4_gemm.cu).
+cudaError_t launch_q4_gemm(const Q4Product& p, cudaStream_t st);
 
 }  // namespace moe

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4Product p) {
 }  // namespace
 
 cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st) {
+  if (p.R > 16) return launch_q4_gemm(p, st);
   return launch_pdl(q4_rows_kernel, dim3((unsigned)p.R * ((p.N + 63) / 64)), dim3(256), 0, st, p);
 }
 
