@@ -234,11 +234,10 @@ __device__ __forceinline__ uint4 load_rows(uint32_t at) {
   return v;
 }
 
-// A scale in both halves of a word.
 __device__ __forceinline__ uint32_t load_scale(uint32_t at) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return v | (uint32_t)v << 16;
+  return v;
 }
 
 // One output pair of an item: rows r and r + 8 of the 16, token `tok` of the
@@ -375,11 +374,12 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP> {
       const uint32_t wat = (from + g * PIECE + u * 64 + c * 16) ^ ((g & 1) << 6);
       const uint4 w0 = load_rows(wat), w1 = load_rows(wat + 8 * PIECE);
       const uint32_t sat = slab + ((u * 128 + c * 32) >> p.log_g) * 32;
-      const uint32_t s0 = load_scale(sat), s1 = load_scale(sat + 16);
-      const uint32_t r0[4] = {w0.x, w0.y, w0.z, w0.w}, r1[4] = {w1.x, w1.y, w1.z, w1.w};
+      uint4 r0[4], r1[4];
+      q4_words(w0, q4_scale(load_scale(sat)), r0);
+      q4_words(w1, q4_scale(load_scale(sat + 16)), r1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 a = q4_word(r0[j], s0), b = q4_word(r1[j], s1);
+        const uint4 a = r0[j], b = r1[j];
         auto products = [&](float (&c0)[4], float (&c1)[4], uint32_t x_at) {
           const uint4 x = load_rows(x_at);
           mma16816(c0, a.x, b.x, a.y, b.y, x.x, x.y);

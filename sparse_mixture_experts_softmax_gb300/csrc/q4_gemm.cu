@@ -3,23 +3,24 @@
 //
 //   c[r, f] = act(sum_k w_e[f, k] x[r, k] + bias_e[f])     rows r of expert e
 //
-// A tile is 128 outputs by up to BN rows of one expert (64 outputs of W and the same
-// of W3 for SwiGLU): the outputs are the lanes of the accumulator, the rows its
-// columns, so that a tile of few rows wastes no more than the narrow side of the
-// instruction (its N is the rows rounded up to 16) and one of many rows reads the
-// weights, which have to be widened, once for up to 256 rows.
+// A tile is 128 outputs by up to bn rows of one expert (64 outputs of W and the same of
+// W3 for SwiGLU): the outputs are the lanes of the accumulator, the rows its columns,
+// so that a tile of few rows wastes no more than the narrow side of the instruction (its
+// N is the rows rounded up to 16).  The widened weights are the A operand, which lies in
+// tensor memory beside the two accumulators: a lane is an output, and a thread writes 64
+// of its inputs with one instruction.
 //
 // One persistent block an SM, its warps specialised:
 //   warp 0       codes and scales by bulk-tensor copies, 128 inputs at a time;
 //   warp 1       the matrix instructions (and the tensor memory);
 //   warps 2..5   the epilogue: a lane an output, column by column;
-//   warp 6       the rows of x by bulk-tensor copies, 64 inputs at a time;
-//   warps 7..14  4-bit to bf16: a thread 32 inputs of an output, written in the
-//                128-byte swizzle that the instructions read.
+//   warp 6       the rows of x by bulk-tensor copies, 128 inputs at a time;
+//   warps 7..    4-bit to bf16, in groups of four warps that take 64 inputs in turn.
 // Two accumulators let a tile's epilogue run beside the next one's products.
 // Every wait is bounded (2 s); when one expires the block raises an abort flag and
 // the status word, waits for its copies and products in flight, frees its tensor
 // memory and returns.
+#include <cstdlib>
 #include "q4.cuh"
 #include "q4.h"
 #include "tc_ptx.cuh"
@@ -30,29 +31,41 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, BK = 64, UK = 16, RAW_K = 128;
-constexpr int A_BYTES = BM * BK * 2;                     // 16 KB
 constexpr int CODE_BYTES = BM * RAW_K / 2;               // 8 KB
 constexpr int RAW_BYTES = CODE_BYTES + BM * (RAW_K / 32) * 2;   // + the scales, up to 1 KB
-constexpr int X_BOX = 64;                                // rows of a copy of x
-constexpr int W_RAW = 0, W_MMA = 1, W_EPI = 2, W_X = 6, W_WIDEN = 7, N_WIDEN = 8;
+// Heights of a copy of x: the least that has a tile's rows.
+constexpr int X_BOXES = 8;
+__host__ __device__ constexpr int box_rows(int i) { return i < 4 ? 16 * (i + 1) : 32 * (i - 1); }
+__host__ __device__ constexpr int box_of(int rows) { return rows <= 64 ? (rows - 1) / 16 : (rows - 1) / 32 + 2; }
+static_assert(box_rows(0) == 16 && box_rows(3) == 64 && box_rows(4) == 96 && box_rows(7) == 192, "heights");
+static_assert(box_of(1) == 0 && box_of(64) == 3 && box_of(65) == 4 && box_of(96) == 4 && box_of(97) == 5 &&
+              box_of(192) == 7, "heights");
+constexpr int W_RAW = 0, W_MMA = 1, W_EPI = 2, W_X = 6, W_WIDEN = 7, NG = 4, N_WIDEN = 4 * NG;
 constexpr int THREADS = 32 * (W_WIDEN + N_WIDEN);
 constexpr int MAX_E = 256;
 constexpr int TMEM_COLS = 512;
 constexpr long long LIMIT_NS = 2000000000ll;
 
-// Operand stages (64 inputs) and raw stages (128 inputs) by the rows of a tile.
-template <int BN> struct Ring;
-template <> struct Ring<256> { static constexpr int S = 4, Q = 3; };
-template <> struct Ring<128> { static constexpr int S = 4, Q = 10; };
-template <> struct Ring<64> { static constexpr int S = 5, Q = 10; };
-template <int BN> constexpr int kStage = A_BYTES + BN * BK * 2;
-template <int BN> constexpr int kSmem = Ring<BN>::S * kStage<BN> + Ring<BN>::Q * RAW_BYTES;
-static_assert(kSmem<256> + 4096 <= 232448 && kSmem<128> + 4096 <= 232448 && kSmem<64> + 4096 <= 232448,
-              "shared memory of one block");
+// Stages, each of 128 inputs: Q of codes and scales, SA of widened weights, SX of rows.
+// The accumulators take 2 bn of the 512 columns, a stage of weights 64; a stage of rows
+// 256 bn bytes.  The groups of widening warps run apart from one another, and copies do
+// not land in the order of their issue: a group may only wait on stages whose every use
+// is its own (a barrier tells no more than the parity of its phase).  So a pair of
+// groups shares a stage, 64 inputs each, and Q and SA are multiples of the pairs.  Of a
+// tile's last stage, where it has 64 inputs or less, the second half is without work.
+constexpr int Q = 8, X_RING = 144 * 1024, MAX_SA = 6, MAX_SX = 8;
+constexpr int SMEM = X_RING + Q * RAW_BYTES;
+__host__ __device__ constexpr int stages_a(int bn) { return (TMEM_COLS - 2 * bn) / 64; }
+__host__ __device__ constexpr int stages_x(int bn) {
+  return X_RING / (bn * 256) < MAX_SX ? X_RING / (bn * 256) : MAX_SX;
+}
+static_assert(Q % (NG / 2) == 0 && stages_a(192) == 2 && stages_a(128) == 4 && stages_a(64) == 6,
+              "stages of one pair");
+static_assert(SMEM + 5120 <= 232448, "shared memory of one block");
 
 struct Params {
   int R, E, N, K, log_g;
-  int act;
+  int act, bn;
   int nF, per;                 // tiles along the outputs, outputs of a tile
   const int* offsets;
   const float* bias;
@@ -60,10 +73,14 @@ struct Params {
   int* status;
 };
 
+struct XMaps {
+  CUtensorMap box[X_BOXES];
+};
+
 // Row tiles of the experts: first tile and rows of a tile by expert.
 struct Table {
   int offs[MAX_E + 1], first[MAX_E + 1], step[MAX_E];
-  int scan[2][16];
+  int scan[2][32];
 };
 struct Tile {
   int e, r0, n, f0;
@@ -102,7 +119,6 @@ __device__ __forceinline__ int block_scan(int v, int* part) {
 // Offsets clamped to a sequence that does not decrease within [0, R], and the row tiles:
 // an expert's rows in tiles of equal size, a multiple of 16, so that none is much
 // smaller than the others.
-template <int BN>
 __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
   const int e = threadIdx.x;
   int v = 0;
@@ -113,7 +129,7 @@ __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
   int tiles = 0;
   if (e < p.E) {
     const int rows = tb.offs[e + 1] - v;
-    const int least = (rows + BN - 1) / BN;
+    const int least = (rows + p.bn - 1) / p.bn;
     const int step = rows ? ((rows + least - 1) / least + 15) & ~15 : 16;
     tiles = (rows + step - 1) / step;
     tb.step[e] = step;
@@ -122,6 +138,31 @@ __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
   if (e < p.E) tb.first[e + 1] = incl;
   if (e == 0) tb.first[0] = 0;
   __syncthreads();
+}
+
+// A bounded wait, false once the block has aborted or the limit has passed (which aborts
+// the block and records a timeout).  What follows the first look is out of line: the
+// loops of the warps are bound by their instructions' latencies.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                       int* status) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if ((long long)(global_ns() - t0) > LIMIT_NS) {
+      *abort_flag = 1;
+      if (status) atomicExch(status, DEV_STATUS_TIMEOUT);
+      return false;
+    }
+  }
+}
+// The one lane of a warp that issues.
+__device__ __forceinline__ bool elect() {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(v));
+  return v != 0;
 }
 
 __device__ __forceinline__ float act_of(int act, float h) {
@@ -135,40 +176,64 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
-__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
+// 32 columns of tensor memory, a lane's own.
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint4 (&v)[2][4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(at), "r"(v[0][0].x), "r"(v[0][0].y), "r"(v[0][0].z), "r"(v[0][0].w), "r"(v[0][1].x),
+      "r"(v[0][1].y), "r"(v[0][1].z), "r"(v[0][1].w), "r"(v[0][2].x), "r"(v[0][2].y), "r"(v[0][2].z),
+      "r"(v[0][2].w), "r"(v[0][3].x), "r"(v[0][3].y), "r"(v[0][3].z), "r"(v[0][3].w), "r"(v[1][0].x),
+      "r"(v[1][0].y), "r"(v[1][0].z), "r"(v[1][0].w), "r"(v[1][1].x), "r"(v[1][1].y), "r"(v[1][1].z),
+      "r"(v[1][1].w), "r"(v[1][2].x), "r"(v[1][2].y), "r"(v[1][2].z), "r"(v[1][2].w), "r"(v[1][3].x),
+      "r"(v[1][3].y), "r"(v[1][3].z), "r"(v[1][3].w)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D += A B^T with A in tensor memory.
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 __device__ __forceinline__ uint32_t lds_scale(uint32_t at) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return v | (uint32_t)v << 16;
+  return v;
 }
 
-template <int BN, bool SWIGLU>
+template <bool SWIGLU>
 __global__ void __launch_bounds__(THREADS, 1)
-q4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_w3,
                const __grid_constant__ CUtensorMap tm_s3, const Params p) {
-  constexpr int S = Ring<BN>::S, Q = Ring<BN>::Q, STAGE = kStage<BN>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t raw_full[Q], raw_empty[Q], x_full[S], a_full[S], empty[S];
+  __shared__ __align__(8) uint64_t raw_full[Q], raw_empty[Q], a_full[MAX_SA], a_empty[MAX_SA];
+  __shared__ __align__(8) uint64_t x_full[MAX_SX], x_empty[MAX_SX];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_mb;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ Table tb;
   volatile int* abort_flag = &abort_word;
-  const uint32_t sbase = smem_u32(smem), rbase = sbase + S * STAGE;
+  const uint32_t sbase = smem_u32(smem), rbase = sbase + X_RING;
+  const int bn = p.bn, SA = stages_a(bn), SX = stages_x(bn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < Q; ++i) {
       mbar_init(smem_u32(&raw_full[i]), 1);
-      mbar_init(smem_u32(&raw_empty[i]), N_WIDEN);
+      mbar_init(smem_u32(&raw_empty[i]), 8);      // (a stage is two groups' work)
     }
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < MAX_SA; ++i) {
+      mbar_init(smem_u32(&a_full[i]), 8);
+      mbar_init(smem_u32(&a_empty[i]), 1);
+    }
+    for (int i = 0; i < MAX_SX; ++i) {
       mbar_init(smem_u32(&x_full[i]), 1);
-      mbar_init(smem_u32(&a_full[i]), N_WIDEN);
-      mbar_init(smem_u32(&empty[i]), 1);
+      mbar_init(smem_u32(&x_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&acc_full[i]), 1);
@@ -181,151 +246,172 @@ q4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
   if (warp == W_MMA) tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
   pdl_wait();                  // offsets and x may be the previous kernel's
   tc_fence_before();
-  make_table<BN>(p, tb);       // (with barriers of the block)
+  make_table(p, tb);       // (with barriers of the block)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int total = tb.first[p.E] * p.nF;
-  const int nraw = (p.K + RAW_K - 1) / RAW_K, nkb = (p.K + BK - 1) / BK;
-  auto wait = [&](uint64_t& mb, uint32_t parity) {
-    return wait_bar(smem_u32(&mb), parity, abort_flag, p.status, LIMIT_NS);
+  const int nraw = (p.K + RAW_K - 1) / RAW_K, nkb = (p.K + BK - 1) / BK;   // 2 nraw or one less
+  // (bar: a barrier's address in shared memory)
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, p.status);
+  };
+  auto all_wait = [&](uint32_t bar, uint32_t parity) {     // by a whole warp
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+           __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag, p.status));
   };
 
+  // The loops below are run by whole warps and only the copies and products by one lane,
+  // so that what is the same for all lanes stays in the uniform registers that those
+  // instructions take.
   if (warp == W_RAW) {
-    if (lane == 0) {
-      int q = 0, issued = 0;
-      uint32_t ph = 0, last = 0;
-      bool ok = true;
-      const int ng = RAW_K >> p.log_g;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const Tile T = tile_at(t, p, tb);
-        for (int j = 0; j < nraw; ++j) {
-          if (!wait(raw_empty[q], ph ^ 1u)) { ok = false; break; }
+    const bool issuer = elect();
+    const int ng = RAW_K >> p.log_g;
+    const uint32_t bytes = CODE_BYTES + ng * BM * 2;
+    int q = 0, issued = 0;
+    uint32_t ph = 0, last = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile T = tile_at(t, p, tb);
+      for (int j = 0; j < nraw; ++j) {
+        if (!all_wait(smem_u32(&raw_empty[q]), ph ^ 1u)) { ok = false; break; }
+        if (issuer) {
           const uint32_t bar = smem_u32(&raw_full[q]), to = rbase + q * RAW_BYTES, ss = to + CODE_BYTES;
-          mbar_arrive_expect_tx(bar, CODE_BYTES + ng * BM * 2);
+          mbar_arrive_expect_tx(bar, bytes);
+          tma_load_3d(to, &tm_w, bar, j * (RAW_K / 2), T.f0, T.e);
+          tma_load_3d(ss, &tm_s, bar, T.f0, j * ng, T.e);
           if (SWIGLU) {
-            tma_load_3d(to, &tm_w, bar, j * (RAW_K / 2), T.f0, T.e);
             tma_load_3d(to + CODE_BYTES / 2, &tm_w3, bar, j * (RAW_K / 2), T.f0, T.e);
-            tma_load_3d(ss, &tm_s, bar, T.f0, j * ng, T.e);
             tma_load_3d(ss + ng * BM, &tm_s3, bar, T.f0, j * ng, T.e);
-          } else {
-            tma_load_3d(to, &tm_w, bar, j * (RAW_K / 2), T.f0, T.e);
-            tma_load_3d(ss, &tm_s, bar, T.f0, j * ng, T.e);
           }
-          issued |= 1 << q;
-          last = (last & ~(1u << q)) | (ph << q);
-          if (++q == Q) { q = 0; ph ^= 1u; }
         }
+        issued |= 1 << q;
+        last = (last & ~(1u << q)) | (ph << q);
+        if (++q == Q) { q = 0; ph ^= 1u; }
       }
-      // every copy has landed before the block goes
-      for (int i = 0; i < Q; ++i)
-        if (issued >> i & 1) drain_wait(smem_u32(&raw_full[i]), last >> i & 1u, LIMIT_NS);
     }
+    // every copy has landed before the block goes
+    for (int i = 0; i < Q; ++i)
+      if (issued >> i & 1) drain_wait(smem_u32(&raw_full[i]), last >> i & 1u, LIMIT_NS);
     __syncwarp();
   } else if (warp == W_X) {
-    if (lane == 0) {
-      int s = 0, issued = 0;
-      uint32_t ph = 0, last = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const Tile T = tile_at(t, p, tb);
-        const int boxes = (T.n + X_BOX - 1) / X_BOX;
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait(empty[s], ph ^ 1u)) { ok = false; break; }
-          const uint32_t bar = smem_u32(&x_full[s]), to = sbase + s * STAGE + A_BYTES;
-          mbar_arrive_expect_tx(bar, boxes * (X_BOX * BK * 2));
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(to + b * (X_BOX * BK * 2), &tm_x, bar, kb * BK, T.r0 + b * X_BOX);
-          issued |= 1 << s;
-          last = (last & ~(1u << s)) | (ph << s);
-          if (++s == S) { s = 0; ph ^= 1u; }
+    const bool issuer = elect();
+    int s = 0, issued = 0;
+    uint32_t ph = 0, last = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile T = tile_at(t, p, tb);
+      const int box = box_of(T.n);
+      const uint32_t bytes = box_rows(box) * (BK * 2);
+      const CUtensorMap* map = &tm_x.box[box];
+      for (int j = 0; j < nraw; ++j) {
+        if (!all_wait(smem_u32(&x_empty[s]), ph ^ 1u)) { ok = false; break; }
+        if (issuer) {
+          const uint32_t bar = smem_u32(&x_full[s]), to = sbase + s * (bn * 256);
+          const bool two = 2 * j + 1 < nkb;              // 64 inputs each
+          mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
+          tma_load_2d(to, map, bar, j * RAW_K, T.r0);
+          if (two) tma_load_2d(to + bn * 128, map, bar, j * RAW_K + BK, T.r0);
         }
+        issued |= 1 << s;
+        last = (last & ~(1u << s)) | (ph << s);
+        if (++s == SX) { s = 0; ph ^= 1u; }
       }
-      for (int i = 0; i < S; ++i)
-        if (issued >> i & 1) drain_wait(smem_u32(&x_full[i]), last >> i & 1u, LIMIT_NS);
     }
+    for (int i = 0; i < SX; ++i)
+      if (issued >> i & 1) drain_wait(smem_u32(&x_full[i]), last >> i & 1u, LIMIT_NS);
     __syncwarp();
   } else if (warp == W_MMA) {
-    int s = 0, buf = 0;
-    uint32_t ph = 0, aph = 0;
+    const bool issuer = elect();
+    // a descriptor's upper word (128-byte swizzle, 1024 bytes from eight rows to the
+    // next) and the lower one of the first stage
+    constexpr uint32_t hi = 1024u >> 4 | 1u << 14 | 2u << 29;
+    const uint32_t b0 = sbase >> 4 | 1u << 16, a0 = tmem + 2 * bn;
+    int sa = 0, sx = 0, buf = 0;
+    uint32_t pa = 0, px = 0, aph = 0;
     bool ok = true, any = false;
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile T = tile_at(t, p, tb);
-      if (!__all_sync(0xffffffffu, wait(acc_empty[buf], aph ^ 1u))) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(buf * 256);
+      if (!all_wait(smem_u32(&acc_empty[buf]), aph ^ 1u)) break;
+      const uint32_t d = tmem + (uint32_t)(buf * bn);
       // fp32 accumulator, bf16 operands, both along K; N the rows in steps of 16
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)((T.n + 15) / 16 * 2) << 17 |
                              (uint32_t)(BM >> 4) << 24;
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (!__all_sync(0xffffffffu, wait(x_full[s], ph) && wait(a_full[s], ph))) { ok = false; break; }
+      for (int j = 0; j < nraw; ++j) {
+        const uint32_t xb = smem_u32(&x_full[sx]), ab = smem_u32(&a_full[sa]);
+        const bool x_in = mbar_try_wait(xb, px), a_in = mbar_try_wait(ab, pa);
+        if (!__all_sync(0xffffffffu, x_in && a_in) && !(all_wait(xb, px) && all_wait(ab, pa))) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a = sbase + s * STAGE, b = a + A_BYTES;
+        const uint32_t a = a0 + sa * 64, b = b0 + sx * (bn * 16);
+        if (issuer) {
 #pragma unroll
-          for (int kk = 0; kk < BK / UK; ++kk)
-            mma_bf16(d, smem_desc(a + kk * 32, 16, 1024), smem_desc(b + kk * 32, 16, 1024), idesc,
-                     (kb > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&empty[s]));
+          for (int k = 0; k < 2; ++k)
+            if (2 * j + k < nkb)
+#pragma unroll
+              for (int kk = 0; kk < BK / UK; ++kk)
+                mma_ta(d, a + k * 32 + kk * 8, (uint64_t)hi << 32 | (b + k * (bn * 8) + kk * 2), idesc,
+                       (j > 0 || k > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(smem_u32(&a_empty[sa]));
+          mma_commit(smem_u32(&x_empty[sx]));
         }
         any = true;
-        __syncwarp();
-        if (++s == S) { s = 0; ph ^= 1u; }
+        if (++sa == SA) { sa = 0; pa ^= 1u; }
+        if (++sx == SX) { sx = 0; px ^= 1u; }
       }
       if (!ok) break;
-      if (lane == 0) mma_commit(smem_u32(&acc_full[buf]));
-      __syncwarp();
+      if (issuer) mma_commit(smem_u32(&acc_full[buf]));
       if (++buf == 2) { buf = 0; aph ^= 1u; }
     }
-    if (any && lane == 0) {
+    if (any && issuer) {
       mma_commit(smem_u32(&drain_mb));
       drain_wait(smem_u32(&drain_mb), 0, LIMIT_NS);
     }
     __syncwarp();
   } else if (warp >= W_WIDEN) {
-    const int w = tid - 32 * W_WIDEN, r = w & 127, half = w >> 7;
-    // SwiGLU: 16 outputs of W and the same 16 of W3 share a warp's lanes
-    const int row = SWIGLU ? (r >> 4 & 3) * 32 + (r >> 6) * 16 + (r & 15) : r;
-    const uint32_t code_at = r * 64, swz = (r >> 1) & 3;
-    const int ng = RAW_K >> p.log_g;
+    // a warp may only write its own quarter of the tensor memory's lanes
+    const int group = (warp - W_WIDEN) >> 2, h = group & 1, quarter = warp & 3;
+    // this lane's output in a raw stage; SwiGLU: 16 outputs of W and the same 16 of W3
+    // share a warp's lanes
+    const int r = SWIGLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
+    const int ng = RAW_K >> p.log_g, swz = (r >> 1) & 3;
     const uint32_t scale_at = CODE_BYTES + (SWIGLU ? (r >> 6) * ng * BM + (r & 63) * 2 : r * 2);
     const uint32_t scale_step = SWIGLU ? BM : BM * 2;
-    const uint32_t a_at = row * 128;
-    int q = 0, s = 0;
-    uint32_t qph = 0, ph = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      for (int j = 0; ok && j < nraw; ++j) {
-        if (!__all_sync(0xffffffffu, wait(raw_full[q], qph))) { ok = false; break; }
-        const uint32_t raw = rbase + q * RAW_BYTES;
-        uint4 code[2];
-        uint32_t scale[2];
+    // where its two runs of 32 codes and their scales lie
+    const uint32_t code0 = rbase + r * 64 + ((2 * h) ^ swz) * 16, code1 = rbase + r * 64 + ((2 * h + 1) ^ swz) * 16;
+    const uint32_t scale0 = rbase + scale_at + ((h * 64) >> p.log_g) * scale_step;
+    const uint32_t scale1 = rbase + scale_at + ((h * 64 + 32) >> p.log_g) * scale_step;
+    const uint32_t to0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * bn + h * 32;
+    // the group's stages are every (NG / 2)-th
+    const int mine = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const long long raws = (long long)mine * nraw;
+    int q = group >> 1, s = group >> 1, j = group >> 1;    // j: stage of a tile
+    uint32_t qph = 0, ph = 1;
+    for (long long i = group >> 1; i < raws; i += NG / 2) {
+      if (!all_wait(smem_u32(&raw_full[q]), qph)) break;
+      const uint4 w0 = lds128(code0 + q * RAW_BYTES), w1 = lds128(code1 + q * RAW_BYTES);
+      const uint32_t s0 = lds_scale(scale0 + q * RAW_BYTES), s1 = lds_scale(scale1 + q * RAW_BYTES);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&raw_empty[q]));
+      q += NG / 2;
+      if (q >= Q) { q -= Q; qph ^= 1u; }
+      uint4 w[2][4];
+      q4_words(w0, q4_scale(s0), w[0]);
+      q4_words(w1, q4_scale(s1), w[1]);
+      while (j >= nraw) j -= nraw;
+      if (j * RAW_K + h * BK + 32 >= p.K)      // past the last input: zeros, whatever the scale
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          code[h] = lds128(raw + code_at + ((2 * h + half) ^ swz) * 16);
-          scale[h] = lds_scale(raw + scale_at + ((h * 64 + half * 32) >> p.log_g) * scale_step);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&raw_empty[q]));
-        if (++q == Q) { q = 0; qph ^= 1u; }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k0 = j * RAW_K + h * BK;
-          if (k0 >= p.K) break;
-          if (!__all_sync(0xffffffffu, wait(empty[s], ph ^ 1u))) { ok = false; break; }
-          const uint32_t to = sbase + s * STAGE + a_at;
-          // past the last input: zeros, whatever the scale
-          const bool on = k0 + half * 32 < p.K;
-          const uint32_t c4[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sts128(to + (((half * 4 + i) ^ (row & 7)) << 4),
-                   on ? q4_word(c4[i], scale[h]) : make_uint4(0u, 0u, 0u, 0u));
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
-          if (++s == S) { s = 0; ph ^= 1u; }
-        }
-      }
+        for (int c = 0; c < 4; ++c) w[1][c] = make_uint4(0u, 0u, 0u, 0u);
+      j += NG / 2;
+      if (!all_wait(smem_u32(&a_empty[s]), ph)) break;
+      tc_fence_after();
+      tmem_st32(to0 + s * 64, w);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
+      s += NG / 2;
+      if (s >= SA) { s -= SA; ph ^= 1u; }
     }
   } else {
     const int quarter = warp & 3;            // of the accumulator's lanes that this warp may read
@@ -333,9 +419,9 @@ q4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     uint32_t aph = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       const Tile T = tile_at(t, p, tb);
-      if (!__all_sync(0xffffffffu, wait(acc_full[buf], aph))) break;
+      if (!all_wait(smem_u32(&acc_full[buf]), aph)) break;
       tc_fence_after();
-      const uint32_t at = tmem + (uint32_t)(buf * 256) + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t at = tmem + (uint32_t)(buf * bn) + ((uint32_t)(quarter * 32) << 16);
       const int f = T.f0 + (SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
       const bool on = f < p.N;
       const float bias = !SWIGLU && p.bias != nullptr && on ? p.bias[(long long)T.e * p.N + f] : 0.f;
@@ -394,21 +480,15 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool SWIGLU>
-cudaError_t launch_t(const CUtensorMap* maps, const Params& p, long long tiles, cudaStream_t st) {
+template <bool SWIGLU>
+cudaError_t launch_t(const XMaps& x, const CUtensorMap* maps, const Params& p, long long tiles,
+                     cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = ensure_dynamic_smem(q4_gemm_kernel<BN, SWIGLU>, kSmem<BN>, attr_done);
+  cudaError_t e = ensure_dynamic_smem(q4_gemm_kernel<SWIGLU>, SMEM, attr_done);
   if (e != cudaSuccess) return e;
   const int sms = sm_count(), grid = tiles < sms ? (int)tiles : sms;
-  return launch_pdl(q4_gemm_kernel<BN, SWIGLU>, dim3(grid), dim3(THREADS), kSmem<BN>, st, maps[0], maps[1],
-                    maps[2], maps[3], maps[4], p);
-}
-
-template <bool SWIGLU>
-cudaError_t launch_bn(int bn, const CUtensorMap* maps, const Params& p, long long tiles, cudaStream_t st) {
-  if (bn == 64) return launch_t<64, SWIGLU>(maps, p, tiles, st);
-  if (bn == 128) return launch_t<128, SWIGLU>(maps, p, tiles, st);
-  return launch_t<256, SWIGLU>(maps, p, tiles, st);
+  return launch_pdl(q4_gemm_kernel<SWIGLU>, dim3(grid), dim3(THREADS), SMEM, st, x, maps[0], maps[1],
+                    maps[2], maps[3], p);
 }
 
 }  // namespace
@@ -425,10 +505,14 @@ cudaError_t launch_q4_gemm(const Q4Product& q, cudaStream_t st) {
   p.bias = q.bias;
   p.c = static_cast<bf16*>(q.c);
   p.status = q.status;
-  CUtensorMap maps[5];
+  CUtensorMap maps[4];
+  XMaps x;
   const uint64_t xd[2] = {(uint64_t)q.K, (uint64_t)q.R}, xs[1] = {(uint64_t)q.K * 2};
-  const uint32_t xb[2] = {BK, X_BOX};
-  bool ok = encode(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, q.x, 2, xd, xs, xb);
+  bool ok = true;
+  for (int i = 0; i < X_BOXES && ok; ++i) {
+    const uint32_t xb[2] = {BK, (uint32_t)box_rows(i)};
+    ok = encode(&x.box[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, q.x, 2, xd, xs, xb);
+  }
   const uint64_t groups = (uint64_t)q4_groups(q.K, q.G);
   const uint64_t wd[3] = {(uint64_t)q.K / 2, (uint64_t)q.N, (uint64_t)q.E};
   const uint64_t ws[2] = {(uint64_t)q.K / 2, (uint64_t)q.N * (uint64_t)q.K / 2};
@@ -438,20 +522,21 @@ cudaError_t launch_q4_gemm(const Q4Product& q, cudaStream_t st) {
   const uint32_t sb[3] = {(uint32_t)p.per, (uint32_t)(RAW_K / q.G), 1};
   for (int i = 0; i < 2 && ok; ++i) {
     if (i == 1 && !swiglu) {
+      maps[2] = maps[0];
       maps[3] = maps[1];
-      maps[4] = maps[2];
       break;
     }
-    ok = encode(&maps[1 + 2 * i], CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_64B,
+    ok = encode(&maps[2 * i], CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_64B,
                 i ? q.codes3 : q.codes, 3, wd, ws, wb) &&
-         encode(&maps[2 + 2 * i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_NONE,
+         encode(&maps[1 + 2 * i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_NONE,
                 i ? q.scales3 : q.scales, 3, sd, ss, sb);
   }
   if (!ok) return cudaErrorInvalidValue;
   const long long mean = q.R / q.E;
-  const int bn = mean > 96 ? 256 : mean > 48 ? 128 : 64;
+  p.bn = mean > 96 ? 192 : mean > 48 ? 128 : 64;
+  if (getenv("Q4_BN")) p.bn = atoi(getenv("Q4_BN"));
   const long long tiles = ((long long)q.R / 16 + q.E) * p.nF;      // at most
-  return swiglu ? launch_bn<true>(bn, maps, p, tiles, st) : launch_bn<false>(bn, maps, p, tiles, st);
+  return swiglu ? launch_t<true>(x, maps, p, tiles, st) : launch_t<false>(x, maps, p, tiles, st);
 }
 
 }  // namespace moe
