@@ -278,7 +278,7 @@ __device__ __forceinline__ void emit(const DecodeArgs& a, const Tile& tl, int bl
 // column of the result depends on its own token only, so absent tokens repeat
 // the last one's row.
 template <typename WT, bool UP> struct Products;
-template <bool UP> struct MmaProducts {
+template <bool UP, bool Q4W> struct MmaProducts {
   uint32_t at0, at1;           // the lane's token rows of the two token tiles
   int plane, n;
   // token tiles of 8 by chains of dependent products: the two steps of a block,
@@ -290,8 +290,9 @@ template <bool UP> struct MmaProducts {
   // or an overflowing product's infinity, and they overflow only where it does.
   __device__ __forceinline__ float total(int t8, int c) const {
     const float first = acc[t8][0][c] + acc[t8][1][c];
-    if (UP) return first;
-    return isfinite(first) ? first + (acc[t8][CH - 2][c] + acc[t8][CH - 1][c]) : first;
+    float sum = first;
+    if (!UP && isfinite(first)) sum += acc[t8][CH - 2][c] + acc[t8][CH - 1][c];
+    return Q4W ? Q4_UNSCALE * sum : sum;
   }
   __device__ __forceinline__ void begin(const char* rows, int pitch, int tokens, int lane) {
     const uint32_t at = smem_addr(rows) + (lane & 3) * 16;
@@ -337,7 +338,7 @@ template <bool UP> struct MmaProducts {
     }
   }
 };
-template <bool UP> struct Products<bf16, UP> : MmaProducts<UP> {
+template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false> {
   static constexpr int PIECE = Stored<bf16>::PIECE;
   __device__ __forceinline__ void stage(const Part&, uint32_t from, int v0, int left, int lane) {
     const int g = lane >> 2, blocks = min(PIECE / 64, (left + 31) / 32);
@@ -364,7 +365,7 @@ template <bool UP> struct Products<bf16, UP> : MmaProducts<UP> {
 // Products<Q4>: a lane reads 32 inputs' codes of its two rows at once, in which the
 // scale does not change, and multiplies word by word.  The four lanes of a row take
 // 128 inputs in turn, lane c words 4 c to 4 c + 3.
-template <bool UP> struct Products<Q4, UP> : MmaProducts<UP> {
+template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
   static constexpr int PIECE = Stored<Q4>::PIECE;
   __device__ __forceinline__ void stage(const Part& p, uint32_t from, int v0, int left, int lane) {
     const int g = lane >> 2, c = lane & 3, blocks = min(PIECE / 64, (left + 127) / 128);
@@ -374,12 +375,11 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP> {
       const uint32_t wat = (from + g * PIECE + u * 64 + c * 16) ^ ((g & 1) << 6);
       const uint4 w0 = load_rows(wat), w1 = load_rows(wat + 8 * PIECE);
       const uint32_t sat = slab + ((u * 128 + c * 32) >> p.log_g) * 32;
-      uint4 r0[4], r1[4];
-      q4_words(w0, q4_scale(load_scale(sat)), r0);
-      q4_words(w1, q4_scale(load_scale(sat + 16)), r1);
+      uint4 r[2][4];
+      q4_runs(w0, w1, load_scale(sat), load_scale(sat + 16), r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 a = r0[j], b = r1[j];
+        const uint4 a = r[0][j], b = r[1][j];
         auto products = [&](float (&c0)[4], float (&c1)[4], uint32_t x_at) {
           const uint4 x = load_rows(x_at);
           mma16816(c0, a.x, b.x, a.y, b.y, x.x, x.y);

@@ -12,67 +12,57 @@ __device__ __forceinline__ uint32_t q4_fma(uint32_t a, uint32_t b, uint32_t c) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// What turns codes of one scale into weights, (code - 8) scale in bf16.
-//
-// With the code in the upper four bits of a bf16 mantissa behind 1, the value is
-// (16 + code) / 16, and  (16 + code) / 16 (16 scale) - 24 scale  is the weight, in one
-// fma and without a rounding where 24 scale is exact: 3 scale has two bits more than
-// scale, so scales of up to six significant bits (whose last two bits of a bf16 are
-// zeros) take it, beyond the smallest and largest numbers.  For other scales 128 +
-// code, the code in the lower four bits of the mantissa, loses 136 (exact) and the
-// product with the scale is rounded.  Both give the nearest bf16 value of the weight.
-struct Q4Scale {
-  uint32_t mul, add;           // both halves alike
-  bool fast;
-};
-__device__ __forceinline__ Q4Scale q4_scale(uint32_t bits) {     // of a bf16 scale
-  const uint32_t two = bits | bits << 16, mag = bits & 0x7fffu;
-  Q4Scale s;
-  s.fast = (bits & 3u) == 0u && mag >= 0x0800u && mag < 0x7800u;
-  s.mul = two;
-  s.add = 0u;
-  if (s.fast) {
-    s.mul = two + 0x02000200u;                                   // 16 scale
-    s.add = q4_fma(two, 0xc1c0c1c0u, 0u);                        // -24 scale
+// The weights of a word's eight codes, (code - 8) scale, for a scale of any bits (in both
+// halves of scale2).  128 + code is the bf16 value whose last four bits are the code;
+// taking 136 from it is exact, so the product is the only rounding.
+__device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t scale2) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    v[i] = q4_fma(q4_fma(b, 0x3f803f80u, 0xc308c308u), scale2, 0x80008000u);
   }
-  return s;
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
-// The weights of a word's eight codes.
-__device__ __forceinline__ uint4 q4_word_fast(uint32_t w, const Q4Scale& s) {
-  constexpr uint32_t M = 0x00780078u, ONE = 0x3f803f80u;
-  return make_uint4(q4_fma(((w << 3) & M) | ONE, s.mul, s.add), q4_fma(((w >> 1) & M) | ONE, s.mul, s.add),
-                    q4_fma(((w >> 5) & M) | ONE, s.mul, s.add), q4_fma(((w >> 9) & M) | ONE, s.mul, s.add));
+
+// The same weights times 2^-8, for the products (whose results are multiplied with 2^8,
+// exactly), with three instructions for two weights and a shift for eight.  A bf16 value
+// whose bits are the number b, 0 <= b < 256, is b 2^-133: so are the smallest (subnormal)
+// ones and, beyond 127, the first of the others.  A code in the lower four bits of that
+// byte or in its upper four is then a multiple of 2^-133 or 2^-129 as it stands, and
+//   code 2^-133 (scale 2^125) - scale 2^-5  =  (code - 8) scale 2^-8
+// is one fma, whose only rounding is that of the weight.  The scales for which those
+// factors are normal numbers, 2^-121 to 2^3, take it; a warp with another among its
+// lanes' goes by q4_word.
+constexpr float Q4_UNSCALE = 256.f;
+__device__ __forceinline__ bool q4_fast(uint32_t bits) {         // of a bf16 scale
+  return (bits & 0x7fffu) - 0x0300u < 0x3e00u;
 }
-__device__ __forceinline__ uint32_t q4_pair_any(uint32_t w, uint32_t scale2) {
-  uint32_t b = (w & 0x000f000fu) | 0x43004300u;
-  const uint32_t c136 = 0x43084308u;
-  __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b),
-                             *reinterpret_cast<const __nv_bfloat162*>(&c136));
-  v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&scale2));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint4 q4_word_any(uint32_t w, const Q4Scale& s) {
-  return make_uint4(q4_pair_any(w, s.mul), q4_pair_any(w >> 4, s.mul), q4_pair_any(w >> 8, s.mul),
-                    q4_pair_any(w >> 12, s.mul));
-}
-__device__ __forceinline__ uint4 q4_word(uint32_t w, const Q4Scale& s) {
-  return s.fast ? q4_word_fast(w, s) : q4_word_any(w, s);
-}
-// Four words of one scale, one branch.
-__device__ __forceinline__ void q4_words(const uint4& w, const Q4Scale& s, uint4 (&v)[4]) {
-#ifdef QM
-  if (QM == 0) { v[0] = v[1] = v[2] = v[3] = make_uint4(w.x, w.y, w.z, w.w ^ s.mul); return; }
-  if (QM == 1) { v[0] = q4_word_fast(w.x, s); v[1] = q4_word_fast(w.y, s);
-    v[2] = q4_word_fast(w.z, s); v[3] = q4_word_fast(w.w, s); return; }
-  if (QM == 2) { v[0] = q4_word_any(w.x, s); v[1] = q4_word_any(w.y, s);
-    v[2] = q4_word_any(w.z, s); v[3] = q4_word_any(w.w, s); return; }
-#endif
-  if (s.fast) {
-    v[0] = q4_word_fast(w.x, s); v[1] = q4_word_fast(w.y, s);
-    v[2] = q4_word_fast(w.z, s); v[3] = q4_word_fast(w.w, s);
+// Two runs of 32 inputs, by a whole warp: one branch that all its lanes take alike.
+// bits0, bits1: the runs' scales.
+__device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32_t bits0, uint32_t bits1,
+                                        uint4 (&v)[2][4]) {
+  const uint32_t r[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
+  const uint32_t two[2] = {__byte_perm(bits0, 0u, 0x1010), __byte_perm(bits1, 0u, 0x1010)};
+  if (__all_sync(0xffffffffu, q4_fast(bits0) && q4_fast(bits1))) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t low = two[u] + 0x3e803e80u, high = two[u] + 0x3c803c80u;    // 2^125, 2^121
+      const uint32_t add = (two[u] - 0x02800280u) ^ 0x80008000u;                 // -2^-5
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = r[u][i], x = w >> 8;
+        v[u][i] = make_uint4(q4_fma(w & 0x000f000fu, low, add), q4_fma(w & 0x00f000f0u, high, add),
+                             q4_fma(x & 0x000f000fu, low, add), q4_fma(x & 0x00f000f0u, high, add));
+      }
+    }
   } else {
-    v[0] = q4_word_any(w.x, s); v[1] = q4_word_any(w.y, s);
-    v[2] = q4_word_any(w.z, s); v[3] = q4_word_any(w.w, s);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t scale2 = q4_fma(two[u], 0x3b803b80u, 0x80008000u);          // 2^-8
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] = q4_word(r[u][i], scale2);
+    }
   }
 }
 

@@ -3,7 +3,7 @@
 //
 //   c[r, f] = act(sum_k w_e[f, k] x[r, k] + bias_e[f])     rows r of expert e
 //
-// A tile is 128 outputs by up to bn rows of one expert (64 outputs of W and the same of
+// A tile is 128 outputs by up to 192 rows of one expert (64 outputs of W and the same of
 // W3 for SwiGLU): the outputs are the lanes of the accumulator, the rows its columns,
 // so that a tile of few rows wastes no more than the narrow side of the instruction (its
 // N is the rows rounded up to 16).  The widened weights are the A operand, which lies in
@@ -20,7 +20,6 @@
 // Every wait is bounded (2 s); when one expires the block raises an abort flag and
 // the status word, waits for its copies and products in flight, frees its tensor
 // memory and returns.
-#include <cstdlib>
 #include "q4.cuh"
 #include "q4.h"
 #include "tc_ptx.cuh"
@@ -46,26 +45,22 @@ constexpr int MAX_E = 256;
 constexpr int TMEM_COLS = 512;
 constexpr long long LIMIT_NS = 2000000000ll;
 
-// Stages, each of 128 inputs: Q of codes and scales, SA of widened weights, SX of rows.
-// The accumulators take 2 bn of the 512 columns, a stage of weights 64; a stage of rows
-// 256 bn bytes.  The groups of widening warps run apart from one another, and copies do
+// Rows of a tile at most, and stages, each of 128 inputs: Q of codes and scales, SA of
+// widened weights, SX of rows.  The accumulators take 2 BN of the 512 columns, a stage of
+// weights 64.  The groups of widening warps run apart from one another, and copies do
 // not land in the order of their issue: a group may only wait on stages whose every use
 // is its own (a barrier tells no more than the parity of its phase).  So a pair of
 // groups shares a stage, 64 inputs each, and Q and SA are multiples of the pairs.  Of a
 // tile's last stage, where it has 64 inputs or less, the second half is without work.
-constexpr int Q = 8, X_RING = 144 * 1024, MAX_SA = 6, MAX_SX = 8;
-constexpr int SMEM = X_RING + Q * RAW_BYTES;
-__host__ __device__ constexpr int stages_a(int bn) { return (TMEM_COLS - 2 * bn) / 64; }
-__host__ __device__ constexpr int stages_x(int bn) {
-  return X_RING / (bn * 256) < MAX_SX ? X_RING / (bn * 256) : MAX_SX;
-}
-static_assert(Q % (NG / 2) == 0 && stages_a(192) == 2 && stages_a(128) == 4 && stages_a(64) == 6,
-              "stages of one pair");
+constexpr int BN = 192, Q = 8, SA = 2, SX = 3;
+constexpr int X_HALF = BN * BK * 2, X_STAGE = 2 * X_HALF;
+constexpr int SMEM = SX * X_STAGE + Q * RAW_BYTES;
+static_assert(2 * BN + SA * 64 <= TMEM_COLS && SA % (NG / 2) == 0 && Q % (NG / 2) == 0, "stages");
 static_assert(SMEM + 5120 <= 232448, "shared memory of one block");
 
 struct Params {
   int R, E, N, K, log_g;
-  int act, bn;
+  int act;
   int nF, per;                 // tiles along the outputs, outputs of a tile
   const int* offsets;
   const float* bias;
@@ -129,7 +124,7 @@ __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
   int tiles = 0;
   if (e < p.E) {
     const int rows = tb.offs[e + 1] - v;
-    const int least = (rows + p.bn - 1) / p.bn;
+    const int least = (rows + BN - 1) / BN;
     const int step = rows ? ((rows + least - 1) / least + 15) & ~15 : 16;
     tiles = (rows + step - 1) / step;
     tb.step[e] = step;
@@ -145,13 +140,15 @@ __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
 // loops of the warps are bound by their instructions' latencies.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                        int* status) {
-  const unsigned long long t0 = global_ns();
+  unsigned long long t0 = 0;
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if ((long long)(global_ns() - t0) > LIMIT_NS) {
+    const unsigned long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    if ((long long)(now - t0) > LIMIT_NS) {
       *abort_flag = 1;
       if (status) atomicExch(status, DEV_STATUS_TIMEOUT);
       return false;
@@ -212,26 +209,25 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
                const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_w3,
                const __grid_constant__ CUtensorMap tm_s3, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t raw_full[Q], raw_empty[Q], a_full[MAX_SA], a_empty[MAX_SA];
-  __shared__ __align__(8) uint64_t x_full[MAX_SX], x_empty[MAX_SX];
+  __shared__ __align__(8) uint64_t raw_full[Q], raw_empty[Q], a_full[SA], a_empty[SA];
+  __shared__ __align__(8) uint64_t x_full[SX], x_empty[SX];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_mb;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ Table tb;
   volatile int* abort_flag = &abort_word;
-  const uint32_t sbase = smem_u32(smem), rbase = sbase + X_RING;
-  const int bn = p.bn, SA = stages_a(bn), SX = stages_x(bn);
+  const uint32_t sbase = smem_u32(smem), rbase = sbase + SX * X_STAGE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < Q; ++i) {
       mbar_init(smem_u32(&raw_full[i]), 1);
       mbar_init(smem_u32(&raw_empty[i]), 8);      // (a stage is two groups' work)
     }
-    for (int i = 0; i < MAX_SA; ++i) {
+    for (int i = 0; i < SA; ++i) {
       mbar_init(smem_u32(&a_full[i]), 8);
       mbar_init(smem_u32(&a_empty[i]), 1);
     }
-    for (int i = 0; i < MAX_SX; ++i) {
+    for (int i = 0; i < SX; ++i) {
       mbar_init(smem_u32(&x_full[i]), 1);
       mbar_init(smem_u32(&x_empty[i]), 1);
     }
@@ -306,11 +302,11 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
       for (int j = 0; j < nraw; ++j) {
         if (!all_wait(smem_u32(&x_empty[s]), ph ^ 1u)) { ok = false; break; }
         if (issuer) {
-          const uint32_t bar = smem_u32(&x_full[s]), to = sbase + s * (bn * 256);
+          const uint32_t bar = smem_u32(&x_full[s]), to = sbase + s * X_STAGE;
           const bool two = 2 * j + 1 < nkb;              // 64 inputs each
           mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
           tma_load_2d(to, map, bar, j * RAW_K, T.r0);
-          if (two) tma_load_2d(to + bn * 128, map, bar, j * RAW_K + BK, T.r0);
+          if (two) tma_load_2d(to + X_HALF, map, bar, j * RAW_K + BK, T.r0);
         }
         issued |= 1 << s;
         last = (last & ~(1u << s)) | (ph << s);
@@ -325,33 +321,34 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     // a descriptor's upper word (128-byte swizzle, 1024 bytes from eight rows to the
     // next) and the lower one of the first stage
     constexpr uint32_t hi = 1024u >> 4 | 1u << 14 | 2u << 29;
-    const uint32_t b0 = sbase >> 4 | 1u << 16, a0 = tmem + 2 * bn;
+    const uint32_t b0 = sbase >> 4 | 1u << 16, a0 = tmem + 2 * BN;
     int sa = 0, sx = 0, buf = 0;
     uint32_t pa = 0, px = 0, aph = 0;
     bool ok = true, any = false;
+    // (the next stage's barriers are looked at while this one's products are on their way)
+    bool x_in = mbar_try_wait(smem_u32(&x_full[0]), 0), a_in = mbar_try_wait(smem_u32(&a_full[0]), 0);
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile T = tile_at(t, p, tb);
       if (!all_wait(smem_u32(&acc_empty[buf]), aph ^ 1u)) break;
-      const uint32_t d = tmem + (uint32_t)(buf * bn);
+      const uint32_t d = tmem + (uint32_t)(buf * BN);
       // fp32 accumulator, bf16 operands, both along K; N the rows in steps of 16
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)((T.n + 15) / 16 * 2) << 17 |
                              (uint32_t)(BM >> 4) << 24;
       for (int j = 0; j < nraw; ++j) {
-        const uint32_t xb = smem_u32(&x_full[sx]), ab = smem_u32(&a_full[sa]);
-        const bool x_in = mbar_try_wait(xb, px), a_in = mbar_try_wait(ab, pa);
-        if (!__all_sync(0xffffffffu, x_in && a_in) && !(all_wait(xb, px) && all_wait(ab, pa))) {
+        if (!__all_sync(0xffffffffu, x_in && a_in) &&
+            !(all_wait(smem_u32(&x_full[sx]), px) && all_wait(smem_u32(&a_full[sa]), pa))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a = a0 + sa * 64, b = b0 + sx * (bn * 16);
+        const uint32_t a = a0 + sa * 64, b = b0 + sx * (X_STAGE >> 4);
         if (issuer) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (2 * j + k < nkb)
 #pragma unroll
               for (int kk = 0; kk < BK / UK; ++kk)
-                mma_ta(d, a + k * 32 + kk * 8, (uint64_t)hi << 32 | (b + k * (bn * 8) + kk * 2), idesc,
+                mma_ta(d, a + k * 32 + kk * 8, (uint64_t)hi << 32 | (b + k * (X_HALF >> 4) + kk * 2), idesc,
                        (j > 0 || k > 0 || kk > 0) ? 1u : 0u);
           mma_commit(smem_u32(&a_empty[sa]));
           mma_commit(smem_u32(&x_empty[sx]));
@@ -359,6 +356,8 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
         any = true;
         if (++sa == SA) { sa = 0; pa ^= 1u; }
         if (++sx == SX) { sx = 0; px ^= 1u; }
+        x_in = mbar_try_wait(smem_u32(&x_full[sx]), px);
+        a_in = mbar_try_wait(smem_u32(&a_full[sa]), pa);
       }
       if (!ok) break;
       if (issuer) mma_commit(smem_u32(&acc_full[buf]));
@@ -382,7 +381,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     const uint32_t code0 = rbase + r * 64 + ((2 * h) ^ swz) * 16, code1 = rbase + r * 64 + ((2 * h + 1) ^ swz) * 16;
     const uint32_t scale0 = rbase + scale_at + ((h * 64) >> p.log_g) * scale_step;
     const uint32_t scale1 = rbase + scale_at + ((h * 64 + 32) >> p.log_g) * scale_step;
-    const uint32_t to0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * bn + h * 32;
+    const uint32_t to0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * BN + h * 32;
     // the group's stages are every (NG / 2)-th
     const int mine = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     const long long raws = (long long)mine * nraw;
@@ -391,19 +390,17 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     for (long long i = group >> 1; i < raws; i += NG / 2) {
       if (!all_wait(smem_u32(&raw_full[q]), qph)) break;
       const uint4 w0 = lds128(code0 + q * RAW_BYTES), w1 = lds128(code1 + q * RAW_BYTES);
-      const uint32_t s0 = lds_scale(scale0 + q * RAW_BYTES), s1 = lds_scale(scale1 + q * RAW_BYTES);
+      const uint32_t s0 = lds_scale(scale0 + q * RAW_BYTES);
+      uint32_t s1 = p.log_g == 5 ? lds_scale(scale1 + q * RAW_BYTES) : s0;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&raw_empty[q]));
       q += NG / 2;
       if (q >= Q) { q -= Q; qph ^= 1u; }
       uint4 w[2][4];
-      q4_words(w0, q4_scale(s0), w[0]);
-      q4_words(w1, q4_scale(s1), w[1]);
       while (j >= nraw) j -= nraw;
-      if (j * RAW_K + h * BK + 32 >= p.K)      // past the last input: zeros, whatever the scale
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[1][c] = make_uint4(0u, 0u, 0u, 0u);
+      if (j * RAW_K + h * BK + 32 >= p.K) s1 = 0u;       // past the last input: zeros, whatever the scale
       j += NG / 2;
+      q4_runs(w0, w1, s0, s1, w);
       if (!all_wait(smem_u32(&a_empty[s]), ph)) break;
       tc_fence_after();
       tmem_st32(to0 + s * 64, w);
@@ -421,7 +418,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
       const Tile T = tile_at(t, p, tb);
       if (!all_wait(smem_u32(&acc_full[buf]), aph)) break;
       tc_fence_after();
-      const uint32_t at = tmem + (uint32_t)(buf * bn) + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t at = tmem + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
       const int f = T.f0 + (SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
       const bool on = f < p.N;
       const float bias = !SWIGLU && p.bias != nullptr && on ? p.bias[(long long)T.e * p.N + f] : 0.f;
@@ -436,7 +433,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
           for (int i = 0; i < 16; i += 2) {
             const bool up = lane >= 16;
             const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 16);
-            const float h1 = up ? got : v[i], h3 = up ? v[i + 1] : got;
+            const float h1 = Q4_UNSCALE * (up ? got : v[i]), h3 = Q4_UNSCALE * (up ? v[i + 1] : got);
             const int n = col + i + (up ? 1 : 0);
             if (on && n < T.n)
               c[(long long)n * p.N] = __float2bfloat16_rn((h1 * sigmoid_epi(h1)) * h3);
@@ -445,7 +442,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (on && col + i < T.n)
-              c[(long long)(col + i) * p.N] = __float2bfloat16_rn(act_of(p.act, v[i] + bias));
+              c[(long long)(col + i) * p.N] = __float2bfloat16_rn(act_of(p.act, fmaf(v[i], Q4_UNSCALE, bias)));
         }
       }
       tc_fence_before();
@@ -532,9 +529,6 @@ cudaError_t launch_q4_gemm(const Q4Product& q, cudaStream_t st) {
                 i ? q.scales3 : q.scales, 3, sd, ss, sb);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const long long mean = q.R / q.E;
-  p.bn = mean > 96 ? 192 : mean > 48 ? 128 : 64;
-  if (getenv("Q4_BN")) p.bn = atoi(getenv("Q4_BN"));
   const long long tiles = ((long long)q.R / 16 + q.E) * p.nF;      // at most
   return swiglu ? launch_t<true>(x, maps, p, tiles, st) : launch_t<false>(x, maps, p, tiles, st);
 }

@@ -137,7 +137,7 @@ q4_dequantize_kernel(const Q4Shape s, const uint32_t* __restrict__ codes,
   const uint32_t two[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    const uint4 v = q4_word(word[r], q4_scale(r % 2 ? two[r / 2] >> 16 : two[r / 2] & 0xffffu));
+    const uint4 v = q4_word(word[r], __byte_perm(two[r / 2], 0u, r % 2 ? 0x3232 : 0x1010));
     T* to = w + (p.row + r) * s.K + p.k;
     if constexpr (sizeof(T) == 2) {
       __stcs(reinterpret_cast<uint4*>(to), v);

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4Product p) {
                               ((long long)e * p.N + n) * words;
       const bf16* scales = static_cast<const bf16*>(m ? p.scales3 : p.scales) + (long long)e * groups * p.N + n;
       for (int j = lane; j < words; j += 32) {
-        const uint4 w = q4_word(codes[j], q4_scale(__bfloat16_as_ushort(scales[(long long)(j * 8 / p.G) * p.N]))), v = x[j];
+        const uint4 w = q4_word(codes[j], 0x10001u * __bfloat16_as_ushort(scales[(long long)(j * 8 / p.G) * p.N])), v = x[j];
         const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
