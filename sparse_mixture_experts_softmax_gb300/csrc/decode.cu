@@ -79,17 +79,18 @@ decode_kernel(const __grid_constant__ DecodeArgs a, const int tt) {
 
   int* row_at = reinterpret_cast<int*>(sm + P.off_at);
   const int warp = tid >> 5;
-  if (warp < CW) {
-    const uint32_t ring = smem_addr(sm) + warp * NS * Stored<WT>::STAGE;
+  if (warp < Stored<WT>::CW) {
+    const uint32_t ring = smem_addr(sm) + warp * Stored<WT>::NS * Stored<WT>::STAGE;
 #pragma unroll 1
     for (int shared = 0; shared < (a.Fs > 0 ? 2 : 1); ++shared)
-      compute<WT, true>(a, make_part<WT, true>(a, nr, nt, !shared), rt, tt, row_at + shared * nr, rows,
-                    P.rows_bytes, red, ring, nullptr);
+      compute<WT, true>(LayerJob<WT, true>{a, rt, nullptr}, make_part<WT, true>(a, nr, nt, !shared),
+                        rt.tiles, tt, row_at + shared * nr, rows, P.rows_bytes, red, ring);
 #pragma unroll 1
     for (int shared = 0; shared < (a.Fs > 0 ? 2 : 1); ++shared)
-      compute<WT, false>(a, make_part<WT, false>(a, nr, nt, !shared), rt, tt, row_at + shared * nr, rows,
-                     P.rows_bytes, red, ring, shared ? nullptr : &flag);
-    grid_barrier<CTHREADS>(a.ctl, 2, &flag);
+      compute<WT, false>(LayerJob<WT, false>{a, rt, shared ? nullptr : &flag},
+                         make_part<WT, false>(a, nr, nt, !shared), rt.tiles, tt, row_at + shared * nr,
+                         rows, P.rows_bytes, red, ring);
+    grid_barrier<kCThreads<WT>>(a.ctl, 2, &flag);
   }
   __syncthreads();
   if (flag == 0) {

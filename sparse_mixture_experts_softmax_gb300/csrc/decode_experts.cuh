@@ -10,34 +10,38 @@ namespace moe {
 namespace {
 
 constexpr int WARPS = 16, THREADS = WARPS * 32;
-constexpr int CW = 8, CTHREADS = CW * 32;       // warps that multiply (all of them route)
-constexpr int NS = 2;                           // stages of a warp
 
 // How a kind of weights is stored: the type of the tokens that it multiplies, the
-// bytes of a row's part in a stage (PIECE) and its values, and the bytes of a whole row.
+// bytes of a row's part in a stage (PIECE) and its values, and the bytes of a whole row;
+// CW: the warps that multiply (all of them route), NS: the stages of a warp.
 // The tokens' rows have zeros up to a multiple of BLOCK values, which is what a lane
 // group of the products takes at once.
+#ifndef Q4NS
+#define Q4NS 2
+#endif
 struct Q4 {};                                   // 4-bit weights (q4.cuh)
 template <typename WT> struct Stored;
 template <> struct Stored<float> {
   typedef float Act;
-  static constexpr int PIECE = 512, VALUES = 128, STAGE = 16 * PIECE, BLOCK = 1;
+  static constexpr int PIECE = 512, VALUES = 128, STAGE = 16 * PIECE, BLOCK = 1, CW = 8, NS = 2;
   static __host__ __device__ __forceinline__ int row(int K) { return K * 4; }
 };
 template <> struct Stored<bf16> {
   typedef bf16 Act;
-  static constexpr int PIECE = 512, VALUES = 256, STAGE = 16 * PIECE, BLOCK = 32;
+  static constexpr int PIECE = 512, VALUES = 256, STAGE = 16 * PIECE, BLOCK = 32, CW = 8, NS = 2;
   static __host__ __device__ __forceinline__ int row(int K) { return K * 2; }
 };
-// A stage of 4-bit weights ends with its scales: for each of up to 16 groups (of 32
-// inputs), those of the 16 rows.
+// A stage of 4-bit weights ends with its scales: for each of up to 8 groups (of 32
+// inputs), those of the 16 rows.  Widening them takes more than eight warps.
 template <> struct Stored<Q4> {
   typedef bf16 Act;
-  static constexpr int PIECE = 256, VALUES = 512, STAGE = 16 * PIECE + VALUES / 32 * 32, BLOCK = 128;
+  static constexpr int PIECE = 128, VALUES = 256, STAGE = 16 * PIECE + VALUES / 32 * 32, BLOCK = 128,
+                       CW = 16, NS = Q4NS;
   static __host__ __device__ __forceinline__ int row(int K) { return K / 2; }
 };
 template <typename WT> constexpr bool kBf16Tokens = sizeof(typename Stored<WT>::Act) == 2;
 template <typename WT> constexpr bool kQ4 = Stored<WT>::BLOCK == 128;
+template <typename WT> constexpr int kCThreads = Stored<WT>::CW * 32;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) & ~15; }
 // Bytes of one token's row in shared memory.  bf16: 64 past a multiple of 128, so
@@ -62,8 +66,8 @@ __host__ __device__ inline Plan make_plan(int T, int k, int E, int Fs, int tt) {
   Plan p;
   const int R = T * k;
   const int tiles = (E < R ? E : R) + R / tt + (Fs ? (T + tt - 1) / tt : 0);
-  int o = CW * NS * Stored<WT>::STAGE;   // (the router's and the selection's scratch lies there first)
-  p.off_red = o; o += 2 * CW * part_floats<WT>(tt) * 4;
+  int o = Stored<WT>::CW * Stored<WT>::NS * Stored<WT>::STAGE;   // (the router's and the selection's scratch lies there first)
+  p.off_red = o; o += 2 * Stored<WT>::CW * part_floats<WT>(tt) * 4;
   p.off_idx = o; o += up16(R * 2);
   p.off_gate = o; o += up16(R * 4);
   p.off_tok = o; o += up16(R * 2);
@@ -74,7 +78,7 @@ __host__ __device__ inline Plan make_plan(int T, int k, int E, int Fs, int tt) {
   p.rows_bytes = SMEM_MAX - o;
   return p;
 }
-static_assert((768 + WARPS * 256) * 4 <= CW * NS * Stored<Q4>::STAGE, "scratch");
+static_assert((768 + WARPS * 256) * 4 <= Stored<Q4>::CW * Stored<Q4>::NS * Stored<Q4>::STAGE, "scratch");
 // Tokens of a tile: as many as there is room for one tile of, or 0.
 template <typename WT>
 int tile_tokens(const DecodeArgs& a) {
@@ -180,7 +184,7 @@ __device__ __forceinline__ void load_tile(const DecodeArgs& a, const Routing& rt
   typedef typename Stored<WT>::Act Act;
   constexpr int BLOCK = Stored<WT>::BLOCK;
   const int pitch = row_pitch<WT>(K), plane = tl.n * pitch;
-  for (int t = threadIdx.x >> 5; t < tl.n; t += CW) {              // a warp a token
+  for (int t = threadIdx.x >> 5; t < tl.n; t += Stored<WT>::CW) {              // a warp a token
     const int tok = tl.e >= 0 && UP ? rt.tok[tl.start + t] : tl.start + t;
     const Act* x = static_cast<const Act*>(a.x) + (long long)tok * a.D;
     const float* h = (tl.e >= 0 ? a.hidden : a.hidden_s) + (long long)tok * K;
@@ -226,6 +230,9 @@ __device__ __forceinline__ void load_tile(const DecodeArgs& a, const Routing& rt
 __device__ __forceinline__ void copy16(uint32_t dst, const char* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 load_rows(uint32_t at) {
   uint4 v;
@@ -294,7 +301,7 @@ template <bool UP, bool Q4W> struct MmaProducts {
     if (!UP && isfinite(first)) sum += acc[t8][CH - 2][c] + acc[t8][CH - 1][c];
     return Q4W ? Q4_UNSCALE * sum : sum;
   }
-  __device__ __forceinline__ void begin(const char* rows, int pitch, int tokens, int lane) {
+  __device__ __forceinline__ void begin(const Part&, const char* rows, int pitch, int tokens, int lane) {
     const uint32_t at = smem_addr(rows) + (lane & 3) * 16;
     n = tokens;
     plane = n * pitch;
@@ -340,7 +347,7 @@ template <bool UP, bool Q4W> struct MmaProducts {
 };
 template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false> {
   static constexpr int PIECE = Stored<bf16>::PIECE;
-  __device__ __forceinline__ void stage(const Part&, uint32_t from, int v0, int left, int lane) {
+  __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
     const int g = lane >> 2, blocks = min(PIECE / 64, (left + 31) / 32);
     from += g * PIECE;
 #pragma unroll 4
@@ -367,33 +374,47 @@ template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false> {
 // 128 inputs in turn, lane c words 4 c to 4 c + 3.
 template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
   static constexpr int PIECE = Stored<Q4>::PIECE;
-  __device__ __forceinline__ void stage(const Part& p, uint32_t from, int v0, int left, int lane) {
-    const int g = lane >> 2, c = lane & 3, blocks = min(PIECE / 64, (left + 127) / 128);
-    const uint32_t slab = from + 16 * PIECE + g * 2;
-#pragma unroll 2
-    for (int u = 0; u < blocks; ++u) {
-      const uint32_t wat = (from + g * PIECE + u * 64 + c * 16) ^ ((g & 1) << 6);
-      const uint4 w0 = load_rows(wat), w1 = load_rows(wat + 8 * PIECE);
-      const uint32_t sat = slab + ((u * 128 + c * 32) >> p.log_g) * 32;
-      uint4 r[2][4];
-      q4_runs(w0, w1, load_scale(sat), load_scale(sat + 16), r);
+  static_assert(PIECE == 128, "two blocks of 128 inputs");
+  uint32_t code_at, scale_at[2];     // the lane's, in a stage
+  __device__ __forceinline__ void begin(const Part& p, const char* rows, int pitch, int tokens, int lane) {
+    MmaProducts<UP, true>::begin(p, rows, pitch, tokens, lane);
+    const int g = lane >> 2, c = lane & 3;
+    code_at = g * PIECE + ((c * 16) ^ ((g & 1) << 6));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 a = r[0][j], b = r[1][j];
-        auto products = [&](float (&c0)[4], float (&c1)[4], uint32_t x_at) {
-          const uint4 x = load_rows(x_at);
-          mma16816(c0, a.x, b.x, a.y, b.y, x.x, x.y);
-          mma16816(c1, a.z, b.z, a.w, b.w, x.z, x.w);
-        };
-        const uint32_t off = (v0 + u * 128) * 2 + j * 64;
-        products(this->acc[0][0], this->acc[0][1], this->at0 + off);
-        if (!UP) products(this->acc[0][this->CH - 2], this->acc[0][this->CH - 1], this->at0 + this->plane + off);
-        if (this->n > 8) {
-          products(this->acc[1][0], this->acc[1][1], this->at1 + off);
-          if (!UP) products(this->acc[1][this->CH - 2], this->acc[1][this->CH - 1], this->at1 + this->plane + off);
+    for (int u = 0; u < 2; ++u) scale_at[u] = 16 * PIECE + g * 2 + ((u * 128 + c * 32) >> p.log_g) * 32;
+  }
+  template <int T8>
+  __device__ __forceinline__ void block(uint32_t codes, uint32_t scales, const uint32_t (&x)[2]) {
+    const uint4 w0 = load_rows(codes), w1 = load_rows(codes + 8 * PIECE);
+    uint4 r[2][4];
+    q4_runs(w0, w1, load_scale(scales), load_scale(scales + 16), r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 a = r[0][j], b = r[1][j];
+#pragma unroll
+      for (int t = 0; t < T8; ++t)
+#pragma unroll
+        for (int h = 0; h < (UP ? 1 : 2); ++h) {
+          const uint4 v = load_rows(x[t] + (h ? this->plane : 0) + j * 64);
+          mma16816(this->acc[t][2 * h], a.x, b.x, a.y, b.y, v.x, v.y);
+          mma16816(this->acc[t][2 * h + 1], a.z, b.z, a.w, b.w, v.z, v.w);
         }
-      }
     }
+  }
+  template <int T8>
+  __device__ __forceinline__ void blocks(uint32_t from, int v0, int left) {
+    uint32_t x[2] = {this->at0 + v0 * 2, this->at1 + v0 * 2};
+    block<T8>(from + code_at, from + scale_at[0], x);
+    if (left > 128) {
+      x[0] += 256;
+      x[1] += 256;
+      block<T8>(from + (code_at ^ 64), from + scale_at[1], x);
+    }
+  }
+  __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
+    if (left <= 0) return;
+    if (this->n > 8) blocks<2>(from, v0, left);
+    else blocks<1>(from, v0, left);
   }
 };
 // Products<float>: a lane multiplies 4 values of each row with 4 of each token.
@@ -401,7 +422,7 @@ template <bool UP> struct Products<float, UP> {
   uint32_t at;
   int pitch, n;
   float acc[64];               // row * 4 + token
-  __device__ __forceinline__ void begin(const char* rows, int row_bytes, int tokens, int lane) {
+  __device__ __forceinline__ void begin(const Part&, const char* rows, int row_bytes, int tokens, int lane) {
     at = smem_addr(rows) + lane * 16;
     pitch = row_bytes;
     n = tokens;
@@ -409,7 +430,7 @@ template <bool UP> struct Products<float, UP> {
     for (int i = 0; i < 64; ++i) acc[i] = 0.f;
   }
   static constexpr int PIECE = Stored<float>::PIECE;
-  __device__ __forceinline__ void stage(const Part&, uint32_t from, int v0, int left, int lane) {
+  __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
     if (lane * 4 >= left) return;
     float x[4][4];
 #pragma unroll
@@ -466,12 +487,14 @@ template <bool UP> struct Products<float, UP> {
 // Warps to an item: the number that takes the fewest quarter stages for the
 // block's share, an item shared by several warps counting one more for adding
 // their parts.
+template <int CW>
 __device__ __forceinline__ int warps_per_item(int items, int stages) {
-  static_assert(CW == 8, "three halvings");
+  static_assert(CW == 8 || CW == 16, "halvings");
+  constexpr int L = CW == 8 ? 3 : 4;
   int best = 1, cost = 0x7fffffff;
 #pragma unroll 1
-  for (int l = 0; l <= 3; ++l) {
-    const int c = ((items + (CW >> l) - 1) >> (3 - l)) *
+  for (int l = 0; l <= L; ++l) {
+    const int c = ((items + (CW >> l) - 1) >> (L - l)) *
                   (((stages + (1 << l) - 1) >> l) * 4 + (l > 0 ? 1 : 0));
     if (c < cost) {
       cost = c;
@@ -481,22 +504,45 @@ __device__ __forceinline__ int warps_per_item(int items, int stages) {
   return best;
 }
 
-// The items of a part, by the multiplying warps.  Where `flag` is given, the grid
-// barrier before the down projection stands between the first weight copies and
-// the tiles' tokens.
-template <typename WT, bool UP>
-__device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, const Routing& rt, int tt,
+// The layer's own tokens and results: routed tiles and the shared branch's.  Where `flag`
+// is given, the grid barrier before the down projection stands between the first weight
+// copies and the tiles' tokens.
+template <typename WT, bool UP> struct LayerJob {
+  const DecodeArgs& a;
+  const Routing& rt;
+  int* flag;
+  __device__ __forceinline__ void wait_tokens() const {
+    if (!UP && flag != nullptr) grid_barrier<kCThreads<WT>>(a.ctl, 1, flag);
+  }
+  __device__ __forceinline__ void load(const Tile& tl, int K, char* rows) const {
+    load_tile<WT, UP>(a, rt, tl, K, rows);
+  }
+  // the bias of row `lane` of an item
+  __device__ __forceinline__ float bias(const Part& p, const Tile& tl, int block, int lane) const {
+    if (!UP || a.b1 == nullptr || lane >= 16 || block * 16 + lane >= p.width) return 0.f;
+    return __ldg(a.b1 + (long long)tl.e * a.F + block * 16 + lane);
+  }
+  __device__ __forceinline__ void out(const Part&, const Tile& tl, int block, int row, int tok, float v0,
+                                      float v1, float b0, float b1) const {
+    emit<UP>(a, tl, block, row, tok, v0, v1, b0, b1);
+  }
+};
+
+// The items of a part, by the multiplying warps.
+template <typename WT, bool UP, typename Job>
+__device__ __forceinline__ void compute(const Job& job, const Part& p, const Tile* tiles, int tt,
                                         int* row_at, char* rows, int rows_bytes, float* red,
-                                        uint32_t ring, int* flag) {
+                                        uint32_t ring) {
   if (p.lo >= p.hi) {
-    if (!UP && flag != nullptr) grid_barrier<CTHREADS>(a.ctl, 1, flag);
+    job.wait_tokens();
     return;
   }
+  constexpr int CW = Stored<WT>::CW, NS = Stored<WT>::NS, CTHREADS = kCThreads<WT>;
   constexpr int PIECE = Stored<WT>::PIECE, STAGE = Stored<WT>::STAGE;
   constexpr int SV = Stored<WT>::VALUES;                       // values of a row in a stage
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int K = p.K, stages = (K + SV - 1) / SV;
-  const int KS = warps_per_item(p.hi - p.lo, stages), groups = CW >> (__ffs(KS) - 1);
+  const int KS = warps_per_item<CW>(p.hi - p.lo, stages), groups = CW >> (__ffs(KS) - 1);
   const int lg = __ffs(KS) - 1, mine = warp >> lg, ks = warp & (KS - 1);
   const int steps = (stages + KS - 1) >> lg;
   const int pitch = row_pitch<WT>(K), size = part_floats<WT>(tt);
@@ -506,33 +552,42 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
   // the next stage to be copied: item, its tile and block, step; rows 0..7 of it
   int li = p.lo + mine, lt = li / p.per, lb = li - lt * p.per, ls = 0, put_slot = 0;
   int it = lt, ib = lb;        // (where the computing starts, too)
-  const char* lp = li < p.hi ? item_rows<WT>(p, rt.tiles, lt, lb) : nullptr;
-  const char* sp = kQ4<WT> && li < p.hi ? item_scales(p, rt.tiles, lt, lb) : nullptr;
+  const char *lp = nullptr, *sp = nullptr;     // (4-bit weights: this lane's, of the next stage)
+  const uint32_t q4_to = (ring + (lane >> 3) * PIECE + (lane & 7) * 16) ^ ((lane >> 3 & 1) << 6);
+  auto begin_item = [&] {
+    lp = item_rows<WT>(p, tiles, lt, lb);
+    if constexpr (kQ4<WT>) {
+      lp += (long long)(lane >> 3) * row + ks * PIECE + (lane & 7) * 16;
+      sp = item_scales(p, tiles, lt, lb) +
+           ((long long)ks * (SV >> p.log_g) + (lane >> 1)) * 2 * p.width + (lane & 1) * p.second_s;
+    }
+  };
+  if (li < p.hi) begin_item();
   auto put = [&] {
     const int v0 = (ls * KS + ks) * SV;
     if (li < p.hi && v0 < K) {
       // row r's 16-byte pieces change places with their neighbours 64 bytes on
       // for odd r, so that the rows a quarter-warp reads fall on different banks
       if constexpr (kQ4<WT>) {
-        // two rows at a time, then the scales: lane 2 g + h has group g's of half h
-        const uint32_t dst = ring + put_slot * STAGE + (lane >> 4) * PIECE + (lane & 15) * 16;
-        const int at = v0 / 2 + (lane & 15) * 16;
-        const bool on = at < row, upper = has_upper(p, lb);
-        const char* src = lp + (lane >> 4) * row + (on ? at : 0);
-#pragma unroll
-        for (int r = 0; r < 8; r += 2) copy16((dst + r * PIECE) ^ (lane >> 4 << 6), src + (long long)r * row, on);
-        if (upper) {
-          src += p.second;
-#pragma unroll
-          for (int r = 0; r < 8; r += 2)
-            copy16((dst + (8 + r) * PIECE) ^ (lane >> 4 << 6), src + (long long)r * row, on);
+        // four rows at a time, then the scales: lane 2 g + h has group g's of half h.
+        // What lies in the place of codes past the row's end are codes, which meet
+        // zeros of x; their scales are zeros.
+        const bool upper = has_upper(p, lb);
+        if (v0 / 2 + (lane & 7) * 16 < row) {
+          const uint32_t dst = q4_to + put_slot * STAGE;
+          copy16(dst, lp);
+          copy16(dst + 4 * PIECE, lp + 4ll * row);
+          if (upper) {
+            copy16(dst + 8 * PIECE, lp + p.second);
+            copy16(dst + 12 * PIECE, lp + p.second + 4ll * row);
+          }
         }
-        const int g = lane >> 1, h = lane & 1, gi = (v0 >> p.log_g) + g;
-        if (g < SV >> p.log_g) {
-          const bool there = gi < p.groups && (h == 0 || upper);
-          copy16(ring + put_slot * STAGE + 16 * PIECE + lane * 16,
-                 sp + (there ? gi * 2ll * p.width + h * p.second_s : 0), there);
+        if (lane < 2 * (SV >> p.log_g)) {
+          const bool there = (v0 >> p.log_g) + (lane >> 1) < p.groups && (upper || !(lane & 1));
+          copy16(ring + put_slot * STAGE + 16 * PIECE + lane * 16, there ? sp : p.s, there);
         }
+        lp += KS * PIECE;
+        sp += (long long)KS * (SV >> p.log_g) * 2 * p.width;
       } else {
         const uint32_t dst = ring + put_slot * STAGE + lane * 16;
         const int at = v0 * (PIECE / SV) + lane * 16;
@@ -554,17 +609,21 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
     ls = 0;
     li += groups;
     lb += groups;
+    if (kQ4<WT>) {
+      if (li >= p.hi) return;
+      while (lb >= p.per) { lb -= p.per; ++lt; }
+      begin_item();
+      return;
+    }
     lp += item_step;
-    if (kQ4<WT>) sp += (long long)groups * p.rows * 2;
     if (lb >= p.per && li < p.hi) {
       do { lb -= p.per; ++lt; } while (lb >= p.per);
-      lp = item_rows<WT>(p, rt.tiles, lt, lb);
-      if (kQ4<WT>) sp = item_scales(p, rt.tiles, lt, lb);
+      begin_item();
     }
   };
 #pragma unroll
   for (int u = 0; u < NS; ++u) put();
-  if (!UP && flag != nullptr) grid_barrier<CTHREADS>(a.ctl, 1, flag);
+  job.wait_tokens();
 
   // what is being computed: item, its tile and block
   int i = p.lo + mine, parity = 0, slot = 0;
@@ -575,10 +634,10 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
     bar_sync<CTHREADS>();      // the last ones are no longer read
     const int first = t;
     for (; t * p.per < p.hi; ++t) {
-      const Tile tl = rt.tiles[p.t0 + t];
+      const Tile tl = tiles[p.t0 + t];
       const int need = tl.n * pitch * (!UP && kBf16Tokens<WT> ? 2 : 1);
       if (t > first && used + need > rows_bytes) break;
-      load_tile<WT, UP>(a, rt, tl, K, rows + used);
+      job.load(tl, K, rows + used);
       if (threadIdx.x == 0) row_at[t] = used;
       used += need;
     }
@@ -588,18 +647,16 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
     bar_sync<CTHREADS>();
 
     while (i < b_hi) {
-      const Tile tl = rt.tiles[p.t0 + it];
+      const Tile tl = tiles[p.t0 + it];
       Products<WT, UP> sum;
-      sum.begin(rows + row_at[it], pitch, tl.n, lane);
+      sum.begin(p, rows + row_at[it], pitch, tl.n, lane);
       // the biases of the item's rows, one a lane, on their way from here on
-      float bias = 0.f;
-      if (UP && a.b1 != nullptr && lane < 16 && ib * 16 + lane < p.width)
-        bias = __ldg(a.b1 + (long long)tl.e * a.F + ib * 16 + lane);
+      const float bias = job.bias(p, tl, ib, lane);
       for (int s = 0; s < steps; ++s) {
         asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
         __syncwarp();
         const int v0 = (s * KS + ks) * SV;
-        sum.stage(p, ring + slot * STAGE, v0, K - v0, lane);
+        sum.stage(ring + slot * STAGE, v0, K - v0, lane);
         __syncwarp();
         put();
         slot = slot + 1 == NS ? 0 : slot + 1;
@@ -607,7 +664,7 @@ __device__ __forceinline__ void compute(const DecodeArgs& a, const Part& p, cons
       auto out = [&](int row, int tok, float v0, float v1) {       // by whole warps
         const float b0 = UP ? __shfl_sync(0xffffffffu, bias, row) : 0.f;
         const float b1 = UP ? __shfl_sync(0xffffffffu, bias, row + 8) : 0.f;
-        emit<UP>(a, tl, ib, row, tok, v0, v1, b0, b1);
+        job.out(p, tl, ib, row, tok, v0, v1, b0, b1);
       };
       if (KS == 1) {
         sum.each(lane, out);

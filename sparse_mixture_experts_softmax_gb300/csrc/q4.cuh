@@ -35,8 +35,12 @@ __device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t scale2) {
 // factors are normal numbers, 2^-121 to 2^3, take it; a warp with another among its
 // lanes' goes by q4_word.
 constexpr float Q4_UNSCALE = 256.f;
-__device__ __forceinline__ bool q4_fast(uint32_t bits) {         // of a bf16 scale
-  return (bits & 0x7fffu) - 0x0300u < 0x3e00u;
+// Whether both of two bf16 scales (one in each half) take it.
+__device__ __forceinline__ bool q4_fast(uint32_t scales) {
+  const __nv_bfloat162 a = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&scales));
+  const uint32_t lo = 0x03000300u, hi = 0x41004100u;
+  return __hbge2(a, *reinterpret_cast<const __nv_bfloat162*>(&lo)) &&
+         __hblt2(a, *reinterpret_cast<const __nv_bfloat162*>(&hi));
 }
 // Two runs of 32 inputs, by a whole warp: one branch that all its lanes take alike.
 // bits0, bits1: the runs' scales.
@@ -44,11 +48,12 @@ __device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32
                                         uint4 (&v)[2][4]) {
   const uint32_t r[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
   const uint32_t two[2] = {__byte_perm(bits0, 0u, 0x1010), __byte_perm(bits1, 0u, 0x1010)};
-  if (__all_sync(0xffffffffu, q4_fast(bits0) && q4_fast(bits1))) {
+  if (__all_sync(0xffffffffu, q4_fast(__byte_perm(bits0, bits1, 0x5410)))) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t low = two[u] + 0x3e803e80u, high = two[u] + 0x3c803c80u;    // 2^125, 2^121
-      const uint32_t add = (two[u] - 0x02800280u) ^ 0x80008000u;                 // -2^-5
+      const uint32_t low = q4_fma(two[u], 0x7e007e00u, 0x80008000u);             // 2^125
+      const uint32_t high = q4_fma(two[u], 0x7c007c00u, 0x80008000u);            // 2^121
+      const uint32_t add = q4_fma(two[u], 0xbd00bd00u, 0x80008000u);             // -2^-5
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t w = r[u][i], x = w >> 8;
@@ -64,6 +69,31 @@ __device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32
       for (int i = 0; i < 4; ++i) v[u][i] = q4_word(r[u][i], scale2);
     }
   }
+}
+
+// Inclusive scan over the threads of a block (those without a value pass a neutral one):
+// the running maximum or the running sum.  part: 32 words of shared memory of its own.
+template <bool MAX>
+__device__ __forceinline__ int q4_block_scan(int v, int* part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = MAX ? max(v, u) : v + u;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v = MAX ? max(v, part[w]) : v + part[w];
+  return v;
+}
+// Thread e's offset, e <= E, of the given ones (nullptr: one expert with all R rows)
+// clamped to a sequence that does not decrease within [0, R].  By the whole block, of more
+// than E threads.
+__device__ __forceinline__ int clamped_offset(const int* offsets, int E, int R, int* part) {
+  const int e = threadIdx.x;
+  int v = 0;
+  if (e <= E) v = offsets != nullptr ? min(max(offsets[e], 0), R) : e * R;
+  return q4_block_scan<true>(v, part);
 }
 
 }  // namespace moe

@@ -95,30 +95,12 @@ __device__ __forceinline__ Tile tile_at(int t, const Params& p, const Table& tb)
   return T;
 }
 
-// Inclusive scan over the block's first MAX_E + 1 threads (others pass the neutral
-// element): the running maximum or the running sum.
-template <bool MAX>
-__device__ __forceinline__ int block_scan(int v, int* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v = MAX ? max(v, u) : v + u;
-  }
-  if (lane == 31) part[warp] = v;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) v = MAX ? max(v, part[w]) : v + part[w];
-  return v;
-}
-
 // Offsets clamped to a sequence that does not decrease within [0, R], and the row tiles:
 // an expert's rows in tiles of equal size, a multiple of 16, so that none is much
 // smaller than the others.
 __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
   const int e = threadIdx.x;
-  int v = 0;
-  if (e <= p.E) v = p.offsets ? min(max(p.offsets[e], 0), p.R) : e * p.R;
-  v = block_scan<true>(v, tb.scan[0]);
+  const int v = clamped_offset(p.offsets, p.E, p.R, tb.scan[0]);
   if (e <= p.E) tb.offs[e] = v;
   __syncthreads();
   int tiles = 0;
@@ -129,7 +111,7 @@ __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
     tiles = (rows + step - 1) / step;
     tb.step[e] = step;
   }
-  const int incl = block_scan<false>(tiles, tb.scan[1]);
+  const int incl = q4_block_scan<false>(tiles, tb.scan[1]);
   if (e < p.E) tb.first[e + 1] = incl;
   if (e == 0) tb.first[0] = 0;
   __syncthreads();

@@ -1,67 +1,153 @@
-// The matrix product grouped by expert with 4-bit weights.
-#include <float.h>
+// The matrix product grouped by expert with 4-bit weights, for few rows, and the choice
+// between this kernel and the one for many (q4_gemm.cu).
+//
+// A few rows of an expert are bound by reading its weights once, and a single matrix has
+// to be spread over all SMs: the few-token layer's way (decode_experts.cuh), 16 rows of
+// a matrix times up to 16 rows of x an item, items of equal bytes dealt to the blocks,
+// the warps of a block sharing an item's inputs where it has few items.
+#include <limits.h>
 
-#include "kernels.h"
-#include "q4.cuh"
+#include "decode_experts.cuh"
 #include "q4.h"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float act_of(int act, float h1, float h3) {
-  if (act == 2) return silu_f(h1) * h3;
-  if (act == 1) return gelu_tanh_f(h1);
-  return act == 0 && h1 < 0.f ? 0.f : h1;        // a NaN stays one
+constexpr int CW_ = Stored<Q4>::CW;
+static_assert(CW_ == WARPS, "all warps multiply");
+constexpr int MAX_ROWS = 4096;               // of a call (their tiles lie in shared memory)
+struct RowsPlan {
+  int off_red, off_tile, off_at, off_rows, rows_bytes, max_tiles;
+};
+__host__ __device__ inline RowsPlan rows_plan(int R, int E, int tt) {
+  RowsPlan P;
+  P.max_tiles = (E < R ? E : R) + R / tt;
+  int o = CW_ * Stored<Q4>::NS * Stored<Q4>::STAGE;
+  P.off_red = o; o += 2 * CW_ * part_floats<Q4>(tt) * 4;
+  P.off_tile = o; o += up16(P.max_tiles * 8);
+  P.off_at = o; o += up16(P.max_tiles * 4);
+  P.off_rows = o;
+  P.rows_bytes = SMEM_MAX - o;
+  return P;
 }
 
-// A block: one row, 64 outputs; a warp takes eight of them, its lanes words of K.
-__global__ void __launch_bounds__(256) q4_rows_kernel(const Q4Product p) {
-  __shared__ int expert;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blocks_n = (p.N + 63) / 64;
-  const int r = blockIdx.x / blocks_n, n0 = (blockIdx.x % blocks_n) * 64 + warp * 8;
-  pdl_begin();
-  if (threadIdx.x == 0) {
-    int prev = p.offsets ? min(max(p.offsets[0], 0), p.R) : 0;
-    expert = p.offsets ? -1 : 0;
-    for (int e = 0; p.offsets && e < p.E; ++e) {
-      const int hi = min(max(p.offsets[e + 1], prev), p.R);
-      if (r >= prev && r < hi) { expert = e; break; }
-      prev = hi;
-    }
-  }
-  __syncthreads();
-  const int e = expert, words = p.K / 8, groups = (p.K + p.G - 1) / p.G;
-  if (e < 0) return;
-  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.x) + (long long)r * p.K);
-  for (int n = n0; n < min(n0 + 8, p.N); ++n) {
-    float sum[2] = {0.f, 0.f};
-    for (int m = 0; m < (p.act == 2 ? 2 : 1); ++m) {
-      const uint32_t* codes = static_cast<const uint32_t*>(m ? p.codes3 : p.codes) +
-                              ((long long)e * p.N + n) * words;
-      const bf16* scales = static_cast<const bf16*>(m ? p.scales3 : p.scales) + (long long)e * groups * p.N + n;
-      for (int j = lane; j < words; j += 32) {
-        const uint4 w = q4_word(codes[j], 0x10001u * __bfloat16_as_ushort(scales[(long long)(j * 8 / p.G) * p.N])), v = x[j];
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[m] = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), sum[m]);
-          sum[m] = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u), sum[m]);
-        }
+// Tokens straight from x, results straight to c.
+struct RowsJob {
+  const Q4Product& p;
+  __device__ __forceinline__ void wait_tokens() const {}
+  __device__ __forceinline__ void load(const Tile& tl, int K, char* rows) const {
+    const int pitch = row_pitch<Q4>(K), pieces = (K + 127) / 128 * 16;       // of 8 values
+    for (int t = threadIdx.x >> 5; t < tl.n; t += CW_) {
+      const bf16* x = static_cast<const bf16*>(p.x) + (long long)(tl.start + t) * K;
+#pragma unroll 4
+      for (int c = threadIdx.x & 31; c < pieces; c += 32) {
+        const int at = (c & ~15) | (c & 3) << 2 | (c >> 2 & 3);             // (as load_tile has it)
+        *reinterpret_cast<uint4*>(rows + t * pitch + at * 16) =
+            c * 8 < K ? __ldg(reinterpret_cast<const uint4*>(x + c * 8)) : make_uint4(0u, 0u, 0u, 0u);
       }
-      sum[m] = warp_sum(sum[m]);
     }
-    if (p.bias != nullptr) sum[0] += p.bias[(long long)e * p.N + n];
-    if (lane == 0)
-      static_cast<bf16*>(p.c)[(long long)r * p.N + n] = __float2bfloat16_rn(act_of(p.act, sum[0], sum[1]));
   }
+  __device__ __forceinline__ float bias(const Part& pt, const Tile& tl, int block, int lane) const {
+    if (p.bias == nullptr || lane >= 16 || block * 16 + lane >= pt.width) return 0.f;
+    return __ldg(p.bias + (long long)tl.e * p.N + block * 16 + lane);
+  }
+  __device__ __forceinline__ void out(const Part& pt, const Tile& tl, int block, int row, int tok, float v0,
+                                      float v1, float b0, float b1) const {
+    if (tok >= tl.n) return;
+    bf16* c = static_cast<bf16*>(p.c) + (long long)(tl.start + tok) * p.N + block * pt.rows + row;
+    if (p.act == 2) {
+      *c = __float2bfloat16_rn(silu_f(v0) * v1);
+      return;
+    }
+    c[0] = __float2bfloat16_rn(act(v0 + b0));
+    if (block * 16 + 8 < pt.width) c[8] = __float2bfloat16_rn(act(v1 + b1));
+  }
+  __device__ __forceinline__ float act(float v) const {
+    if (p.act == 1) return gelu_tanh_f(v);
+    return p.act == 0 && v < 0.f ? 0.f : v;      // a NaN stays one
+  }
+};
+
+__global__ void __launch_bounds__(THREADS, 1)
+q4_rows_kernel(const __grid_constant__ Q4Product p, const int tt) {
+  extern __shared__ __align__(128) char sm[];
+  __shared__ int n_tiles;
+  int* scan = reinterpret_cast<int*>(sm);          // (where the weights' buffers lie later)
+  int* offs = scan + 64;                           // [E + 1]
+  const RowsPlan P = rows_plan(p.R, p.E, tt);
+  Tile* tiles = reinterpret_cast<Tile*>(sm + P.off_tile);
+  const int e = threadIdx.x;
+  pdl_begin();
+  const int lo = clamped_offset(p.offsets, p.E, p.R, scan);
+  if (e <= p.E) offs[e] = lo;
+  __syncthreads();
+  const int rows = e < p.E ? offs[e + 1] - lo : 0, mine = (rows + tt - 1) / tt;
+  const int behind = q4_block_scan<false>(mine, scan + 32);
+  for (int i = 0; i < mine; ++i)
+    tiles[behind - mine + i] = Tile{(short)e, (short)min(tt, rows - i * tt), lo + i * tt};
+  if (e == THREADS - 1) n_tiles = behind;
+  __syncthreads();
+
+  Part pt;
+  const bool pair = p.act == 2;
+  pt.rows = pair ? 8 : 16;
+  pt.K = p.K;
+  pt.width = p.N;
+  pt.per = (p.N + pt.rows - 1) / pt.rows;
+  pt.t0 = 0;
+  const long long items = (long long)n_tiles * pt.per;
+  pt.lo = (int)(items * blockIdx.x / gridDim.x);
+  pt.hi = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  pt.w = static_cast<const char*>(p.codes);
+  pt.s = static_cast<const char*>(p.scales);
+  pt.second = !pair ? 8ll * Stored<Q4>::row(p.K) : static_cast<const char*>(p.codes3) - pt.w;
+  pt.second_s = !pair ? 16 : static_cast<const char*>(p.scales3) - pt.s;
+  pt.log_g = p.G == 32 ? 5 : p.G == 64 ? 6 : 7;
+  pt.groups = (p.K + p.G - 1) / p.G;
+  const uint32_t ring = smem_addr(sm) + (threadIdx.x >> 5) * Stored<Q4>::NS * Stored<Q4>::STAGE;
+  compute<Q4, true>(RowsJob{p}, pt, tiles, tt, reinterpret_cast<int*>(sm + P.off_at), sm + P.off_rows,
+                    P.rows_bytes, reinterpret_cast<float*>(sm + P.off_red), ring);
+}
+
+// Rows of a tile: as many as there is room for one tile of, or 0.
+int tile_rows(const Q4Product& p) {
+  const long long pitch = row_pitch<Q4>(p.K);
+  for (int tt = most_tokens<Q4>(); tt >= 1; --tt)
+    if (tt * pitch <= rows_plan(p.R, p.E, tt).rows_bytes) return tt;
+  return 0;
+}
+
+cudaError_t launch_q4_rows(const Q4Product& p, int tt, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t err = ensure_dynamic_smem(q4_rows_kernel, SMEM_MAX, attr_done);
+  if (err != cudaSuccess) return err;
+  static std::atomic<int> sms{0};
+  int n = sms.load(std::memory_order_relaxed);
+  if (n == 0) {
+    int dev = 0;
+    if ((err = cudaGetDevice(&dev)) != cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+      return err;
+    sms.store(n, std::memory_order_relaxed);
+  }
+  // a block an SM, or fewer where each would have less than 8 KB of weights
+  const long long experts = p.E < p.R ? p.E : p.R;
+  const long long blocks = (experts * p.N * (p.K / 2) * (p.act == 2 ? 2 : 1) + 8191) / 8192;
+  return launch_pdl(q4_rows_kernel, dim3((unsigned)(blocks < n ? blocks : n)), dim3(THREADS), SMEM_MAX,
+                    st, p, tt);
 }
 
 }  // namespace
 
 cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st) {
-  if (p.R > 16) return launch_q4_gemm(p, st);
-  return launch_pdl(q4_rows_kernel, dim3((unsigned)p.R * ((p.N + 63) / 64)), dim3(256), 0, st, p);
+  const int tt = p.R <= MAX_ROWS ? tile_rows(p) : 0;
+  if (tt == 0) return launch_q4_gemm(p, st);
+  // Every row tile reads its expert's matrix again, most of it from L2
+  const long long tiles = (p.E < p.R ? p.E : p.R) + p.R / tt;
+  const long long bytes = tiles * p.N * (p.K / 2) * (p.act == 2 ? 2 : 1);
+  const bool few = 2ll * p.R <= (long long)tt * p.E || bytes <= (32ll << 20);
+  if (!few || tiles * ((p.N + 7) / 8) > INT_MAX) return launch_q4_gemm(p, st);
+  return launch_q4_rows(p, tt, st);
 }
 
 }  // namespace moe
