@@ -16,9 +16,6 @@ constexpr int WARPS = 16, THREADS = WARPS * 32;
 // CW: the warps that multiply (all of them route), NS: the stages of a warp.
 // The tokens' rows have zeros up to a multiple of BLOCK values, which is what a lane
 // group of the products takes at once.
-#ifndef Q4NS
-#define Q4NS 2
-#endif
 struct Q4 {};                                   // 4-bit weights (q4.cuh)
 template <typename WT> struct Stored;
 template <> struct Stored<float> {
@@ -31,12 +28,12 @@ template <> struct Stored<bf16> {
   static constexpr int PIECE = 512, VALUES = 256, STAGE = 16 * PIECE, BLOCK = 32, CW = 8, NS = 2;
   static __host__ __device__ __forceinline__ int row(int K) { return K * 2; }
 };
-// A stage of 4-bit weights ends with its scales: for each of up to 8 groups (of 32
+// A stage of 4-bit weights ends with its scales: for each of up to 16 groups (of 32
 // inputs), those of the 16 rows.  Widening them takes more than eight warps.
 template <> struct Stored<Q4> {
   typedef bf16 Act;
-  static constexpr int PIECE = 128, VALUES = 256, STAGE = 16 * PIECE + VALUES / 32 * 32, BLOCK = 128,
-                       CW = 16, NS = Q4NS;
+  static constexpr int PIECE = 256, VALUES = 512, STAGE = 16 * PIECE + VALUES / 32 * 32, BLOCK = 128,
+                       CW = 16, NS = 2;
   static __host__ __device__ __forceinline__ int row(int K) { return K / 2; }
 };
 template <typename WT> constexpr bool kBf16Tokens = sizeof(typename Stored<WT>::Act) == 2;
@@ -231,8 +228,24 @@ __device__ __forceinline__ void copy16(uint32_t dst, const char* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes of each of four rows, two rows of a stage of 256-byte pieces apart, where on.
+__device__ __forceinline__ void copy16_rows(uint32_t dst, const char* src, long long two_rows, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\tadd.s64 a, %1, %2;\n\t"
+      "@p cp.async.cg.shared.global [%0+512], [a], 16;\n\tadd.s64 a, a, %2;\n\t"
+      "@p cp.async.cg.shared.global [%0+1024], [a], 16;\n\tadd.s64 a, a, %2;\n\t"
+      "@p cp.async.cg.shared.global [%0+1536], [a], 16;\n\t}" ::"r"(dst), "l"(src), "l"(two_rows),
+      "r"((int)on)
+      : "memory");
+}
+// 16 bytes, or zeros, where on.
+__device__ __forceinline__ void copy16_or0(uint32_t dst, const char* src, bool there, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst), "l"(src), "r"(there ? 16 : 0),
+      "r"((int)on)
+      : "memory");
 }
 __device__ __forceinline__ uint4 load_rows(uint32_t at) {
   uint4 v;
@@ -374,14 +387,14 @@ template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false> {
 // 128 inputs in turn, lane c words 4 c to 4 c + 3.
 template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
   static constexpr int PIECE = Stored<Q4>::PIECE;
-  static_assert(PIECE == 128, "two blocks of 128 inputs");
-  uint32_t code_at, scale_at[2];     // the lane's, in a stage
+  static_assert(PIECE == 256, "four blocks of 128 inputs");
+  uint32_t code_at, scale_at, scale_step;      // the lane's, in a stage; from one block to the next
   __device__ __forceinline__ void begin(const Part& p, const char* rows, int pitch, int tokens, int lane) {
     MmaProducts<UP, true>::begin(p, rows, pitch, tokens, lane);
     const int g = lane >> 2, c = lane & 3;
     code_at = g * PIECE + ((c * 16) ^ ((g & 1) << 6));
-#pragma unroll
-    for (int u = 0; u < 2; ++u) scale_at[u] = 16 * PIECE + g * 2 + ((u * 128 + c * 32) >> p.log_g) * 32;
+    scale_at = 16 * PIECE + g * 2 + (c * 32 >> p.log_g) * 32;
+    scale_step = 128 * 32 >> p.log_g;
   }
   template <int T8>
   __device__ __forceinline__ void block(uint32_t codes, uint32_t scales, const uint32_t (&x)[2]) {
@@ -402,19 +415,22 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
     }
   }
   template <int T8>
-  __device__ __forceinline__ void blocks(uint32_t from, int v0, int left) {
+  __device__ __forceinline__ void blocks(uint32_t from, int v0, int end) {
     uint32_t x[2] = {this->at0 + v0 * 2, this->at1 + v0 * 2};
-    block<T8>(from + code_at, from + scale_at[0], x);
-    if (left > 128) {
+    uint32_t scales = from + scale_at;
+    const uint32_t codes = from + code_at;       // (a stage starts at a multiple of 256 bytes)
+#pragma unroll 2
+    for (int u = 0; u < end; u += 64) {
+      block<T8>(codes ^ u, scales, x);
+      scales += scale_step;
       x[0] += 256;
       x[1] += 256;
-      block<T8>(from + (code_at ^ 64), from + scale_at[1], x);
     }
   }
   __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
-    if (left <= 0) return;
-    if (this->n > 8) blocks<2>(from, v0, left);
-    else blocks<1>(from, v0, left);
+    const int end = min(PIECE, (left + 127) / 128 * 64);
+    if (this->n > 8) blocks<2>(from, v0, end);
+    else blocks<1>(from, v0, end);
   }
 };
 // Products<float>: a lane multiplies 4 values of each row with 4 of each token.
@@ -553,41 +569,41 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
   int li = p.lo + mine, lt = li / p.per, lb = li - lt * p.per, ls = 0, put_slot = 0;
   int it = lt, ib = lb;        // (where the computing starts, too)
   const char *lp = nullptr, *sp = nullptr;     // (4-bit weights: this lane's, of the next stage)
-  const uint32_t q4_to = (ring + (lane >> 3) * PIECE + (lane & 7) * 16) ^ ((lane >> 3 & 1) << 6);
+  // where it copies codes to, the row's bytes from there on, and groups from its own on
+  const uint32_t q4_to = (ring + (lane >> 4) * PIECE + (lane & 15) * 16) ^ (lane >> 4 << 6);
+  const bool q4_scales = lane < 2 * (SV >> p.log_g);
+  const long long q4_sp_step = 2ll * KS * (SV >> p.log_g) * p.width;
+  int q4_left = 0, q4_groups = 0;
   auto begin_item = [&] {
     lp = item_rows<WT>(p, tiles, lt, lb);
     if constexpr (kQ4<WT>) {
-      lp += (long long)(lane >> 3) * row + ks * PIECE + (lane & 7) * 16;
-      sp = item_scales(p, tiles, lt, lb) +
-           ((long long)ks * (SV >> p.log_g) + (lane >> 1)) * 2 * p.width + (lane & 1) * p.second_s;
+      const int at = ks * PIECE + (lane & 15) * 16, g = ks * (SV >> p.log_g) + (lane >> 1);
+      lp += (lane >> 4) * row + at;
+      sp = item_scales(p, tiles, lt, lb) + 2ll * g * p.width + (lane & 1) * p.second_s;
+      q4_left = row - at;
+      q4_groups = p.groups - g;
     }
   };
   if (li < p.hi) begin_item();
   auto put = [&] {
-    const int v0 = (ls * KS + ks) * SV;
-    if (li < p.hi && v0 < K) {
+    const int v0 = kQ4<WT> ? 0 : (ls * KS + ks) * SV;
+    if (li < p.hi && v0 < K) {     // (4-bit weights: q4_left and q4_groups tell where the row ends)
       // row r's 16-byte pieces change places with their neighbours 64 bytes on
       // for odd r, so that the rows a quarter-warp reads fall on different banks
       if constexpr (kQ4<WT>) {
-        // four rows at a time, then the scales: lane 2 g + h has group g's of half h.
+        // two rows at a time, then the scales: lane 2 g + h has group g's of half h.
         // What lies in the place of codes past the row's end are codes, which meet
         // zeros of x; their scales are zeros.
-        const bool upper = has_upper(p, lb);
-        if (v0 / 2 + (lane & 7) * 16 < row) {
-          const uint32_t dst = q4_to + put_slot * STAGE;
-          copy16(dst, lp);
-          copy16(dst + 4 * PIECE, lp + 4ll * row);
-          if (upper) {
-            copy16(dst + 8 * PIECE, lp + p.second);
-            copy16(dst + 12 * PIECE, lp + p.second + 4ll * row);
-          }
-        }
-        if (lane < 2 * (SV >> p.log_g)) {
-          const bool there = (v0 >> p.log_g) + (lane >> 1) < p.groups && (upper || !(lane & 1));
-          copy16(ring + put_slot * STAGE + 16 * PIECE + lane * 16, there ? sp : p.s, there);
-        }
+        const bool upper = has_upper(p, lb), on = q4_left > 0;
+        const uint32_t slot_at = put_slot * STAGE;
+        copy16_rows(q4_to + slot_at, lp, 2 * row, on);
+        copy16_rows(q4_to + slot_at + 8 * PIECE, lp + p.second, 2 * row, on && upper);
+        const bool there = q4_groups > 0 && (upper || !(lane & 1));
+        copy16_or0(ring + slot_at + 16 * PIECE + lane * 16, there ? sp : p.s, there, q4_scales);
         lp += KS * PIECE;
-        sp += (long long)KS * (SV >> p.log_g) * 2 * p.width;
+        sp += q4_sp_step;
+        q4_left -= KS * PIECE;
+        q4_groups -= KS * (SV >> p.log_g);
       } else {
         const uint32_t dst = ring + put_slot * STAGE + lane * 16;
         const int at = v0 * (PIECE / SV) + lane * 16;

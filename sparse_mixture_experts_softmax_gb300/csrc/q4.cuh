@@ -35,12 +35,11 @@ __device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t scale2) {
 // factors are normal numbers, 2^-121 to 2^3, take it; a warp with another among its
 // lanes' goes by q4_word.
 constexpr float Q4_UNSCALE = 256.f;
-// Whether both of two bf16 scales (one in each half) take it.
+// Whether both of two bf16 scales (one in each half) take it: bit 15 of either
+// difference says that the magnitude is in range from that side.
 __device__ __forceinline__ bool q4_fast(uint32_t scales) {
-  const __nv_bfloat162 a = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&scales));
-  const uint32_t lo = 0x03000300u, hi = 0x41004100u;
-  return __hbge2(a, *reinterpret_cast<const __nv_bfloat162*>(&lo)) &&
-         __hblt2(a, *reinterpret_cast<const __nv_bfloat162*>(&hi));
+  const uint32_t m = scales & 0x7fff7fffu;
+  return ((m + 0x7d007d00u) & (0xc0ffc0ffu - m) & 0x80008000u) == 0x80008000u;
 }
 // Two runs of 32 inputs, by a whole warp: one branch that all its lanes take alike.
 // bits0, bits1: the runs' scales.

@@ -70,7 +70,7 @@ struct RowsJob {
 
 __global__ void __launch_bounds__(THREADS, 1)
 q4_rows_kernel(const __grid_constant__ Q4Product p, const int tt) {
-  extern __shared__ __align__(128) char sm[];
+  extern __shared__ __align__(256) char sm[];
   __shared__ int n_tiles;
   int* scan = reinterpret_cast<int*>(sm);          // (where the weights' buffers lie later)
   int* offs = scan + 64;                           // [E + 1]
