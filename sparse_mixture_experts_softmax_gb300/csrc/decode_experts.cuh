@@ -396,11 +396,11 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
     scale_at = 16 * PIECE + g * 2 + (c * 32 >> p.log_g) * 32;
     scale_step = 128 * 32 >> p.log_g;
   }
-  template <int T8>
+  template <bool FAST, int T8>
   __device__ __forceinline__ void block(uint32_t codes, uint32_t scales, const uint32_t (&x)[2]) {
     const uint4 w0 = load_rows(codes), w1 = load_rows(codes + 8 * PIECE);
     uint4 r[2][4];
-    q4_runs(w0, w1, load_scale(scales), load_scale(scales + 16), r);
+    q4_runs<FAST>(w0, w1, load_scale(scales), load_scale(scales + 16), r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint4 a = r[0][j], b = r[1][j];
@@ -414,23 +414,43 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
         }
     }
   }
-  template <int T8>
+  template <bool FAST, int T8>
   __device__ __forceinline__ void blocks(uint32_t from, int v0, int end) {
     uint32_t x[2] = {this->at0 + v0 * 2, this->at1 + v0 * 2};
     uint32_t scales = from + scale_at;
     const uint32_t codes = from + code_at;       // (a stage starts at a multiple of 256 bytes)
-#pragma unroll 2
+    if (FAST && end == PIECE) {
+#pragma unroll
+      for (int u = 0; u < PIECE; u += 64) {
+        block<FAST, T8>(codes ^ u, scales, x);
+        scales += scale_step;
+        x[0] += 256;
+        x[1] += 256;
+      }
+      return;
+    }
+#pragma unroll 1
     for (int u = 0; u < end; u += 64) {
-      block<T8>(codes ^ u, scales, x);
+      block<FAST, T8>(codes ^ u, scales, x);
       scales += scale_step;
       x[0] += 256;
       x[1] += 256;
     }
   }
+  // (whether all of the stage's scales take the fast way is looked at once)
   __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
     const int end = min(PIECE, (left + 127) / 128 * 64);
-    if (this->n > 8) blocks<2>(from, v0, end);
-    else blocks<1>(from, v0, end);
+    uint32_t ok = 0x80008000u;
+    if (lane < (int)(scale_step >> 2)) {         // (a stage's groups are scale_step / 8, of 32 bytes)
+      const uint4 s = load_rows(from + 16 * PIECE + lane * 16);
+      ok &= q4_fast(s.x) & q4_fast(s.y) & q4_fast(s.z) & q4_fast(s.w);
+    }
+    if (__all_sync(0xffffffffu, ok == 0x80008000u)) {
+      if (this->n > 8) blocks<true, 2>(from, v0, end);
+      else blocks<true, 1>(from, v0, end);
+    } else {
+      blocks<false, 2>(from, v0, end);
+    }
   }
 };
 // Products<float>: a lane multiplies 4 values of each row with 4 of each token.
@@ -574,6 +594,7 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
   const bool q4_scales = lane < 2 * (SV >> p.log_g);
   const long long q4_sp_step = 2ll * KS * (SV >> p.log_g) * p.width;
   int q4_left = 0, q4_groups = 0;
+  bool q4_upper = false;
   auto begin_item = [&] {
     lp = item_rows<WT>(p, tiles, lt, lb);
     if constexpr (kQ4<WT>) {
@@ -582,6 +603,7 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
       sp = item_scales(p, tiles, lt, lb) + 2ll * g * p.width + (lane & 1) * p.second_s;
       q4_left = row - at;
       q4_groups = p.groups - g;
+      q4_upper = has_upper(p, lb);
     }
   };
   if (li < p.hi) begin_item();
@@ -594,11 +616,11 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
         // two rows at a time, then the scales: lane 2 g + h has group g's of half h.
         // What lies in the place of codes past the row's end are codes, which meet
         // zeros of x; their scales are zeros.
-        const bool upper = has_upper(p, lb), on = q4_left > 0;
+        const bool on = q4_left > 0;
         const uint32_t slot_at = put_slot * STAGE;
         copy16_rows(q4_to + slot_at, lp, 2 * row, on);
-        copy16_rows(q4_to + slot_at + 8 * PIECE, lp + p.second, 2 * row, on && upper);
-        const bool there = q4_groups > 0 && (upper || !(lane & 1));
+        copy16_rows(q4_to + slot_at + 8 * PIECE, lp + p.second, 2 * row, on && q4_upper);
+        const bool there = q4_groups > 0 && (q4_upper || !(lane & 1));
         copy16_or0(ring + slot_at + 16 * PIECE + lane * 16, there ? sp : p.s, there, q4_scales);
         lp += KS * PIECE;
         sp += q4_sp_step;

@@ -35,21 +35,20 @@ __device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t scale2) {
 // factors are normal numbers, 2^-121 to 2^3, take it; a warp with another among its
 // lanes' goes by q4_word.
 constexpr float Q4_UNSCALE = 256.f;
-// Whether both of two bf16 scales (one in each half) take it: bit 15 of either
-// difference says that the magnitude is in range from that side.
-__device__ __forceinline__ bool q4_fast(uint32_t scales) {
+// Bits 15 and 31: whether the two bf16 scales of a word take it (as zeros do).
+__device__ __forceinline__ uint32_t q4_fast(uint32_t scales) {
   const uint32_t m = scales & 0x7fff7fffu;
-  return ((m + 0x7d007d00u) & (0xc0ffc0ffu - m) & 0x80008000u) == 0x80008000u;
+  return (~(m + 0x7fff7fffu) | (m + 0x7d007d00u)) & (0xc0ffc0ffu - m);
 }
-// Two runs of 32 inputs, by a whole warp: one branch that all its lanes take alike.
-// bits0, bits1: the runs' scales.
+// Two runs of 32 inputs; bits0, bits1: their scales.
+template <bool FAST>
 __device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32_t bits0, uint32_t bits1,
                                         uint4 (&v)[2][4]) {
   const uint32_t r[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
   const uint32_t two[2] = {__byte_perm(bits0, 0u, 0x1010), __byte_perm(bits1, 0u, 0x1010)};
-  if (__all_sync(0xffffffffu, q4_fast(__byte_perm(bits0, bits1, 0x5410)))) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < 2; ++u) {
+    if (FAST) {
       const uint32_t low = q4_fma(two[u], 0x7e007e00u, 0x80008000u);             // 2^125
       const uint32_t high = q4_fma(two[u], 0x7c007c00u, 0x80008000u);            // 2^121
       const uint32_t add = q4_fma(two[u], 0xbd00bd00u, 0x80008000u);             // -2^-5
@@ -59,15 +58,20 @@ __device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32
         v[u][i] = make_uint4(q4_fma(w & 0x000f000fu, low, add), q4_fma(w & 0x00f000f0u, high, add),
                              q4_fma(x & 0x000f000fu, low, add), q4_fma(x & 0x00f000f0u, high, add));
       }
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    } else {
       const uint32_t scale2 = q4_fma(two[u], 0x3b803b80u, 0x80008000u);          // 2^-8
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[u][i] = q4_word(r[u][i], scale2);
     }
   }
+}
+// The same by a whole warp, which takes one branch.
+__device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32_t bits0, uint32_t bits1,
+                                        uint4 (&v)[2][4]) {
+  if (__all_sync(0xffffffffu, (q4_fast(__byte_perm(bits0, bits1, 0x5410)) & 0x80008000u) == 0x80008000u))
+    q4_runs<true>(w0, w1, bits0, bits1, v);
+  else
+    q4_runs<false>(w0, w1, bits0, bits1, v);
 }
 
 // Inclusive scan over the threads of a block (those without a value pass a neutral one):

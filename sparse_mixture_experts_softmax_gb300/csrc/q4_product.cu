@@ -145,7 +145,7 @@ cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st) {
   // Every row tile reads its expert's matrix again, most of it from L2
   const long long tiles = (p.E < p.R ? p.E : p.R) + p.R / tt;
   const long long bytes = tiles * p.N * (p.K / 2) * (p.act == 2 ? 2 : 1);
-  const bool few = 2ll * p.R <= (long long)tt * p.E || bytes <= (32ll << 20);
+  const bool few = 4ll * p.R <= 3ll * tt * p.E || bytes <= (32ll << 20);
   if (!few || tiles * ((p.N + 7) / 8) > INT_MAX) return launch_q4_gemm(p, st);
   return launch_q4_rows(p, tt, st);
 }
