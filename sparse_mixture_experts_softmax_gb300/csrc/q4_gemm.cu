@@ -3,7 +3,7 @@
 //
 //   c[r, f] = act(sum_k w_e[f, k] x[r, k] + bias_e[f])     rows r of expert e
 //
-// A tile is 128 outputs by up to 192 rows of one expert (64 outputs of W and the same of
+// A tile is 128 outputs by up to 160 rows of one expert (64 outputs of W and the same of
 // W3 for SwiGLU): the outputs are the lanes of the accumulator, the rows its columns,
 // so that a tile of few rows wastes no more than the narrow side of the instruction (its
 // N is the rows rounded up to 16).  The widened weights are the A operand, which lies in
@@ -15,7 +15,7 @@
 //   warp 1       the matrix instructions (and the tensor memory);
 //   warps 2..5   the epilogue: a lane an output, column by column;
 //   warp 6       the rows of x by bulk-tensor copies, 128 inputs at a time;
-//   warps 7..    4-bit to bf16, in groups of four warps that take 64 inputs in turn.
+//   warps 7..    4-bit to bf16, in groups of four warps that take 128 inputs in turn.
 // Two accumulators let a tile's epilogue run beside the next one's products.
 // Every wait is bounded (2 s); when one expires the block raises an abort flag and
 // the status word, waits for its copies and products in flight, frees its tensor
@@ -39,8 +39,7 @@ __host__ __device__ constexpr int box_of(int rows) { return rows <= 64 ? (rows -
 static_assert(box_rows(0) == 16 && box_rows(3) == 64 && box_rows(4) == 96 && box_rows(7) == 192, "heights");
 static_assert(box_of(1) == 0 && box_of(64) == 3 && box_of(65) == 4 && box_of(96) == 4 && box_of(97) == 5 &&
               box_of(192) == 7, "heights");
-constexpr int W_RAW = 0, W_MMA = 1, W_EPI = 2, W_X = 6, W_WIDEN = 7, NG = 4, N_WIDEN = 4 * NG;
-constexpr int THREADS = 32 * (W_WIDEN + N_WIDEN);
+constexpr int W_RAW = 0, W_MMA = 1, W_EPI = 2, W_X = 6, W_WIDEN = 7;
 constexpr int MAX_E = 256;
 constexpr int TMEM_COLS = 512;
 constexpr long long LIMIT_NS = 2000000000ll;
@@ -49,13 +48,14 @@ constexpr long long LIMIT_NS = 2000000000ll;
 // widened weights, SX of rows.  The accumulators take 2 BN of the 512 columns, a stage of
 // weights 64.  The groups of widening warps run apart from one another, and copies do
 // not land in the order of their issue: a group may only wait on stages whose every use
-// is its own (a barrier tells no more than the parity of its phase).  So a pair of
-// groups shares a stage, 64 inputs each, and Q and SA are multiples of the pairs.  Of a
-// tile's last stage, where it has 64 inputs or less, the second half is without work.
-constexpr int BN = 192, Q = 8, SA = 2, SX = 3;
+// is its own (a barrier tells no more than the parity of its phase), so Q and SA are
+// multiples of the groups.  Of a tile's last stage, where it has 64 inputs or less, the
+// second half is without work.
+constexpr int BN = 160, Q = 6, SA = 3, SX = 4;
+constexpr int NG = 3, N_WIDEN = 4 * NG, THREADS = 32 * (W_WIDEN + N_WIDEN);
 constexpr int X_HALF = BN * BK * 2, X_STAGE = 2 * X_HALF;
 constexpr int SMEM = SX * X_STAGE + Q * RAW_BYTES;
-static_assert(2 * BN + SA * 64 <= TMEM_COLS && SA % (NG / 2) == 0 && Q % (NG / 2) == 0, "stages");
+static_assert(2 * BN + SA * 64 <= TMEM_COLS && SA % NG == 0 && Q % NG == 0, "stages");
 static_assert(SMEM + 5120 <= 232448, "shared memory of one block");
 
 struct Params {
@@ -144,11 +144,10 @@ __device__ __forceinline__ bool elect() {
   return v != 0;
 }
 
-__device__ __forceinline__ float act_of(int act, float h) {
-  if (act == 1) return gelu_epi(h);
-  return act == 0 && h < 0.f ? 0.f : h;          // a NaN stays one
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
-
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -203,10 +202,10 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
   if (tid == 0) {
     for (int i = 0; i < Q; ++i) {
       mbar_init(smem_u32(&raw_full[i]), 1);
-      mbar_init(smem_u32(&raw_empty[i]), 8);      // (a stage is two groups' work)
+      mbar_init(smem_u32(&raw_empty[i]), 4);      // (a group's warps)
     }
     for (int i = 0; i < SA; ++i) {
-      mbar_init(smem_u32(&a_full[i]), 8);
+      mbar_init(smem_u32(&a_full[i]), 4);
       mbar_init(smem_u32(&a_empty[i]), 1);
     }
     for (int i = 0; i < SX; ++i) {
@@ -352,44 +351,62 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     __syncwarp();
   } else if (warp >= W_WIDEN) {
     // a warp may only write its own quarter of the tensor memory's lanes
-    const int group = (warp - W_WIDEN) >> 2, h = group & 1, quarter = warp & 3;
+    // a warp may only write its own quarter of the tensor memory's lanes
+    const int group = (warp - W_WIDEN) >> 2, quarter = warp & 3;
     // this lane's output in a raw stage; SwiGLU: 16 outputs of W and the same 16 of W3
     // share a warp's lanes
     const int r = SWIGLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
     const int ng = RAW_K >> p.log_g, swz = (r >> 1) & 3;
     const uint32_t scale_at = CODE_BYTES + (SWIGLU ? (r >> 6) * ng * BM + (r & 63) * 2 : r * 2);
     const uint32_t scale_step = SWIGLU ? BM : BM * 2;
-    // where its two runs of 32 codes and their scales lie
-    const uint32_t code0 = rbase + r * 64 + ((2 * h) ^ swz) * 16, code1 = rbase + r * 64 + ((2 * h + 1) ^ swz) * 16;
-    const uint32_t scale0 = rbase + scale_at + ((h * 64) >> p.log_g) * scale_step;
-    const uint32_t scale1 = rbase + scale_at + ((h * 64 + 32) >> p.log_g) * scale_step;
-    const uint32_t to0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * BN + h * 32;
-    // the group's stages are every (NG / 2)-th
+    uint32_t code[4], scale[4];        // where its four runs of 32 codes and their scales lie
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      code[c] = rbase + r * 64 + (c ^ swz) * 16;
+      scale[c] = rbase + scale_at + ((c * 32) >> p.log_g) * scale_step;
+    }
+    const uint32_t to0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * BN;
     const int mine = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     const long long raws = (long long)mine * nraw;
-    int q = group >> 1, s = group >> 1, j = group >> 1;    // j: stage of a tile
+    int q = group, s = group, j = group;         // (j: stage of a tile) every NG-th is the group's
     uint32_t qph = 0, ph = 1;
-    for (long long i = group >> 1; i < raws; i += NG / 2) {
+    for (long long i = group; i < raws; i += NG) {
       if (!all_wait(smem_u32(&raw_full[q]), qph)) break;
-      const uint4 w0 = lds128(code0 + q * RAW_BYTES), w1 = lds128(code1 + q * RAW_BYTES);
-      const uint32_t s0 = lds_scale(scale0 + q * RAW_BYTES);
-      uint32_t s1 = p.log_g == 5 ? lds_scale(scale1 + q * RAW_BYTES) : s0;
+      uint4 c4[4];
+      uint32_t sc[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        c4[c] = lds128(code[c] + q * RAW_BYTES);
+        sc[c] = lds_scale(scale[c] + q * RAW_BYTES);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&raw_empty[q]));
-      q += NG / 2;
+      q += NG;
       if (q >= Q) { q -= Q; qph ^= 1u; }
-      uint4 w[2][4];
       while (j >= nraw) j -= nraw;
-      if (j * RAW_K + h * BK + 32 >= p.K) s1 = 0u;       // past the last input: zeros, whatever the scale
-      j += NG / 2;
-      q4_runs(w0, w1, s0, s1, w);
+      if (j == nraw - 1) {             // past the last input: zeros, whatever the scale
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (j * RAW_K + c * 32 >= p.K) sc[c] = 0u;
+      }
+      j += NG;
+      uint4 w[2][2][4];
+      const uint32_t ok = q4_fast(__byte_perm(sc[0], sc[1], 0x5410)) & q4_fast(__byte_perm(sc[2], sc[3], 0x5410));
+      if (__all_sync(0xffffffffu, (ok & 0x80008000u) == 0x80008000u)) {
+        q4_runs<true>(c4[0], c4[1], sc[0], sc[1], w[0]);
+        q4_runs<true>(c4[2], c4[3], sc[2], sc[3], w[1]);
+      } else {
+        q4_runs<false>(c4[0], c4[1], sc[0], sc[1], w[0]);
+        q4_runs<false>(c4[2], c4[3], sc[2], sc[3], w[1]);
+      }
       if (!all_wait(smem_u32(&a_empty[s]), ph)) break;
       tc_fence_after();
-      tmem_st32(to0 + s * 64, w);
+      tmem_st32(to0 + s * 64, w[0]);
+      tmem_st32(to0 + s * 64 + 32, w[1]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
-      s += NG / 2;
+      s += NG;
       if (s >= SA) { s -= SA; ph ^= 1u; }
     }
   } else {
@@ -404,28 +421,56 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
       const int f = T.f0 + (SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
       const bool on = f < p.N;
       const float bias = !SWIGLU && p.bias != nullptr && on ? p.bias[(long long)T.e * p.N + f] : 0.f;
-      bf16* c = p.c + (long long)T.r0 * p.N + f;
+      // Lanes pair up so that each stores two outputs of every other row: lane and
+      // lane ^ 1 (their own outputs), for SwiGLU after lane ^ 16 has given W3's
+      const bool odd = lane & 1, upper = lane >= 16;
+      uint32_t* c = reinterpret_cast<uint32_t*>(p.c + (long long)T.r0 * p.N + (f & ~1));
+      const int half_n = p.N / 2;              // (N is even: a row is a whole number of pairs)
       for (int col = 0; col < T.n; col += 16) {
         float v[16];
         tmem_ld16(at + col, v);
         tmem_ld_wait();
+        const int left = T.n - col;
         if (SWIGLU) {
-          // lanes 0..15 have W's outputs, 16..31 W3's: of two columns each half takes one
+          // lanes 0..15 have W's outputs, 16..31 W3's: of two rows each half takes one
+          float u[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const bool up = lane >= 16;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 16);
-            const float h1 = Q4_UNSCALE * (up ? got : v[i]), h3 = Q4_UNSCALE * (up ? v[i + 1] : got);
-            const int n = col + i + (up ? 1 : 0);
-            if (on && n < T.n)
-              c[(long long)n * p.N] = __float2bfloat16_rn((h1 * sigmoid_epi(h1)) * h3);
+          for (int i = 0; i < 8; ++i) {
+            const float got = __shfl_xor_sync(0xffffffffu, upper ? v[2 * i] : v[2 * i + 1], 16);
+            const float h1 = Q4_UNSCALE * (upper ? got : v[2 * i]);
+            const float h3 = Q4_UNSCALE * (upper ? v[2 * i + 1] : got);
+            u[i] = (h1 * sigmoid_epi(h1)) * h3;          // of row 2 i + upper
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? u[i] : u[i + 1], 1);
+            const int n = 2 * (i + (odd ? 1 : 0)) + (upper ? 1 : 0);
+            const uint32_t two = pair_bf16(odd ? got : u[i], odd ? u[i + 1] : got);
+            if (on && n < left) c[(long long)n * half_n] = two;
           }
         } else {
+          if (p.act == 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (on && col + i < T.n)
-              c[(long long)(col + i) * p.N] = __float2bfloat16_rn(act_of(p.act, fmaf(v[i], Q4_UNSCALE, bias)));
+            for (int i = 0; i < 16; ++i) v[i] = gelu_epi(fmaf(v[i], Q4_UNSCALE, bias));
+          } else if (p.act == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v[i] = fmaf(v[i], Q4_UNSCALE, bias);
+              v[i] = v[i] < 0.f ? 0.f : v[i];            // a NaN stays one
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], Q4_UNSCALE, bias);
+          }
+          uint32_t* to = c + (odd ? half_n : 0);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2, to += 2ll * half_n) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+            const uint32_t two = pair_bf16(odd ? got : v[i], odd ? v[i + 1] : got);
+            if (on && i + (odd ? 1 : 0) < left) *to = two;
+          }
         }
+        c += 16ll * half_n;
       }
       tc_fence_before();
       __syncwarp();
