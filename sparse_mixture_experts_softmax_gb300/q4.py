@@ -37,7 +37,7 @@ class Q4Matrix:
     used in place (in the storage that they have when the object is made) and change in
     place only."""
 
-    __slots__ = ("codes", "scales", "group", "E", "N", "K", "device", "_held")
+    __slots__ = ("codes", "scales", "group", "E", "N", "K", "device", "_held", "_c", "_ref")
 
     def __setattr__(self, name, value):
         if hasattr(self, name):
@@ -54,17 +54,31 @@ class Q4Matrix:
             raise ValueError(f"N must be a multiple of 8 and K of 32, got {(E, N, K)}")
         _want("codes", codes, torch.uint8, (E, N, K // 2), codes.device)
         _want("scales", scales, torch.bfloat16, (E, -(-K // group), N), codes.device)
-        self.codes, self.scales, self.group = codes.detach(), scales.detach(), int(group)
-        self.E, self.N, self.K, self.device = E, N, K, codes.device
-        # what c_matrix() has handed out addresses of, whatever becomes of the attributes' storage
-        self._held = codes.detach(), scales.detach()
+        self._set(codes.detach(), scales.detach(), int(group), E, N, K)
+
+    def _set(self, codes, scales, group, E, N, K):
+        put = object.__setattr__
+        c = B.moe_q4_matrix(codes.data_ptr(), scales.data_ptr())
+        # _held: what the addresses are of, whatever becomes of the attributes' storage
+        for name, value in (("codes", codes), ("scales", scales), ("group", group), ("E", E), ("N", N),
+                            ("K", K), ("device", codes.device), ("_c", c), ("_ref", ctypes.byref(c)),
+                            ("_held", (codes.detach(), scales.detach()))):
+            put(self, name, value)
+
+    @classmethod
+    def _new(cls, E, N, K, group, device):
+        m = cls.__new__(cls)
+        m._set(torch.empty((E, N, K // 2), dtype=torch.uint8, device=device),
+               torch.empty((E, -(-K // group), N), dtype=torch.bfloat16, device=device), group, E, N, K)
+        return m
 
     @property
     def shape(self):
         return (self.E, self.N, self.K)
 
     def c_matrix(self) -> B.moe_q4_matrix:
-        return B.make_q4_matrix(*self._held)
+        """The matrix as the C ABI takes it; it keeps no tensor alive."""
+        return B.moe_q4_matrix(self._c.codes, self._c.scales)
 
     def dequantize(self, dtype=torch.bfloat16, out=None):
         """The weights [E, N, K] (bfloat16 values, in float32 where asked)."""
@@ -73,7 +87,11 @@ class Q4Matrix:
         if out.dtype not in _TYPE:
             raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
         _want("out", out, out.dtype, self.shape, self.device)
-        B.moe_q4_dequantize(self.E, self.N, self.K, self.group, _TYPE[out.dtype], self.c_matrix(), out)
+        status = B.lib().moe_q4_dequantize(self.E, self.N, self.K, self.group,
+                                           B.DTYPE[_TYPE[out.dtype]], self._ref, out.data_ptr(),
+                                           B._stream_on(None, self.device))
+        if status != B.MOE_OK:
+            B._check("moe_q4_dequantize", status)
         return out
 
 
@@ -94,12 +112,14 @@ def quantize(w, group=64, out=None) -> Q4Matrix:
     E, N, K = w.shape
     _want("w", w, w.dtype, (E, N, K), w.device)
     if out is None:
-        out = Q4Matrix(torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device),
-                       torch.empty(E, -(-K // group), N, dtype=torch.bfloat16, device=w.device), group)
+        out = Q4Matrix._new(E, N, K, group, w.device)
     elif out.shape != (E, N, K) or out.group != group or out.device != w.device:
         raise ValueError(f"out is {out.shape} with groups of {out.group} on {out.device}, w asks "
                          f"for {(E, N, K)} with groups of {group} on {w.device}")
-    B.moe_q4_quantize(E, N, K, group, _TYPE[w.dtype], w.detach(), *out._held)
+    status = B.lib().moe_q4_quantize(E, N, K, group, B.DTYPE[_TYPE[w.dtype]], w.data_ptr(),
+                                     out._c.codes, out._c.scales, B._stream_on(None, w.device))
+    if status != B.MOE_OK:
+        B._check("moe_q4_quantize", status)
     return out
 
 
