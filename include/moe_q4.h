@@ -67,10 +67,19 @@ typedef struct {
  * Rows outside of every segment are not read and left as they are in c.  c must
  * not overlap an input.  E <= MOE_Q4_MAX_EXPERTS, R K and R N < 2^40.
  * dev_status (int32, device) receives MOE_ERR_TIMEOUT where a bounded device-side
- * wait expired (c is then invalid), and is left as it is otherwise. */
+ * wait expired (c is then invalid), and is left as it is otherwise.  The order of a
+ * row's sums goes with the call's rows and shape: the same call gives the same bits, a
+ * row among other rows may differ in the last bits before the rounding. */
 MOE_API moe_status moe_q4_product(const moe_q4_product_config* cfg, const int32_t* offsets,
                                   const void* x, const moe_q4_matrix* w, const moe_q4_matrix* w3,
                                   const float* bias, void* c, int32_t* dev_status, void* stream);
+
+/* The product for many rows with every load withheld: its waits expire after limit_ns
+ * (1 to 2e9), dev_status receives MOE_ERR_TIMEOUT and c is not written. */
+MOE_API moe_status moe_q4_selftest_wait_timeout(const moe_q4_product_config* cfg,
+                                                const int32_t* offsets, const void* x,
+                                                const moe_q4_matrix* w, void* c, int32_t* dev_status,
+                                                int64_t limit_ns, void* stream);
 
 /* The weights of a layer whose expert matrices are 4-bit ones: as in moe_weights
  * (w1, w3 and ws1, ws3 [E, F, D] and [1, n_shared F, D], w2 and ws2 [E, D, F] and

@@ -205,6 +205,9 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_q4_dequantize.argtypes = [c_int32] * 5 + [P(moe_q4_matrix), c_void_p, c_void_p]
     L.moe_q4_product.argtypes = [P(moe_q4_product_config), c_void_p, c_void_p, P(moe_q4_matrix),
                                  P(moe_q4_matrix)] + [c_void_p] * 4
+    L.moe_q4_selftest_wait_timeout.argtypes = [P(moe_q4_product_config), c_void_p, c_void_p,
+                                               P(moe_q4_matrix), c_void_p, c_void_p, ctypes.c_int64,
+                                               c_void_p]
     L.moe_q4_decode.argtypes = [P(moe_config), P(moe_q4_weights)] + [c_void_p] * 5 + [c_size_t,
                                                                                       c_void_p]
     L.moe_q4_workspace_size.argtypes = [P(moe_config)]
@@ -214,7 +217,7 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_q4_status.argtypes = [P(moe_config), c_void_p, c_size_t, c_void_p, c_void_p]
     for fn in ("moe_norm_forward", "moe_norm_backward", "moe_decode_init", "moe_decode",
                "moe_decode_status", "moe_q4_quantize", "moe_q4_dequantize", "moe_q4_product",
-               "moe_q4_decode", "moe_q4_forward", "moe_q4_status"):
+               "moe_q4_selftest_wait_timeout", "moe_q4_decode", "moe_q4_forward", "moe_q4_status"):
         getattr(L, fn).restype = c_int32
     for fn in ("moe_ep_buffer_offsets", "moe_ep_get_routing", "moe_ep_route",
                "moe_ep_expert_forward",
@@ -620,6 +623,14 @@ def moe_q4_product(cfg, offsets, x, w, w3, bias, c, dev_status, stream=None):
            lib().moe_q4_product(ctypes.byref(cfg), _ptr(offsets), _ptr(x), ctypes.byref(w),
                                 None if w3 is None else ctypes.byref(w3), _ptr(bias), _ptr(c),
                                 _ptr(dev_status), _stream_on(stream, x.device)))
+
+
+def moe_q4_selftest_wait_timeout(cfg, offsets, x, w, c, dev_status, limit_ns, stream=None):
+    """The product for many rows with its loads withheld: its bounded waits must expire."""
+    _check("moe_q4_selftest_wait_timeout",
+           lib().moe_q4_selftest_wait_timeout(ctypes.byref(cfg), _ptr(offsets), _ptr(x),
+                                              ctypes.byref(w), _ptr(c), _ptr(dev_status),
+                                              int(limit_ns), _stream_on(stream, x.device)))
 
 
 def make_q4_weights(w_gate, group, w1, w2, w3=None, b1=None, b2=None, logit_bias=None,

@@ -28,6 +28,8 @@ struct Q4Product {
   const float* bias;           // [E, N] or nullptr
   void* c;                     // [R, N] bf16
   int* status;
+  long long limit_ns;          // bound of each device wait (0: the default, 2 s)
+  int stall;                   // self-test of the bounded waits: the kernel for many rows, no copies
 };
 cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st);
 // The kernel for many rows (q4_gemm.cu).

@@ -60,6 +60,44 @@ moe_status check_forward_ws(const moe_config& c, const void* ws, size_t bytes) {
   return bytes < forward_layout(c).total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
+moe_status run_product(const moe_q4_product_config* cfg, const int32_t* offsets, const void* x,
+                       const moe_q4_matrix* w, const moe_q4_matrix* w3, const float* bias, void* c,
+                       int32_t* dev_status, long long limit_ns, int stall, void* stream) {
+  g_launches = 0;
+  if (cfg == nullptr || cfg->R < 0) return MOE_ERR_INVALID_ARG;
+  RET_IF(check_q4_shape(cfg->E, cfg->N, cfg->K, cfg->group));
+  if (cfg->act < 0 || cfg->act > MOE_Q4_ACT_NONE) return MOE_ERR_INVALID_ARG;
+  const bool swiglu = cfg->act == MOE_ACT_SWIGLU;
+  if (cfg->E > MOE_Q4_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  if ((long long)cfg->R * cfg->K >= (1LL << 40) || (long long)cfg->R * cfg->N >= (1LL << 40))
+    return MOE_ERR_UNSUPPORTED;
+  if (!offsets || !w || !dev_status || swiglu != (w3 != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (swiglu && bias) return MOE_ERR_INVALID_ARG;
+  if (cfg->R > 0 && (!x || !c)) return MOE_ERR_INVALID_ARG;
+  RET_IF(check_q4_matrix(*w));
+  if (w3) RET_IF(check_q4_matrix(*w3));
+  const void* ps[] = {offsets, x, bias, c, dev_status};
+  for (const void* p : ps)
+    if (p && !aligned16(p)) return MOE_ERR_ALIGNMENT;
+  RET_IF(check_device());
+  if (cfg->R == 0) return MOE_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Q4Product p{};
+  p.R = cfg->R; p.E = cfg->E; p.N = cfg->N; p.K = cfg->K; p.G = cfg->group;
+  p.act = cfg->act;
+  p.offsets = offsets;
+  p.x = x;
+  p.codes = w->codes; p.scales = w->scales;
+  p.codes3 = w3 ? w3->codes : nullptr; p.scales3 = w3 ? w3->scales : nullptr;
+  p.bias = bias;
+  p.c = c;
+  p.status = dev_status;
+  p.limit_ns = limit_ns;
+  p.stall = stall;
+  KL("q4_product", launch_q4_product(p, st));
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -93,37 +131,14 @@ moe_status moe_q4_dequantize(int32_t E, int32_t N, int32_t K, int32_t group, int
 moe_status moe_q4_product(const moe_q4_product_config* cfg, const int32_t* offsets, const void* x,
                           const moe_q4_matrix* w, const moe_q4_matrix* w3, const float* bias,
                           void* c, int32_t* dev_status, void* stream) {
-  g_launches = 0;
-  if (cfg == nullptr || cfg->R < 0) return MOE_ERR_INVALID_ARG;
-  RET_IF(check_q4_shape(cfg->E, cfg->N, cfg->K, cfg->group));
-  if (cfg->act < 0 || cfg->act > MOE_Q4_ACT_NONE) return MOE_ERR_INVALID_ARG;
-  const bool swiglu = cfg->act == MOE_ACT_SWIGLU;
-  if (cfg->E > MOE_Q4_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
-  if ((long long)cfg->R * cfg->K >= (1LL << 40) || (long long)cfg->R * cfg->N >= (1LL << 40))
-    return MOE_ERR_UNSUPPORTED;
-  if (!offsets || !w || !dev_status || swiglu != (w3 != nullptr)) return MOE_ERR_INVALID_ARG;
-  if (swiglu && bias) return MOE_ERR_INVALID_ARG;
-  if (cfg->R > 0 && (!x || !c)) return MOE_ERR_INVALID_ARG;
-  RET_IF(check_q4_matrix(*w));
-  if (w3) RET_IF(check_q4_matrix(*w3));
-  const void* ps[] = {offsets, x, bias, c, dev_status};
-  for (const void* p : ps)
-    if (p && !aligned16(p)) return MOE_ERR_ALIGNMENT;
-  RET_IF(check_device());
-  if (cfg->R == 0) return MOE_OK;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Q4Product p{};
-  p.R = cfg->R; p.E = cfg->E; p.N = cfg->N; p.K = cfg->K; p.G = cfg->group;
-  p.act = cfg->act;
-  p.offsets = offsets;
-  p.x = x;
-  p.codes = w->codes; p.scales = w->scales;
-  p.codes3 = w3 ? w3->codes : nullptr; p.scales3 = w3 ? w3->scales : nullptr;
-  p.bias = bias;
-  p.c = c;
-  p.status = dev_status;
-  KL("q4_product", launch_q4_product(p, st));
-  return MOE_OK;
+  return run_product(cfg, offsets, x, w, w3, bias, c, dev_status, 0, 0, stream);
+}
+
+moe_status moe_q4_selftest_wait_timeout(const moe_q4_product_config* cfg, const int32_t* offsets,
+                                        const void* x, const moe_q4_matrix* w, void* c,
+                                        int32_t* dev_status, int64_t limit_ns, void* stream) {
+  if (limit_ns <= 0 || limit_ns > 2000000000ll) return MOE_ERR_INVALID_ARG;
+  return run_product(cfg, offsets, x, w, nullptr, nullptr, c, dev_status, limit_ns, 1, stream);
 }
 
 size_t moe_q4_workspace_size(const moe_config* cfg) {

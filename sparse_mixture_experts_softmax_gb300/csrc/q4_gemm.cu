@@ -42,7 +42,7 @@ static_assert(box_of(1) == 0 && box_of(64) == 3 && box_of(65) == 4 && box_of(96)
 constexpr int W_RAW = 0, W_MMA = 1, W_EPI = 2, W_X = 6, W_WIDEN = 7;
 constexpr int MAX_E = 256;
 constexpr int TMEM_COLS = 512;
-constexpr long long LIMIT_NS = 2000000000ll;
+constexpr long long LIMIT_NS = 2000000000ll;             // bound of every wait
 
 // Rows of a tile at most, and stages, each of 128 inputs: Q of codes and scales, SA of
 // widened weights, SX of rows.  The accumulators take 2 BN of the 512 columns, a stage of
@@ -66,6 +66,8 @@ struct Params {
   const float* bias;
   bf16* c;
   int* status;
+  long long limit_ns;          // bound of every wait
+  int stall;                   // self-test: no copy is issued, the waits run out
 };
 
 struct XMaps {
@@ -121,7 +123,7 @@ __device__ __forceinline__ void make_table(const Params& p, Table& tb) {
 // the block and records a timeout).  What follows the first look is out of line: the
 // loops of the warps are bound by their instructions' latencies.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       int* status) {
+                                       int* status, long long limit_ns) {
   unsigned long long t0 = 0;
   while (true) {
 #pragma unroll 1
@@ -130,7 +132,7 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile i
     if (*abort_flag) return false;
     const unsigned long long now = global_ns();
     if (t0 == 0) t0 = now;
-    if ((long long)(now - t0) > LIMIT_NS) {
+    if ((long long)(now - t0) > limit_ns) {
       *abort_flag = 1;
       if (status) atomicExch(status, DEV_STATUS_TIMEOUT);
       return false;
@@ -230,11 +232,11 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
   const int nraw = (p.K + RAW_K - 1) / RAW_K, nkb = (p.K + BK - 1) / BK;   // 2 nraw or one less
   // (bar: a barrier's address in shared memory)
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, p.status);
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, p.status, p.limit_ns);
   };
   auto all_wait = [&](uint32_t bar, uint32_t parity) {     // by a whole warp
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
-           __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag, p.status));
+           __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag, p.status, p.limit_ns));
   };
 
   // The loops below are run by whole warps and only the copies and products by one lane,
@@ -246,7 +248,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     const uint32_t bytes = CODE_BYTES + ng * BM * 2;
     int q = 0, issued = 0;
     uint32_t ph = 0, last = 0;
-    bool ok = true;
+    bool ok = p.stall == 0;
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile T = tile_at(t, p, tb);
       for (int j = 0; j < nraw; ++j) {
@@ -268,13 +270,13 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     }
     // every copy has landed before the block goes
     for (int i = 0; i < Q; ++i)
-      if (issued >> i & 1) drain_wait(smem_u32(&raw_full[i]), last >> i & 1u, LIMIT_NS);
+      if (issued >> i & 1) drain_wait(smem_u32(&raw_full[i]), last >> i & 1u, p.limit_ns);
     __syncwarp();
   } else if (warp == W_X) {
     const bool issuer = elect();
     int s = 0, issued = 0;
     uint32_t ph = 0, last = 0;
-    bool ok = true;
+    bool ok = p.stall == 0;
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile T = tile_at(t, p, tb);
       const int box = box_of(T.n);
@@ -295,7 +297,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
       }
     }
     for (int i = 0; i < SX; ++i)
-      if (issued >> i & 1) drain_wait(smem_u32(&x_full[i]), last >> i & 1u, LIMIT_NS);
+      if (issued >> i & 1) drain_wait(smem_u32(&x_full[i]), last >> i & 1u, p.limit_ns);
     __syncwarp();
   } else if (warp == W_MMA) {
     const bool issuer = elect();
@@ -346,7 +348,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     }
     if (any && issuer) {
       mma_commit(smem_u32(&drain_mb));
-      drain_wait(smem_u32(&drain_mb), 0, LIMIT_NS);
+      drain_wait(smem_u32(&drain_mb), 0, p.limit_ns);
     }
     __syncwarp();
   } else if (warp >= W_WIDEN) {
@@ -529,6 +531,8 @@ cudaError_t launch_q4_gemm(const Q4Product& q, cudaStream_t st) {
   p.bias = q.bias;
   p.c = static_cast<bf16*>(q.c);
   p.status = q.status;
+  p.limit_ns = q.limit_ns > 0 ? q.limit_ns : LIMIT_NS;
+  p.stall = q.stall;
   CUtensorMap maps[4];
   XMaps x;
   const uint64_t xd[2] = {(uint64_t)q.K, (uint64_t)q.R}, xs[1] = {(uint64_t)q.K * 2};

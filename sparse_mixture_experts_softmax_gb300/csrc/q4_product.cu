@@ -140,7 +140,7 @@ cudaError_t launch_q4_rows(const Q4Product& p, int tt, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st) {
-  const int tt = p.R <= MAX_ROWS ? tile_rows(p) : 0;
+  const int tt = p.R <= MAX_ROWS && !p.stall ? tile_rows(p) : 0;
   if (tt == 0) return launch_q4_gemm(p, st);
   // Every row tile reads its expert's matrix again, most of it from L2
   const long long tiles = (p.E < p.R ? p.E : p.R) + p.R / tt;

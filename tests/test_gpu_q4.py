@@ -79,6 +79,22 @@ def test_dequantize_every_code(five):
     assert np.array_equal(m.dequantize().double().cpu().numpy(), C.weights(codes, scales, 64))
 
 
+@pytest.mark.parametrize("shape", [(1, 8, 32), (3, 40, 352), (2, 16, 8192)])
+def test_pack_stays_in_its_tensors(shape):
+    """Nothing is written behind codes, scales or weights."""
+    E, N, K = shape
+    G = -(-K // 64)
+    codes = torch.full((E * N * K // 2 + 64,), 7, dtype=torch.uint8, device="cuda")
+    scales = torch.full((E * G * N + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = Q4Matrix(codes[:-64].view(E, N, K // 2), scales[:-64].view(E, G, N), 64)
+    quantize(torch.randn(E, N, K, device="cuda"), 64, out=q)
+    assert (codes[-64:] == 7).all() and (scales[-64:] == 7).all() and (codes[:-64] != 7).any()
+    for dt in (torch.bfloat16, torch.float32):
+        w = torch.full((E * N * K + 64,), 7.0, dtype=dt, device="cuda")
+        q.dequantize(out=w[:-64].view(E, N, K))
+        assert (w[-64:] == 7).all()
+
+
 def test_quantize_in_place_and_2d():
     w = torch.randn(24, 96, device="cuda")
     q = quantize(w, 32)
@@ -163,7 +179,35 @@ def test_product_sizes(counts, N, K, group, act):
     assert p.status() == 0
 
 
-@pytest.mark.parametrize("counts", [[4], [40, 90], [300]])
+# more rows than the few-row kernel takes: segments around the row tiles of the other
+MANY = [4100, 1, 0, 15, 16, 17, 33, 64, 65, 96, 97, 127, 128, 129, 159, 160, 161, 0, 320, 321, 480, 5]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("act,bias", [("none", False), ("gelu_tanh", True), ("relu", True), ("swiglu", False)])
+def test_product_many_rows(act, bias, shape):
+    N, K, group = shape
+    c = _product_case(N + 2 * K, MANY, N, K, group, act, bias, before=2, behind=3)
+    p, x, off = _device(c)
+    out = torch.full((c["R"], N), 7.0, dtype=torch.bfloat16, device="cuda")
+    p.forward(x, off, out)
+    _check(c, out, fill=7.0)
+    assert p.status() == 0
+
+
+@pytest.mark.parametrize("counts,N,K,group,act", [
+    ([0, 4096], 8, 32, 32, "none"), ([4096, 1], 8, 32, 32, "none"), ([4097], 8, 32, 32, "swiglu"),
+    ([17] * 256, 16, 96, 64, "none"), ([0] * 255 + [5000], 40, 64, 32, "relu"),
+    ([4000, 600], 136, 8192, 128, "none"), ([5000], 1000, 32, 32, "swiglu"), ([100] * 64, 704, 1024, 64, "swiglu"),
+])
+def test_product_many_rows_sizes(counts, N, K, group, act):
+    c = _product_case(7, counts, N, K, group, act, act == "relu")
+    p, x, off = _device(c)
+    _check(c, p.forward(x, off))
+    assert p.status() == 0
+
+
+@pytest.mark.parametrize("counts", [[4], [40, 90], [300], [3000, 1200]])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_product_scales_of_eight_bits(counts, act):
     c = _product_case(9, counts, 72, 320, 32, act, False, five=False)
@@ -171,7 +215,22 @@ def test_product_scales_of_eight_bits(counts, act):
     _check(c, p.forward(x, off))
 
 
-@pytest.mark.parametrize("counts", [[3, 4], [20, 50], [150, 150]])
+@pytest.mark.parametrize("counts,scale", [([4], 1e-3), ([4], 2.0 ** -119), ([4], 2.0 ** 20), ([40, 90], 8.0),
+                                          ([3000, 1200], 2.0 ** -122), ([3000, 1200], 2.0 ** 30)])
+def test_product_scales_of_any_size(counts, scale):
+    """Scales on both sides of the range of the kernels' short way to widen a code, in one
+    matrix: some groups are `scale` times the others, which are exact zeros in places."""
+    c = _product_case(21, counts, 72, 320, 32, "none", False)
+    codes, s = c["m"]
+    s = s.copy()
+    s[:, ::3] *= scale
+    s[:, 1, ::5] = 0.0
+    c["m"] = (codes, C.bf16(s))
+    p, x, off = _device(c)
+    _check(c, p.forward(x, off))
+
+
+@pytest.mark.parametrize("counts", [[3, 4], [20, 50], [150, 150], [200, 4000]])
 def test_rows_do_not_mix(counts):
     """A row of NaN and one of infinities stay in their rows, a NaN and an infinite scale
     in their outputs; rows outside of the segments are not looked at."""
@@ -217,13 +276,43 @@ def test_offsets_are_clamped():
         _check(dict(c, offsets=np.array(fixed)), guard[:40], fill=3.0)
 
 
+def test_offsets_are_clamped_many_rows():
+    c = _product_case(14, [2000, 1000, 0, 1500], 64, 64, 32, "none", False)
+    p, x, _ = _device(c)
+    for off in ([-5, 10, 4, 30, 4500], [0, 100000, 20, 30, 1 << 30], [8, 3, 12, 4200, 4100]):
+        fixed, prev = [], 0
+        for v in off:
+            prev = max(prev, min(max(v, prev), 4500))
+            fixed.append(prev)
+        guard = torch.full((4700, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        p.forward(x, torch.tensor(off, dtype=torch.int32, device="cuda"), guard[:4500])
+        assert (guard[4500:] == 3).all()
+        _check(dict(c, offsets=np.array(fixed)), guard[:4500], fill=3.0)
+
+
+def test_waits_expire():
+    """With its loads withheld the product for many rows ends by itself, says so and writes
+    nothing; the next call is not affected."""
+    c = _product_case(2, [300, 200], 264, 320, 64, "none", False)
+    p, x, off = _device(c)
+    cfg = B.moe_q4_product_config(500, 2, 264, 320, 64, B.MOE_Q4_ACT_NONE)
+    out = torch.full((500, 264), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    m = C.device_matrix(*c["m"], 64)
+    B.moe_q4_selftest_wait_timeout(cfg, off, x, m.c_matrix(), out, status, 20_000_000)
+    torch.cuda.synchronize()
+    assert status[0] == B.MOE_ERR_TIMEOUT and (out == 7).all()
+    _check(c, p.forward(x, off))
+    assert p.status() == 0
+
+
 def test_no_rows():
     c = _product_case(1, [0, 0], 64, 64, 32, "none", False)
     p, _, off = _device(c)
     assert p.forward(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), off).shape == (0, 64)
 
 
-@pytest.mark.parametrize("counts", [[3, 4], [100, 180]])
+@pytest.mark.parametrize("counts", [[3, 4], [100, 180], [4000, 300]])
 def test_streams_and_graphs(counts):
     """The same bits on another stream, from a captured graph, from two streams at once."""
     c = _product_case(17, counts, 264, 320, 64, "swiglu", False)

@@ -106,6 +106,111 @@ def test_pack_refusals(L):
     assert L.moe_q4_dequantize(1, 8, 32, 32, 1, None, A, None) == B.MOE_ERR_INVALID_ARG
 
 
+def _weights(**kw):
+    w = B.moe_q4_weights()
+    for n in ("w_gate", "b1", "b2", "logit_bias", "corr_bias"):
+        setattr(w, n, A)
+    for n in ("w1", "w3", "w2", "ws1", "ws3", "ws2"):
+        setattr(w, n, B.moe_q4_matrix(A, A))
+    w.group = 32
+    for n, v in kw.items():
+        setattr(w, n, v)
+    return w
+
+
+def _layer_cfg(**kw):
+    base = dict(T=4, D=64, F=32, E=8, k=2, act="swiglu", score="softmax", dtype="bf16", has_bias=False)
+    base.update(kw)
+    return B.make_config(**base)
+
+
+def _decode(L, c, w, x=A, y=A, idx=A, gate=A, ws=A, nbytes=1 << 40):
+    return L.moe_q4_decode(ctypes.byref(c), None if w is None else ctypes.byref(w), x, y, idx, gate, ws,
+                           nbytes, None)
+
+
+def _forward(L, c, w, x=A, y=A, ws=A, nbytes=1 << 40):
+    return L.moe_q4_forward(ctypes.byref(c), None if w is None else ctypes.byref(w), x, y, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("call", [_decode, _forward])
+def test_layer_refusals(L, call):
+    bad, no = B.MOE_ERR_INVALID_ARG, B.MOE_ERR_UNSUPPORTED
+    c = _layer_cfg()
+    for kw in (dict(dtype="f32"), dict(D=40), dict(F=40), dict(E=12), dict(k=9)):
+        assert call(L, _layer_cfg(**kw), _weights()) == no, kw
+    assert call(L, c, _weights(group=16)) == no
+    assert call(L, _layer_cfg(T=-1), _weights()) == bad
+    assert call(L, c, None) == bad
+    assert call(L, c, _weights(w_gate=None)) == bad
+    for n in ("w1", "w3", "w2"):
+        assert call(L, c, _weights(**{n: B.moe_q4_matrix(None, A)})) == bad
+        assert call(L, c, _weights(**{n: B.moe_q4_matrix(A, None)})) == bad
+        assert call(L, c, _weights(**{n: B.moe_q4_matrix(A + 8, A)})) == B.MOE_ERR_ALIGNMENT
+    for n in ("ws1", "ws3", "ws2"):
+        assert call(L, _layer_cfg(n_shared=1), _weights(**{n: B.moe_q4_matrix(A, None)})) == bad
+    biased = _layer_cfg(act="relu", has_bias=True)
+    for n in ("b1", "b2"):
+        assert call(L, biased, _weights(**{n: None})) == bad
+        assert call(L, biased, _weights(**{n: A + 4})) == B.MOE_ERR_ALIGNMENT
+    for kw in (dict(x=None), dict(y=None), dict(ws=None)):
+        assert call(L, c, _weights(), **kw) == bad
+    for kw in (dict(x=A + 8), dict(y=A + 8), dict(ws=A + 8)):
+        assert call(L, c, _weights(), **kw) == B.MOE_ERR_ALIGNMENT
+    assert call(L, c, _weights(), nbytes=64) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_decode_keeps_the_few_token_limits(L):
+    for kw in (dict(T=65), dict(D=16416), dict(F=8224), dict(F=4128, n_shared=2)):
+        assert _decode(L, _layer_cfg(**kw), _weights()) == B.MOE_ERR_UNSUPPORTED
+
+
+def test_workspace_grows_with_tokens():
+    last = 0
+    for T in list(range(0, 200, 7)) + [1000, 5000, 40000, 41000, 77824, 77825, 200000, 650000]:
+        n = B.moe_q4_workspace_size(_layer_cfg(T=T))
+        assert n >= last > -1
+        last = n
+    for kw in (dict(D=40), dict(F=40), dict(dtype="f32", E=8), dict(T=-1)):
+        assert B.moe_q4_workspace_size(_layer_cfg(**kw)) == 0
+
+
+def test_selftest_limits(L):
+    cfg = _cfg()
+    for limit in (0, -1, 2_000_000_001):
+        assert L.moe_q4_selftest_wait_timeout(ctypes.byref(cfg), A, A, _m(), A, A, limit, None) == \
+            B.MOE_ERR_INVALID_ARG
+
+
+def test_calls_on_another_device(monkeypatch):
+    """Tensors of a GPU that is not the current one never reach the library."""
+    from types import SimpleNamespace
+    calls = []
+
+    class Fake:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or B.MOE_OK
+
+    monkeypatch.setattr(B, "lib", lambda: Fake())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 77 + i)
+    monkeypatch.setattr(B, "_ptr", lambda t: None)
+    t = [SimpleNamespace(device=torch.device("cuda", i), numel=lambda: 0) for i in range(2)]
+    m, c, w, cfg = B.moe_q4_matrix(), B.moe_q4_product_config(), B.moe_q4_weights(), _layer_cfg()
+    for call in (lambda v: B.moe_q4_quantize(1, 8, 32, 32, "f32", v, v, v),
+                 lambda v: B.moe_q4_dequantize(1, 8, 32, 32, "f32", m, v),
+                 lambda v: B.moe_q4_product(c, v, v, m, None, None, v, v),
+                 lambda v: B.moe_q4_selftest_wait_timeout(c, v, v, m, v, v, 5),
+                 lambda v: B.moe_q4_decode(cfg, w, v, v, v), lambda v: B.moe_q4_forward(cfg, w, v, v, v),
+                 lambda v: B.moe_q4_status(cfg, v)):
+        n = len(calls)
+        call(t[0])
+        assert len(calls) == n + 1
+        with pytest.raises(ValueError, match="cuda:1"):
+            call(t[1])
+        assert len(calls) == n + 1
+
+
 def test_struct_layout(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
@@ -151,6 +256,36 @@ def test_matrix_refusals():
         m.codes = codes
     with pytest.raises(AttributeError):
         m.group = 64
+
+
+def test_decoder_refusals():
+    from sparse_mixture_experts_softmax_gb300.decode import MoEDecoder
+    from sparse_mixture_experts_softmax_gb300.q4_layer import Q4Layer
+    g, up, down = torch.zeros(8, 64), _matrix(8, 32, 64), _matrix(8, 64, 32)
+    for kw in (dict(w2=_matrix(8, 32, 64)), dict(w2=_matrix(8, 64, 32, 64)),
+               dict(w2=torch.zeros(8, 64, 32, dtype=torch.bfloat16)), dict(w3=torch.zeros(8, 32, 64)),
+               dict(w3=None), dict(w3=_matrix(8, 40, 64)), dict(n_shared=1),
+               dict(n_shared=1, ws1=_matrix(1, 32, 64), ws3=_matrix(1, 32, 64), ws2=_matrix(1, 64, 64)),
+               dict(w_gate=torch.zeros(8, 32)), dict(w1=torch.zeros(8, 32, 64).bfloat16())):
+        args = dict(w_gate=g, w1=up, w2=down, w3=up, act="swiglu", k=2)
+        args.update(kw)
+        for cls in (MoEDecoder, Q4Layer):
+            with pytest.raises(ValueError):
+                cls(**args)
+    with pytest.raises(ValueError, match="Q4Matrix"):        # plain weights make a decoder, not a Q4Layer
+        Q4Layer(g, torch.zeros(8, 32, 64).bfloat16(), torch.zeros(8, 64, 32).bfloat16(), act="relu", k=2)
+    layer = Q4Layer(g, up, down, w3=up, act="swiglu", k=2, max_tokens=3)
+    for x in (torch.zeros(4, 64).bfloat16(), torch.zeros(3, 64), torch.zeros(3, 32).bfloat16()):
+        with pytest.raises(ValueError):
+            layer.forward(x)
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros(3, 64).bfloat16(), torch.zeros(3, 64).bfloat16())
+    with pytest.raises(ValueError, match="GPU"):
+        layer.forward(torch.zeros(3, 64).bfloat16())
+    with pytest.raises(AttributeError):
+        layer.workspace = None
+    with pytest.raises(ValueError):
+        Q4Layer(g, up, down, w3=up, act="swiglu", k=2, max_tokens=0)
 
 
 def test_quantize_refusals():
