@@ -14,7 +14,7 @@ import torch
 
 from . import binding as B
 
-_TYPE = {torch.float32: "f32", torch.bfloat16: "bf16"}
+_CODE = {torch.float32: B.DTYPE["f32"], torch.bfloat16: B.DTYPE["bf16"]}
 
 
 def _want(name, t, dtype, shape, device):
@@ -37,12 +37,7 @@ class Q4Matrix:
     used in place (in the storage that they have when the object is made) and change in
     place only."""
 
-    __slots__ = ("codes", "scales", "group", "E", "N", "K", "device", "_held", "_c", "_ref")
-
-    def __setattr__(self, name, value):
-        if hasattr(self, name):
-            raise AttributeError(f"{name} is fixed when the matrix is made")
-        object.__setattr__(self, name, value)
+    __slots__ = ("_codes", "_scales", "_group", "_shape", "_device", "_held", "_c", "_ref")
 
     def __init__(self, codes, scales, group):
         if group not in B.Q4_GROUPS:
@@ -54,27 +49,24 @@ class Q4Matrix:
             raise ValueError(f"N must be a multiple of 8 and K of 32, got {(E, N, K)}")
         _want("codes", codes, torch.uint8, (E, N, K // 2), codes.device)
         _want("scales", scales, torch.bfloat16, (E, -(-K // group), N), codes.device)
-        self._set(codes.detach(), scales.detach(), int(group), E, N, K)
+        self._set(codes.detach(), scales.detach(), int(group), (E, N, K))
 
-    def _set(self, codes, scales, group, E, N, K):
-        put = object.__setattr__
-        c = B.moe_q4_matrix(codes.data_ptr(), scales.data_ptr())
-        # _held: what the addresses are of, whatever becomes of the attributes' storage
-        for name, value in (("codes", codes), ("scales", scales), ("group", group), ("E", E), ("N", N),
-                            ("K", K), ("device", codes.device), ("_c", c), ("_ref", ctypes.byref(c)),
-                            ("_held", (codes.detach(), scales.detach()))):
-            put(self, name, value)
+    def _set(self, codes, scales, group, shape):
+        self._codes, self._scales, self._group, self._shape = codes, scales, group, shape
+        self._device = codes.device
+        # what the addresses are of, whatever becomes of the attributes' storage
+        self._held = codes.detach(), scales.detach()
+        self._c = c = B.moe_q4_matrix(codes.data_ptr(), scales.data_ptr())
+        self._ref = ctypes.byref(c)
 
-    @classmethod
-    def _new(cls, E, N, K, group, device):
-        m = cls.__new__(cls)
-        m._set(torch.empty((E, N, K // 2), dtype=torch.uint8, device=device),
-               torch.empty((E, -(-K // group), N), dtype=torch.bfloat16, device=device), group, E, N, K)
-        return m
-
-    @property
-    def shape(self):
-        return (self.E, self.N, self.K)
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    group = property(lambda self: self._group)
+    shape = property(lambda self: self._shape)
+    device = property(lambda self: self._device)
+    E = property(lambda self: self._shape[0])
+    N = property(lambda self: self._shape[1])
+    K = property(lambda self: self._shape[2])
 
     def c_matrix(self) -> B.moe_q4_matrix:
         """The matrix as the C ABI takes it; it keeps no tensor alive."""
@@ -82,14 +74,17 @@ class Q4Matrix:
 
     def dequantize(self, dtype=torch.bfloat16, out=None):
         """The weights [E, N, K] (bfloat16 values, in float32 where asked)."""
+        kind = _CODE.get(dtype if out is None else out.dtype)
+        if kind is None:
+            raise ValueError("the weights are float32 or bfloat16, not "
+                             f"{dtype if out is None else out.dtype}")
         if out is None:
-            out = torch.empty(self.shape, dtype=dtype, device=self.device)
-        if out.dtype not in _TYPE:
-            raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
-        _want("out", out, out.dtype, self.shape, self.device)
-        status = B.lib().moe_q4_dequantize(self.E, self.N, self.K, self.group,
-                                           B.DTYPE[_TYPE[out.dtype]], self._ref, out.data_ptr(),
-                                           B._stream_on(None, self.device))
+            out = torch.empty(self._shape, dtype=dtype, device=self._device)
+        else:
+            _want("out", out, out.dtype, self._shape, self._device)
+        E, N, K = self._shape
+        status = B.lib().moe_q4_dequantize(E, N, K, self._group, kind, self._ref, out.data_ptr(),
+                                           B._stream_on(None, self._device))
         if status != B.MOE_OK:
             B._check("moe_q4_dequantize", status)
         return out
@@ -100,24 +95,25 @@ def quantize(w, group=64, out=None) -> Q4Matrix:
     group's scale is the smallest value of five significant bits that is not below
     max |w| / 7, its codes 8 + the nearest whole numbers to w / scale.  ``out``: a
     matrix of that shape and group that is rewritten (what was made with it follows)."""
-    if w.dtype not in _TYPE:
+    kind, device = _CODE.get(w.dtype), w.device
+    if kind is None:
         raise ValueError(f"w must be float32 or bfloat16, got {w.dtype}")
     if group not in B.Q4_GROUPS:
         raise ValueError(f"group must be one of {B.Q4_GROUPS}, got {group}")
-    if w.dim() == 2:
-        w = w.unsqueeze(0)
-    if w.dim() != 3 or w.numel() == 0 or w.shape[1] % 8 or w.shape[2] % 32:
-        raise ValueError("w must be [E, N, K] with N a multiple of 8 and K of 32, got "
+    shape = (1,) * (w.dim() == 2) + tuple(w.shape)
+    if len(shape) != 3 or 0 in shape or shape[1] % 8 or shape[2] % 32 or not w.is_contiguous():
+        raise ValueError("w must be contiguous [E, N, K] with N a multiple of 8 and K of 32, got "
                          f"{tuple(w.shape)}")
-    E, N, K = w.shape
-    _want("w", w, w.dtype, (E, N, K), w.device)
+    E, N, K = shape
     if out is None:
-        out = Q4Matrix._new(E, N, K, group, w.device)
-    elif out.shape != (E, N, K) or out.group != group or out.device != w.device:
+        out = Q4Matrix.__new__(Q4Matrix)
+        out._set(torch.empty((E, N, K // 2), dtype=torch.uint8, device=device),
+                 torch.empty((E, -(-K // group), N), dtype=torch.bfloat16, device=device), group, shape)
+    elif out.shape != shape or out.group != group or out.device != device:
         raise ValueError(f"out is {out.shape} with groups of {out.group} on {out.device}, w asks "
-                         f"for {(E, N, K)} with groups of {group} on {w.device}")
-    status = B.lib().moe_q4_quantize(E, N, K, group, B.DTYPE[_TYPE[w.dtype]], w.data_ptr(),
-                                     out._c.codes, out._c.scales, B._stream_on(None, w.device))
+                         f"for {shape} with groups of {group} on {device}")
+    status = B.lib().moe_q4_quantize(E, N, K, group, kind, w.data_ptr(), out._c.codes, out._c.scales,
+                                     B._stream_on(None, device))
     if status != B.MOE_OK:
         B._check("moe_q4_quantize", status)
     return out
@@ -156,6 +152,7 @@ class Q4Product:
         if w.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
             raise ValueError("a product cannot be made while its stream is being captured")
         self.shape, self.device = w.shape, w.device
+        self._offsets_shape = torch.Size((w.E + 1,))
         self._held = w._held, None if w3 is None else w3._held, None if bias is None else bias.detach()
         self._w = w.c_matrix()
         self._w3 = None if w3 is None else w3.c_matrix()
@@ -172,29 +169,33 @@ class Q4Product:
         or leave 0 .. R are clamped.  Rows outside of every expert's are not read and are
         left as they are in ``out`` (undefined without one)."""
         E, N, K = self.shape
-        shape = x.shape
+        device, shape = self.device, x.shape
         if (len(shape) != 2 or shape[1] != K or x.dtype is not torch.bfloat16 or
-                x.device != self.device or not x.is_contiguous()):
-            raise ValueError(f"x must be contiguous bfloat16 [R, {K}] on {self.device}, got {x.dtype} "
+                x.device != device or not x.is_contiguous()):
+            raise ValueError(f"x must be contiguous bfloat16 [R, {K}] on {device}, got {x.dtype} "
                              f"{tuple(shape)} on {x.device}")
-        if (offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or
-                offsets.device != self.device or not offsets.is_contiguous()):
-            raise ValueError(f"offsets must be contiguous int32 [{E + 1}] on {self.device}, got "
+        if (offsets.dtype is not torch.int32 or offsets.shape != self._offsets_shape or
+                offsets.device != device or not offsets.is_contiguous()):
+            raise ValueError(f"offsets must be contiguous int32 [{E + 1}] on {device}, got "
                              f"{offsets.dtype} {tuple(offsets.shape)} on {offsets.device}")
         R = shape[0]
-        if out is None:
-            out = torch.empty((R, N), dtype=torch.bfloat16, device=self.device)
-        else:
-            _want("out", out, torch.bfloat16, (R, N), self.device)
         c = self._calls.get(R)
         if c is None:
             if len(self._calls) >= 64:
                 self._calls.clear()
             cfg = self._make(R)
-            c = self._calls[R] = cfg, ctypes.byref(cfg)
+            # (a new tensor like another takes half the time of one from its shape)
+            like = torch.empty((R, N), dtype=torch.bfloat16, device=device) if R <= 64 else None
+            c = self._calls[R] = cfg, ctypes.byref(cfg), like
+        if out is not None:
+            _want("out", out, torch.bfloat16, (R, N), device)
+        elif c[2] is not None:
+            out = torch.empty_like(c[2])
+        else:
+            out = torch.empty((R, N), dtype=torch.bfloat16, device=device)
         status = B.lib().moe_q4_product(c[1], offsets.data_ptr(), x.data_ptr(), self._refs[0],
                                         self._refs[1], self._bias, out.data_ptr(), self._status,
-                                        B._stream_on(None, self.device))
+                                        B._stream_on(None, device))
         if status != B.MOE_OK:
             B._check("moe_q4_product", status)
         return out
