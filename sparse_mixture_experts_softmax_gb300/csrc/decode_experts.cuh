@@ -310,8 +310,7 @@ template <bool UP, bool Q4W> struct MmaProducts {
   // or an overflowing product's infinity, and they overflow only where it does.
   __device__ __forceinline__ float total(int t8, int c) const {
     const float first = acc[t8][0][c] + acc[t8][1][c];
-    float sum = first;
-    if (!UP && isfinite(first)) sum += acc[t8][CH - 2][c] + acc[t8][CH - 1][c];
+    const float sum = UP || !isfinite(first) ? first : first + (acc[t8][CH - 2][c] + acc[t8][CH - 1][c]);
     return Q4W ? Q4_UNSCALE * sum : sum;
   }
   __device__ __forceinline__ void begin(const Part&, const char* rows, int pitch, int tokens, int lane) {
@@ -555,8 +554,10 @@ template <typename WT, bool UP> struct LayerJob {
   }
   // the bias of row `lane` of an item
   __device__ __forceinline__ float bias(const Part& p, const Tile& tl, int block, int lane) const {
-    if (!UP || a.b1 == nullptr || lane >= 16 || block * 16 + lane >= p.width) return 0.f;
-    return __ldg(a.b1 + (long long)tl.e * a.F + block * 16 + lane);
+    float b = 0.f;
+    if (UP && a.b1 != nullptr && lane < 16 && block * 16 + lane < p.width)
+      b = __ldg(a.b1 + (long long)tl.e * a.F + block * 16 + lane);
+    return b;
   }
   __device__ __forceinline__ void out(const Part&, const Tile& tl, int block, int row, int tok, float v0,
                                       float v1, float b0, float b1) const {
@@ -606,7 +607,11 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
       q4_upper = has_upper(p, lb);
     }
   };
-  if (li < p.hi) begin_item();
+  if constexpr (kQ4<WT>) {
+    if (li < p.hi) begin_item();
+  } else {
+    lp = li < p.hi ? item_rows<WT>(p, tiles, lt, lb) : nullptr;
+  }
   auto put = [&] {
     const int v0 = kQ4<WT> ? 0 : (ls * KS + ks) * SV;
     if (li < p.hi && v0 < K) {     // (4-bit weights: q4_left and q4_groups tell where the row ends)
@@ -628,16 +633,17 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
         q4_groups -= KS * (SV >> p.log_g);
       } else {
         const uint32_t dst = ring + put_slot * STAGE + lane * 16;
-        const int at = v0 * (PIECE / SV) + lane * 16;
-        const bool on = at < row;
+        constexpr int ES = PIECE / SV;
+        const int at = v0 * ES + lane * 16;
+        const bool on = at < K * ES;
         const char* src = lp + (on ? at : 0);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) copy16((dst + r * PIECE) ^ ((r & 1) << 6), src + (long long)r * row, on);
+        for (int r = 0; r < 8; ++r) copy16((dst + r * PIECE) ^ ((r & 1) << 6), src + (long long)r * K * ES, on);
         if (has_upper(p, lb)) {
           src += p.second;
 #pragma unroll
           for (int r = 0; r < 8; ++r)
-            copy16((dst + (8 + r) * PIECE) ^ ((r & 1) << 6), src + (long long)r * row, on);
+            copy16((dst + (8 + r) * PIECE) ^ ((r & 1) << 6), src + (long long)r * K * ES, on);
         }
       }
     }
@@ -656,7 +662,7 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
     lp += item_step;
     if (lb >= p.per && li < p.hi) {
       do { lb -= p.per; ++lt; } while (lb >= p.per);
-      begin_item();
+      lp = item_rows<WT>(p, tiles, lt, lb);
     }
   };
 #pragma unroll
