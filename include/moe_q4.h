@@ -15,7 +15,8 @@
  *          last group of an output ending with its inputs,
  * and stands for the weights  w = (code - 8) scale,  code 0 to 15, rounded to bf16.
  * Scales of up to five significant bits, such as moe_q4_quantize writes, make that
- * rounding exact.  N is a multiple of 8, K of 32, and group is 32, 64 or 128.
+ * rounding exact.  N is a multiple of 8, K of 32, both at most MOE_Q4_MAX_SIDE, and
+ * group is 32, 64 or 128.
  *
  * The conventions of moe.h hold: device pointers, 16-byte aligned, dense
  * row-major tensors, caller-owned memory, work enqueued on `stream`, arguments
@@ -31,6 +32,7 @@
 extern "C" {
 #endif
 
+#define MOE_Q4_MAX_SIDE (1 << 28)
 typedef struct {
   const void* codes;
   const void* scales;
@@ -51,6 +53,7 @@ MOE_API moe_status moe_q4_dequantize(int32_t E, int32_t N, int32_t K, int32_t gr
 
 #define MOE_Q4_ACT_NONE 3
 #define MOE_Q4_MAX_EXPERTS 256
+#define MOE_Q4_MAX_ROWS (1 << 30)
 typedef struct {
   int32_t R;           /* rows of x and c                                       */
   int32_t E, N, K;     /* experts, outputs, inputs                              */
@@ -65,7 +68,9 @@ typedef struct {
  * matrices; bias [E, N] fp32 or NULL (NULL with MOE_ACT_SWIGLU).  offsets [E+1]
  * (int32) lie on the device; values that decrease or leave [0, R] are clamped.
  * Rows outside of every segment are not read and left as they are in c.  c must
- * not overlap an input.  E <= MOE_Q4_MAX_EXPERTS, R K and R N < 2^40.
+ * not overlap an input.  E <= MOE_Q4_MAX_EXPERTS, R <= MOE_Q4_MAX_ROWS, R K and
+ * R N < 2^40.  Here, in moe_q4_decode and in moe_q4_forward, weights below 2^-118 in
+ * magnitude are rounded to multiples of 2^-125, and sums below it may lose bits.
  * dev_status (int32, device) receives MOE_ERR_TIMEOUT where a bounded device-side
  * wait expired (c is then invalid), and is left as it is otherwise.  The order of a
  * row's sums goes with the call's rows and shape: the same call gives the same bits, a
@@ -102,10 +107,10 @@ MOE_API moe_status moe_q4_decode(const moe_config* cfg, const moe_q4_weights* w,
 
 /* moe_forward with those weights, for any T, in a workspace of its own (its size
  * grows with T: one made for the most tokens serves every call): x [T, D] bf16,
- * y [T, D] fp32, which must not overlap x or a weight.  Hidden activations and the experts' outputs are rounded to
- * bf16, as in moe_forward.  moe_q4_status reads the last call's device status: 0,
- * or MOE_ERR_TIMEOUT when a bounded device-side wait expired (y is then invalid).
- * It synchronises `stream`. */
+ * y [T, D] fp32, which must not overlap x or a weight.  Hidden activations and the
+ * experts' outputs are rounded to bf16, as in moe_forward.  T k <= MOE_Q4_MAX_ROWS.
+ * moe_q4_status reads the last call's device status: 0, or MOE_ERR_TIMEOUT when a
+ * bounded device-side wait expired (y is then invalid).  It synchronises `stream`. */
 MOE_API size_t moe_q4_workspace_size(const moe_config* cfg);
 MOE_API moe_status moe_q4_forward(const moe_config* cfg, const moe_q4_weights* w, const void* x,
                                   float* y, void* workspace, size_t workspace_bytes, void* stream);

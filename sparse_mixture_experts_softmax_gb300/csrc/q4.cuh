@@ -14,13 +14,16 @@ __device__ __forceinline__ uint32_t q4_fma(uint32_t a, uint32_t b, uint32_t c) {
 
 // The weights of a word's eight codes, (code - 8) scale, for a scale of any bits (in both
 // halves of scale2).  128 + code is the bf16 value whose last four bits are the code;
-// taking 136 from it is exact, so the product is the only rounding.
+// taking 136 from it is exact, so the product is the only rounding.  SCALED: the weights
+// times 2^-8 (also where the scale times 2^-8 would not be a bf16 value).
+template <bool SCALED = false>
 __device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t scale2) {
+  constexpr uint32_t one = SCALED ? 0x3b803b80u : 0x3f803f80u, less = SCALED ? 0xbf08bf08u : 0xc308c308u;
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t b = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    v[i] = q4_fma(q4_fma(b, 0x3f803f80u, 0xc308c308u), scale2, 0x80008000u);
+    v[i] = q4_fma(q4_fma(b, one, less), scale2, 0x80008000u);
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
@@ -33,7 +36,8 @@ __device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t scale2) {
 //   code 2^-133 (scale 2^125) - scale 2^-5  =  (code - 8) scale 2^-8
 // is one fma, whose only rounding is that of the weight.  The scales for which those
 // factors are normal numbers, 2^-121 to 2^3, take it; a warp with another among its
-// lanes' goes by q4_word.
+// lanes' goes by q4_word.  Either way a weight below 2^-118 is rounded to a multiple of
+// 2^-125 (its 2^-8 to one of 2^-133, the least bf16 number).
 constexpr float Q4_UNSCALE = 256.f;
 // Bits 15 and 31: whether the two bf16 scales of a word take it (as zeros do).
 __device__ __forceinline__ uint32_t q4_fast(uint32_t scales) {
@@ -59,19 +63,10 @@ __device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32
                              q4_fma(x & 0x000f000fu, low, add), q4_fma(x & 0x00f000f0u, high, add));
       }
     } else {
-      const uint32_t scale2 = q4_fma(two[u], 0x3b803b80u, 0x80008000u);          // 2^-8
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[u][i] = q4_word(r[u][i], scale2);
+      for (int i = 0; i < 4; ++i) v[u][i] = q4_word<true>(r[u][i], two[u]);
     }
   }
-}
-// The same by a whole warp, which takes one branch.
-__device__ __forceinline__ void q4_runs(const uint4& w0, const uint4& w1, uint32_t bits0, uint32_t bits1,
-                                        uint4 (&v)[2][4]) {
-  if (__all_sync(0xffffffffu, (q4_fast(__byte_perm(bits0, bits1, 0x5410)) & 0x80008000u) == 0x80008000u))
-    q4_runs<true>(w0, w1, bits0, bits1, v);
-  else
-    q4_runs<false>(w0, w1, bits0, bits1, v);
 }
 
 // Inclusive scan over the threads of a block (those without a value pass a neutral one):

@@ -52,6 +52,7 @@ Layout forward_layout(const moe_config& c) {
 moe_status check_forward(const moe_config* cfg) {
   RET_IF(validate_config(cfg));
   if (cfg->dtype != MOE_BF16 || cfg->D % 32 != 0 || cfg->F % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((long long)cfg->T * cfg->k > MOE_Q4_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 moe_status check_forward_ws(const moe_config& c, const void* ws, size_t bytes) {
@@ -68,7 +69,7 @@ moe_status run_product(const moe_q4_product_config* cfg, const int32_t* offsets,
   RET_IF(check_q4_shape(cfg->E, cfg->N, cfg->K, cfg->group));
   if (cfg->act < 0 || cfg->act > MOE_Q4_ACT_NONE) return MOE_ERR_INVALID_ARG;
   const bool swiglu = cfg->act == MOE_ACT_SWIGLU;
-  if (cfg->E > MOE_Q4_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  if (cfg->E > MOE_Q4_MAX_EXPERTS || cfg->R > MOE_Q4_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
   if ((long long)cfg->R * cfg->K >= (1LL << 40) || (long long)cfg->R * cfg->N >= (1LL << 40))
     return MOE_ERR_UNSUPPORTED;
   if (!offsets || !w || !dev_status || swiglu != (w3 != nullptr)) return MOE_ERR_INVALID_ARG;

@@ -10,7 +10,7 @@ namespace api {
 inline moe_status check_q4_shape(int32_t E, int32_t N, int32_t K, int32_t group) {
   if (E <= 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
-  if (N % 8 != 0 || K % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (N % 8 != 0 || K % 32 != 0 || N > MOE_Q4_MAX_SIDE || K > MOE_Q4_MAX_SIDE) return MOE_ERR_UNSUPPORTED;
   if ((long long)E * N >= (1LL << 31) || (long long)E * N * K >= (1LL << 40))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

@@ -33,12 +33,12 @@ constexpr int BM = 128, BK = 64, UK = 16, RAW_K = 128;
 constexpr int CODE_BYTES = BM * RAW_K / 2;               // 8 KB
 constexpr int RAW_BYTES = CODE_BYTES + BM * (RAW_K / 32) * 2;   // + the scales, up to 1 KB
 // Heights of a copy of x: the least that has a tile's rows.
-constexpr int X_BOXES = 8;
+constexpr int X_BOXES = 7;
 __host__ __device__ constexpr int box_rows(int i) { return i < 4 ? 16 * (i + 1) : 32 * (i - 1); }
 __host__ __device__ constexpr int box_of(int rows) { return rows <= 64 ? (rows - 1) / 16 : (rows - 1) / 32 + 2; }
-static_assert(box_rows(0) == 16 && box_rows(3) == 64 && box_rows(4) == 96 && box_rows(7) == 192, "heights");
+static_assert(box_rows(0) == 16 && box_rows(3) == 64 && box_rows(4) == 96 && box_rows(6) == 160, "heights");
 static_assert(box_of(1) == 0 && box_of(64) == 3 && box_of(65) == 4 && box_of(96) == 4 && box_of(97) == 5 &&
-              box_of(192) == 7, "heights");
+              box_of(160) == 6, "heights");
 constexpr int W_RAW = 0, W_MMA = 1, W_EPI = 2, W_X = 6, W_WIDEN = 7;
 constexpr int MAX_E = 256;
 constexpr int TMEM_COLS = 512;
@@ -52,6 +52,7 @@ constexpr long long LIMIT_NS = 2000000000ll;             // bound of every wait
 // multiples of the groups.  Of a tile's last stage, where it has 64 inputs or less, the
 // second half is without work.
 constexpr int BN = 160, Q = 6, SA = 3, SX = 4;
+static_assert(box_of(BN) == X_BOXES - 1 && box_rows(X_BOXES - 1) == BN, "heights");
 constexpr int NG = 3, N_WIDEN = 4 * NG, THREADS = 32 * (W_WIDEN + N_WIDEN);
 constexpr int X_HALF = BN * BK * 2, X_STAGE = 2 * X_HALF;
 constexpr int SMEM = SX * X_STAGE + Q * RAW_BYTES;
@@ -352,7 +353,6 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     }
     __syncwarp();
   } else if (warp >= W_WIDEN) {
-    // a warp may only write its own quarter of the tensor memory's lanes
     // a warp may only write its own quarter of the tensor memory's lanes
     const int group = (warp - W_WIDEN) >> 2, quarter = warp & 3;
     // this lane's output in a raw stage; SwiGLU: 16 outputs of W and the same 16 of W3

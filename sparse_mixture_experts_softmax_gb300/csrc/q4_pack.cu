@@ -188,7 +188,7 @@ q4_quantize_kernel(const Q4Shape s, const T* __restrict__ w, uint32_t* __restric
     v[r].get(x);
     uint32_t differ, word;
     if (plain) word = codes_of(x, scale[r], differ);
-    if (!plain || (sizeof(T) == 4 && differ != 0u)) 
+    if (!plain || (sizeof(T) == 4 && differ != 0u))
       word = codes_of_any(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale[r]);
     *to = word;
   }

@@ -230,6 +230,27 @@ def test_product_scales_of_any_size(counts, scale):
     _check(c, p.forward(x, off))
 
 
+@pytest.mark.parametrize("counts", [[4], [40, 90], [3000, 1200]])
+@pytest.mark.parametrize("low,high", [(-133, -126), (-130, -110), (-121, -116)])
+def test_product_smallest_scales(counts, low, high):
+    """Weights down to the least bf16 number.  The kernels round a weight once, to a
+    multiple of 2^-125 where it is below 2^-118 (half a step: 2^-126), the plain form to a
+    multiple of 2^-133 or 8 bits (half a step below 2^-118: 2^-127)."""
+    c = _product_case(23, counts, 72, 320, 32, "none", False)
+    codes, s = c["m"]
+    rng = np.random.default_rng(24)
+    c["m"] = (codes, C.bf16(np.ldexp(rng.uniform(1, 2, s.shape), rng.integers(low, high, s.shape))))
+    c["x"] = C.bf16(np.ldexp(c["x"], 60))
+    p, x, off = _device(c)
+    got = p.forward(x, off).double().cpu().numpy()
+    w = C.weights(*c["m"], 32)
+    for e, (lo, hi) in enumerate(zip(c["offsets"][:-1], c["offsets"][1:])):
+        y, err = C.product_row_block("none", c["x"][lo:hi], w[e])
+        err = err + (2.0 ** -126 + 2.0 ** -127) * np.abs(c["x"][lo:hi]).sum(1, keepdims=True)
+        assert (np.abs(got[lo:hi] - y) <= C.BF16_HALF * np.abs(y) + err * (1 + C.BF16_HALF)).all()
+    assert p.status() == 0
+
+
 @pytest.mark.parametrize("counts", [[3, 4], [20, 50], [150, 150], [200, 4000]])
 def test_rows_do_not_mix(counts):
     """A row of NaN and one of infinities stay in their rows, a NaN and an infinite scale

@@ -62,7 +62,9 @@ def _call(L, cfg, off=A, x=A, w=True, w3=None, bias=None, c=A, status=A):
 
 @pytest.mark.parametrize("kw", [dict(N=12), dict(K=48), dict(group=16), dict(group=0), dict(group=48),
                                 dict(E=257), dict(N=1 << 28, K=1 << 12), dict(E=256, N=1 << 23),
-                                dict(R=2**31 - 1, K=1 << 12), dict(R=2**31 - 1, N=1 << 12)])
+                                dict(R=2**31 - 1, K=1 << 12), dict(R=2**31 - 1, N=1 << 12),
+                                dict(R=(1 << 30) + 1), dict(R=1, K=(1 << 28) + 32),
+                                dict(E=1, N=(1 << 28) + 8)])
 def test_product_unsupported(L, kw):
     assert _call(L, _cfg(**kw)) == B.MOE_ERR_UNSUPPORTED
 
@@ -94,7 +96,8 @@ def test_pack_refusals(L):
         for args, want in [((0, 8, 32, 32, 0), 1), ((1, -8, 32, 32, 0), 1), ((1, 8, 0, 32, 0), 1),
                            ((1, 8, 32, 32, 2), 1), ((1, 8, 32, 32, -1), 1), ((1, 12, 32, 32, 0), 2),
                            ((1, 8, 40, 32, 0), 2), ((1, 8, 32, 40, 0), 2), ((1 << 20, 1 << 12, 32, 32, 0), 2),
-                           ((1 << 10, 1 << 15, 1 << 16, 32, 0), 2)]:
+                           ((1 << 10, 1 << 15, 1 << 16, 32, 0), 2), ((1, 8, (1 << 28) + 32, 32, 0), 2),
+                           ((1, (1 << 28) + 8, 32, 32, 0), 2)]:
             assert fn(*args, A, A, A) == want, args
         ok = (1, 8, 32, 32, 1)
         for i in range(3):
@@ -171,7 +174,7 @@ def test_workspace_grows_with_tokens():
         n = B.moe_q4_workspace_size(_layer_cfg(T=T))
         assert n >= last > -1
         last = n
-    for kw in (dict(D=40), dict(F=40), dict(dtype="f32", E=8), dict(T=-1)):
+    for kw in (dict(D=40), dict(F=40), dict(dtype="f32", E=8), dict(T=-1), dict(T=(1 << 30) + 8, k=1)):
         assert B.moe_q4_workspace_size(_layer_cfg(**kw)) == 0
 
 
