@@ -170,6 +170,12 @@ __device__ __forceinline__ float bf16_part(float v) {
   const float h = __bfloat162float(__float2bfloat16_rn(v));
   return isinf(h) ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : h;
 }
+// Warps to a token's row, as a power of two: all of them for one token, whose row is
+// then one round of loads or two.
+template <int CW>
+__device__ __forceinline__ int warps_a_token(int n) {
+  return max(31 - __clz(CW) - (32 - __clz(n - 1)), 0);
+}
 // A tile's token rows into shared memory (two planes for hidden activations of a
 // bf16 layer, whose rows have zeros from K to the next multiple of BLOCK).  Beside
 // 4-bit weights, of which a lane reads four words at once, the 16-byte pieces of 128
@@ -181,21 +187,23 @@ __device__ __forceinline__ void load_tile(const DecodeArgs& a, const Routing& rt
   typedef typename Stored<WT>::Act Act;
   constexpr int BLOCK = Stored<WT>::BLOCK;
   const int pitch = row_pitch<WT>(K), plane = tl.n * pitch;
-  for (int t = threadIdx.x >> 5; t < tl.n; t += Stored<WT>::CW) {              // a warp a token
+  const int lg = warps_a_token<Stored<WT>::CW>(tl.n);
+  const int c0 = threadIdx.x & ((32 << lg) - 1), step = 32 << lg;
+  for (int t = threadIdx.x >> 5 >> lg; t < tl.n; t += Stored<WT>::CW >> lg) {
     const int tok = tl.e >= 0 && UP ? rt.tok[tl.start + t] : tl.start + t;
     const Act* x = static_cast<const Act*>(a.x) + (long long)tok * a.D;
     const float* h = (tl.e >= 0 ? a.hidden : a.hidden_s) + (long long)tok * K;
     if constexpr (!kBf16Tokens<WT>) {
       const float* src = UP ? reinterpret_cast<const float*>(x) : h;
 #pragma unroll 4
-      for (int c = threadIdx.x & 31; c < K / 4; c += 32)
+      for (int c = c0; c < K / 4; c += step)
         *reinterpret_cast<uint4*>(rows + t * pitch + c * 16) =
             __ldcg(reinterpret_cast<const uint4*>(src) + c);
       continue;
     }
     const int pieces = (K + BLOCK - 1) / BLOCK * (BLOCK / 8);      // of 8 values
 #pragma unroll 4
-    for (int c = threadIdx.x & 31; c < pieces; c += 32) {
+    for (int c = c0; c < pieces; c += step) {
       const int at = kQ4<WT> ? (c & ~15) | (c & 3) << 2 | (c >> 2 & 3) : c;
       char* to = rows + t * pitch + at * 16;
       const bool on = c * 8 < K;

@@ -37,10 +37,11 @@ struct RowsJob {
   __device__ __forceinline__ void wait_tokens() const {}
   __device__ __forceinline__ void load(const Tile& tl, int K, char* rows) const {
     const int pitch = row_pitch<Q4>(K), pieces = (K + 127) / 128 * 16;       // of 8 values
-    for (int t = threadIdx.x >> 5; t < tl.n; t += CW_) {
+    const int lg = warps_a_token<CW_>(tl.n), step = 32 << lg;
+    for (int t = threadIdx.x >> 5 >> lg; t < tl.n; t += CW_ >> lg) {
       const bf16* x = static_cast<const bf16*>(p.x) + (long long)(tl.start + t) * K;
 #pragma unroll 4
-      for (int c = threadIdx.x & 31; c < pieces; c += 32) {
+      for (int c = threadIdx.x & (step - 1); c < pieces; c += step) {
         const int at = (c & ~15) | (c & 3) << 2 | (c >> 2 & 3);             // (as load_tile has it)
         *reinterpret_cast<uint4*>(rows + t * pitch + at * 16) =
             c * 8 < K ? __ldg(reinterpret_cast<const uint4*>(x + c * 8)) : make_uint4(0u, 0u, 0u, 0u);
