@@ -426,16 +426,6 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
     uint32_t x[2] = {this->at0 + v0 * 2, this->at1 + v0 * 2};
     uint32_t scales = from + scale_at;
     const uint32_t codes = from + code_at;       // (a stage starts at a multiple of 256 bytes)
-    if (FAST && end == PIECE) {
-#pragma unroll
-      for (int u = 0; u < PIECE; u += 64) {
-        block<FAST, T8>(codes ^ u, scales, x);
-        scales += scale_step;
-        x[0] += 256;
-        x[1] += 256;
-      }
-      return;
-    }
 #pragma unroll 1
     for (int u = 0; u < end; u += 64) {
       block<FAST, T8>(codes ^ u, scales, x);
