@@ -186,7 +186,7 @@ cudaError_t launch_decode_init(int* ctl, cudaStream_t st) {
 }
 
 cudaError_t launch_decode(int kind, const DecodeArgs& a, cudaStream_t st) {
-  if (kind == DECODE_Q4) return launch_t<Q4>(a, st);
+  if (kind == DECODE_Q4) return a.T <= most_tokens<Q4Few>() ? launch_t<Q4Few>(a, st) : launch_t<Q4>(a, st);
   return kind == DECODE_BF16 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
 }
 

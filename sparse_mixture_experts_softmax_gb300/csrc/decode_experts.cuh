@@ -17,6 +17,7 @@ constexpr int WARPS = 16, THREADS = WARPS * 32;
 // The tokens' rows have zeros up to a multiple of BLOCK values, which is what a lane
 // group of the products takes at once.
 struct Q4 {};                                   // 4-bit weights (q4.cuh)
+struct Q4Few {};                                // the same, of a call of at most four tokens
 template <typename WT> struct Stored;
 template <> struct Stored<float> {
   typedef float Act;
@@ -36,8 +37,11 @@ template <> struct Stored<Q4> {
                        CW = 16, NS = 2;
   static __host__ __device__ __forceinline__ int row(int K) { return K / 2; }
 };
+template <> struct Stored<Q4Few> : Stored<Q4> {};
 template <typename WT> constexpr bool kBf16Tokens = sizeof(typename Stored<WT>::Act) == 2;
 template <typename WT> constexpr bool kQ4 = Stored<WT>::BLOCK == 128;
+template <typename WT> constexpr bool kFew = false;
+template <> constexpr bool kFew<Q4Few> = true;
 template <typename WT> constexpr int kCThreads = Stored<WT>::CW * 32;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) & ~15; }
@@ -50,7 +54,7 @@ __host__ __device__ inline int row_pitch(int K) {
   return kBf16Tokens<WT> ? (K * 2 + B - 1) / B * B + 64 : K * 4;
 }
 template <typename WT>
-__host__ __device__ constexpr int most_tokens() { return kBf16Tokens<WT> ? 16 : 4; }
+__host__ __device__ constexpr int most_tokens() { return kBf16Tokens<WT> && !kFew<WT> ? 16 : 4; }
 // Floats of one warp's partial results: rows by tokens (16 x 8 or 16, or 16 x 4).
 template <typename WT>
 __host__ __device__ inline int part_floats(int tt) { return !kBf16Tokens<WT> ? 64 : tt > 8 ? 256 : 128; }
@@ -304,39 +308,45 @@ __device__ __forceinline__ void emit(const DecodeArgs& a, const Tile& tl, int bl
 // block take 4 of every lane's 8 values, weights and tokens alike, so that each
 // operand is one 16-byte read; the sum over K does not care for the order.  A
 // column of the result depends on its own token only, so absent tokens repeat
-// the last one's row.
+// the last one's row.  FEW: of up to four tokens' hidden activations, the first parts are
+// columns 0 to 3 of the one tile and the second parts columns 4 to 7.
 template <typename WT, bool UP> struct Products;
-template <bool UP, bool Q4W> struct MmaProducts {
+template <bool UP, bool Q4W, bool FEW> struct MmaProducts {
   uint32_t at0, at1;           // the lane's token rows of the two token tiles
   int plane, n;
   // token tiles of 8 by chains of dependent products: the two steps of a block,
   // and for hidden activations their two parts
-  static constexpr int CH = UP ? 2 : 4;
-  float acc[2][CH][4];
+  static constexpr int T8 = FEW ? 1 : 2, CH = UP || FEW ? 2 : 4;
+  float acc[T8][CH][4];
   // A sum over the first parts that is not finite is the result: the second
   // parts, zeros or of the other sign, would make a NaN of an infinite weight's
   // or an overflowing product's infinity, and they overflow only where it does.
   __device__ __forceinline__ float total(int t8, int c) const {
     const float first = acc[t8][0][c] + acc[t8][1][c];
-    const float sum = UP || !isfinite(first) ? first : first + (acc[t8][CH - 2][c] + acc[t8][CH - 1][c]);
+    const float second = UP ? 0.f : FEW ? __shfl_xor_sync(0xffffffffu, first, 2)
+                                        : acc[t8][CH - 2][c] + acc[t8][CH - 1][c];
+    const float sum = UP || !isfinite(first) ? first : first + second;
     return Q4W ? Q4_UNSCALE * sum : sum;
   }
   __device__ __forceinline__ void begin(const Part&, const char* rows, int pitch, int tokens, int lane) {
     const uint32_t at = smem_addr(rows) + (lane & 3) * 16;
     n = tokens;
     plane = n * pitch;
-    at0 = at + min(lane >> 2, n - 1) * pitch;
+    at0 = at + min(FEW && !UP ? lane >> 2 & 3 : lane >> 2, n - 1) * pitch +
+          (FEW && !UP && lane >= 16 ? plane : 0);
     at1 = at + min(8 + (lane >> 2), n - 1) * pitch;
 #pragma unroll
-    for (int h = 0; h < CH; ++h)
+    for (int t = 0; t < T8; ++t)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[0][h][c] = acc[1][h][c] = 0.f;
+      for (int h = 0; h < CH; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[t][h][c] = 0.f;
   }
   // out(row, token, value of row, value of row + 8) for this warp's own item
   template <typename Out>
   __device__ __forceinline__ void each(int lane, const Out& out) const {
 #pragma unroll
-    for (int t8 = 0; t8 < 2; ++t8)
+    for (int t8 = 0; t8 < T8; ++t8)
       if (t8 == 0 || n > 8)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -344,7 +354,7 @@ template <bool UP, bool Q4W> struct MmaProducts {
   }
   __device__ __forceinline__ void store(float* buf, int lane) const {
 #pragma unroll
-    for (int t8 = 0; t8 < 2; ++t8)
+    for (int t8 = 0; t8 < T8; ++t8)
       if (t8 == 0 || n > 8)
         *reinterpret_cast<float4*>(buf + t8 * 128 + lane * 4) =
             make_float4(total(t8, 0), total(t8, 1), total(t8, 2), total(t8, 3));
@@ -365,7 +375,7 @@ template <bool UP, bool Q4W> struct MmaProducts {
     }
   }
 };
-template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false> {
+template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false, false> {
   static constexpr int PIECE = Stored<bf16>::PIECE;
   __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
     const int g = lane >> 2, blocks = min(PIECE / 64, (left + 31) / 32);
@@ -389,21 +399,21 @@ template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false> {
     }
   }
 };
-// Products<Q4>: a lane reads 32 inputs' codes of its two rows at once, in which the
+// 4-bit weights: a lane reads 32 inputs' codes of its two rows at once, in which the
 // scale does not change, and multiplies word by word.  The four lanes of a row take
 // 128 inputs in turn, lane c words 4 c to 4 c + 3.
-template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
+template <bool UP, bool FEW> struct Q4Products : MmaProducts<UP, true, FEW> {
   static constexpr int PIECE = Stored<Q4>::PIECE;
   static_assert(PIECE == 256, "four blocks of 128 inputs");
   uint32_t code_at, scale_at, scale_step;      // the lane's, in a stage; from one block to the next
   __device__ __forceinline__ void begin(const Part& p, const char* rows, int pitch, int tokens, int lane) {
-    MmaProducts<UP, true>::begin(p, rows, pitch, tokens, lane);
+    MmaProducts<UP, true, FEW>::begin(p, rows, pitch, tokens, lane);
     const int g = lane >> 2, c = lane & 3;
     code_at = g * PIECE + ((c * 16) ^ ((g & 1) << 6));
     scale_at = 16 * PIECE + g * 2 + (c * 32 >> p.log_g) * 32;
     scale_step = 128 * 32 >> p.log_g;
   }
-  template <bool FAST, int T8>
+  template <bool FAST, int TT>
   __device__ __forceinline__ void block(uint32_t codes, uint32_t scales, const uint32_t (&x)[2]) {
     const uint4 w0 = load_rows(codes), w1 = load_rows(codes + 8 * PIECE);
     uint4 r[2][4];
@@ -412,23 +422,23 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
     for (int j = 0; j < 4; ++j) {
       const uint4 a = r[0][j], b = r[1][j];
 #pragma unroll
-      for (int t = 0; t < T8; ++t)
+      for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int h = 0; h < (UP ? 1 : 2); ++h) {
+        for (int h = 0; h < (UP || FEW ? 1 : 2); ++h) {
           const uint4 v = load_rows(x[t] + (h ? this->plane : 0) + j * 64);
           mma16816(this->acc[t][2 * h], a.x, b.x, a.y, b.y, v.x, v.y);
           mma16816(this->acc[t][2 * h + 1], a.z, b.z, a.w, b.w, v.z, v.w);
         }
     }
   }
-  template <bool FAST, int T8>
+  template <bool FAST, int TT>
   __device__ __forceinline__ void blocks(uint32_t from, int v0, int end) {
     uint32_t x[2] = {this->at0 + v0 * 2, this->at1 + v0 * 2};
     uint32_t scales = from + scale_at;
     const uint32_t codes = from + code_at;       // (a stage starts at a multiple of 256 bytes)
 #pragma unroll 1
     for (int u = 0; u < end; u += 64) {
-      block<FAST, T8>(codes ^ u, scales, x);
+      block<FAST, TT>(codes ^ u, scales, x);
       scales += scale_step;
       x[0] += 256;
       x[1] += 256;
@@ -443,13 +453,15 @@ template <bool UP> struct Products<Q4, UP> : MmaProducts<UP, true> {
       ok &= q4_fast(s.x) & q4_fast(s.y) & q4_fast(s.z) & q4_fast(s.w);
     }
     if (__all_sync(0xffffffffu, ok == 0x80008000u)) {
-      if (this->n > 8) blocks<true, 2>(from, v0, end);
+      if (!FEW && this->n > 8) blocks<true, FEW ? 1 : 2>(from, v0, end);
       else blocks<true, 1>(from, v0, end);
     } else {
-      blocks<false, 2>(from, v0, end);
+      blocks<false, FEW ? 1 : 2>(from, v0, end);
     }
   }
 };
+template <bool UP> struct Products<Q4, UP> : Q4Products<UP, false> {};
+template <bool UP> struct Products<Q4Few, UP> : Q4Products<UP, true> {};
 // Products<float>: a lane multiplies 4 values of each row with 4 of each token.
 template <bool UP> struct Products<float, UP> {
   uint32_t at;
