@@ -42,19 +42,22 @@ FFMA_PER_SM_PER_CLK = 128
 # DRAM bytes of the expert GEMM family per training step of the large layer,
 # from an ncu capture (dram__bytes_read.sum + dram__bytes_write.sum) of the
 # same per-expert shapes at 8 experts, scaled by 16.  Valid only for the GEMM
-# source it was taken from: reported as null once gemm_tc.cu changes.
-GEMM_TRAFFIC = {"bytes_per_step": 107.4e9, "workload": "large",
-                "gemm_source_sha256_prefix": "f575d8870daa70d5", "gradients_stored": False}
+# source it was taken from: reported as null once one of its files changes.
+GEMM_SOURCE = ("gemm_tc.cu", "tc_ptx.cuh")
+GEMM_TRAFFIC = {"bytes_per_step": 107.3e9, "workload": "large",
+                "gemm_source_sha256_prefix": "93971f2313de58a2", "gradients_stored": False}
 
 
 def gemm_traffic(wl: W.Workload, store_grads: bool = False):
     import hashlib
-    src = os.path.join(ROOT, "sparse_mixture_experts_softmax_gb300", "csrc", "gemm_tc.cu")
+    sha = hashlib.sha256()
     try:
-        with open(src, "rb") as f:
-            sha = hashlib.sha256(f.read()).hexdigest()
+        for name in GEMM_SOURCE:
+            with open(os.path.join(ROOT, "sparse_mixture_experts_softmax_gb300", "csrc", name), "rb") as f:
+                sha.update(f.read())
     except OSError:
         return None
+    sha = sha.hexdigest()
     if wl.name != GEMM_TRAFFIC["workload"] or not sha.startswith(GEMM_TRAFFIC["gemm_source_sha256_prefix"]):
         return None
     if store_grads != GEMM_TRAFFIC["gradients_stored"]:
