@@ -5,6 +5,11 @@
 // outputs: a lane eight inputs of each, which are one word of codes, so that every
 // access of the warp is a run of whole sectors; the scales of the eight outputs, next
 // to one another in memory, are one 16-byte access of a group's first lane.
+//
+// Measured, of a copy's 6.79 TB/s: 2^30 bf16 weights to 4 bits 497 us, 5.4 TB/s (beside
+// HBM the instructions for a code count: with a division and a comparison it was 1.00
+// ms); 2^29 fp32 weights 359 us, 6.8; back to bf16 (2^30) 397 us, 6.8; back to fp32 (2^29) 520 us,
+// 4.7 (a lane's two 16-byte stores are 32 bytes apart from the next lane's).
 #include "kernels.h"
 #include "q4.cuh"
 #include "q4.h"

@@ -131,9 +131,13 @@ cudaError_t launch_q4_rows(const Q4Product& p, int tt, cudaStream_t st) {
       return err;
     sms.store(n, std::memory_order_relaxed);
   }
-  // a block an SM, or fewer where each would have less than 8 KB of weights
-  const long long experts = p.E < p.R ? p.E : p.R;
-  const long long blocks = (experts * p.N * (p.K / 2) * (p.act == 2 ? 2 : 1) + 8191) / 8192;
+  // a block an SM, or fewer where each would have less than 8 KB of weights and less than
+  // eight items (1000 rows of 64 x 32, 1 KB of weights: 83 us on one block, 12 on the 32
+  // that the items ask for; 333 rows of 1000 x 480 21 on 30 blocks, 13 on all)
+  const long long experts = p.E < p.R ? p.E : p.R, mats = p.act == 2 ? 2 : 1;
+  const long long by_bytes = (experts * p.N * (p.K / 2) * mats + 8191) / 8192;
+  const long long by_items = ((experts + p.R / tt) * p.N * mats + 127) / 128;
+  const long long blocks = by_bytes > by_items ? by_bytes : by_items;
   return launch_pdl(q4_rows_kernel, dim3((unsigned)(blocks < n ? blocks : n)), dim3(THREADS), SMEM_MAX,
                     st, p, tt);
 }
@@ -143,10 +147,19 @@ cudaError_t launch_q4_rows(const Q4Product& p, int tt, cudaStream_t st) {
 cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st) {
   const int tt = p.R <= MAX_ROWS && !p.stall ? tile_rows(p) : 0;
   if (tt == 0) return launch_q4_gemm(p, st);
-  // Every row tile reads its expert's matrix again, most of it from L2
+  // Every row tile reads its expert's matrix again, most of it from L2, and widens it
+  // again; the other kernel does so once for up to 160 rows, but its tiles of 128 outputs
+  // leave SMs without work where there are few.  So the few-row kernel is taken where
+  // experts have three quarters of a tile's rows or less in the mean, or where all its
+  // tiles' weights are 24 MB or less.  Measured, few and many (us, with 8 for the events
+  // around a call): 128 experts of 4096 inputs and 2 x 2048 outputs, 1, 4, 8 and 16 rows an
+  // expert 203, 214, 399, 590 and 267, 270, 271, 274; 16 of 2048 inputs and 2 x 2048 outputs, 8
+  // and 16 rows 29, 50 and 36, 36; one matrix of 4096 x 4096, 16, 64 and 128 rows 15, 25, 42 and
+  // 22, 23, 25; 2048 x 2048, 128 and 192 rows 19, 22 and 19, 19; 1024 x 1024, 256 and 512 rows
+  // 15, 17 and 17, 17; 1000 x 480, 333 and 1000 rows 13, 17 and 17, 17.
   const long long tiles = (p.E < p.R ? p.E : p.R) + p.R / tt;
   const long long bytes = tiles * p.N * (p.K / 2) * (p.act == 2 ? 2 : 1);
-  const bool few = 4ll * p.R <= 3ll * tt * p.E || bytes <= (32ll << 20);
+  const bool few = 4ll * p.R <= 3ll * tt * p.E || bytes <= (24ll << 20);
   if (!few || tiles * ((p.N + 7) / 8) > INT_MAX) return launch_q4_gemm(p, st);
   return launch_q4_rows(p, tt, st);
 }
