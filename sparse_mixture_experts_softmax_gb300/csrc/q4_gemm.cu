@@ -23,17 +23,20 @@
 //
 // What bounds it: the matrix instructions (their pipe is 74 to 77 % busy at 160-row tiles,
 // the rest being a tile's beginning and end and waits for the widening warps), and with few
-// rows an expert the widening, which a tile does once for all its rows.  Measured, 128
-// experts, 4096 inputs, 2 x 2048 outputs with SwiGLU: 256 rows an expert 0.70 ms, 1.56
-// PFLOP/s; 32768 rows dealt unevenly, as a router does, 0.80 ms; 16 rows an expert 274 us,
-// 4.1 TB/s of codes, scales and rows.  Without SwiGLU, 2048 inputs and 4096 outputs: 0.39
-// ms, 1.42 PFLOP/s.  One matrix of 4096 x 4096 and 65536 rows: 1.88 PFLOP/s.
+// rows an expert the chain of a stage: widening, the issue of its products (some 27 clocks
+// each) and the wait for their end.  Measured, 128 experts, 4096 inputs, 2 x 2048 outputs
+// with SwiGLU: 256 rows an expert 0.69 ms, 1.60 PFLOP/s; 32768 rows dealt unevenly, as a
+// router does, 0.79 ms; 16 rows an expert 271 us, 4.2 TB/s of codes, scales and rows.
+// Without SwiGLU, 2048 inputs and 4096 outputs: 0.39 ms, 1.42 PFLOP/s.  One matrix of
+// 4096 x 4096 and 65536 rows: 1.15 ms, 1.91 PFLOP/s.
 //
 // Left behind (the 32768 rows dealt unevenly): widened weights in shared memory as the A
 // operand, which take its rate from the rows, 1.19 ms; then 64 inputs a stage and one store
-// an output and row in the epilogue, 0.86.  Tiles of 192 rows leave tensor memory for two
-// stages of widened weights only; without them 161 to 192 rows of an expert are two tiles of
-// 96 (192 rows an expert: 0.72 ms where 160 rows take 0.50).
+// an output and row in the epilogue, 0.86.  Three stages of rows in place of four: 256 rows
+// an expert 0.79 ms, whatever the stages of codes.  Prefetches of the rows into L2 by the
+// warp that copies them 0.73 (its own instructions count).  Tiles of 192 rows leave tensor
+// memory for two stages of widened weights only; without them 161 to 192 rows of an expert are
+// two tiles of 96 (192 rows an expert: 0.63 ms where 160 rows take 0.42).
 #include "q4.cuh"
 #include "q4.h"
 #include "tc_ptx.cuh"
@@ -61,16 +64,20 @@ constexpr long long LIMIT_NS = 2000000000ll;             // bound of every wait
 // Rows of a tile at most, and stages, each of 128 inputs: Q of codes and scales, SA of
 // widened weights, SX of rows.  The accumulators take 2 BN of the 512 columns, a stage of
 // weights 64.  The groups of widening warps run apart from one another, and copies do
-// not land in the order of their issue: a group may only wait on stages whose every use
-// is its own (a barrier tells no more than the parity of its phase), so Q and SA are
-// multiples of the groups.  Of a tile's last stage, where it has 64 inputs or less, the
-// second half is without work.
+// not land in the order of their issue: of copies a group may only wait on stages whose
+// every use is its own (a barrier tells no more than the parity of its phase), so Q is a
+// multiple of the groups.  SA is their number, a stage of widened weights each.  The
+// products of a stage, whose end frees both its weights and its rows, end in order and are
+// told by one barrier (a second one for the weights: 1 to 3 % slower calls): a group waits
+// for those of its last stage, and the next ones of that barrier need this group's weights
+// first.  Of a tile's last stage, where it has 64 inputs or less, the second half is without
+// work.
 constexpr int BN = 160, Q = 6, SA = 3, SX = 4;
 static_assert(box_of(BN) == X_BOXES - 1 && box_rows(X_BOXES - 1) == BN, "heights");
 constexpr int NG = 3, N_WIDEN = 4 * NG, THREADS = 32 * (W_WIDEN + N_WIDEN);
 constexpr int X_HALF = BN * BK * 2, X_STAGE = 2 * X_HALF;
 constexpr int SMEM = SX * X_STAGE + Q * RAW_BYTES;
-static_assert(2 * BN + SA * 64 <= TMEM_COLS && SA % NG == 0 && Q % NG == 0, "stages");
+static_assert(2 * BN + SA * 64 <= TMEM_COLS && SA == NG && Q % NG == 0 && NG <= SX, "stages");
 static_assert(SMEM + 5120 <= 232448, "shared memory of one block");
 
 struct Params {
@@ -207,8 +214,8 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
                const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_w3,
                const __grid_constant__ CUtensorMap tm_s3, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t raw_full[Q], raw_empty[Q], a_full[SA], a_empty[SA];
-  __shared__ __align__(8) uint64_t x_full[SX], x_empty[SX];
+  __shared__ __align__(8) uint64_t raw_full[Q], raw_empty[Q], a_full[SA];
+  __shared__ __align__(8) uint64_t x_full[SX], done[SX];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_mb;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -221,13 +228,10 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
       mbar_init(smem_u32(&raw_full[i]), 1);
       mbar_init(smem_u32(&raw_empty[i]), 4);      // (a group's warps)
     }
-    for (int i = 0; i < SA; ++i) {
-      mbar_init(smem_u32(&a_full[i]), 4);
-      mbar_init(smem_u32(&a_empty[i]), 1);
-    }
+    for (int i = 0; i < SA; ++i) mbar_init(smem_u32(&a_full[i]), 4);
     for (int i = 0; i < SX; ++i) {
       mbar_init(smem_u32(&x_full[i]), 1);
-      mbar_init(smem_u32(&x_empty[i]), 1);
+      mbar_init(smem_u32(&done[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&acc_full[i]), 1);
@@ -298,7 +302,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
       const uint32_t bytes = box_rows(box) * (BK * 2);
       const CUtensorMap* map = &tm_x.box[box];
       for (int j = 0; j < nraw; ++j) {
-        if (!all_wait(smem_u32(&x_empty[s]), ph ^ 1u)) { ok = false; break; }
+        if (!all_wait(smem_u32(&done[s]), ph ^ 1u)) { ok = false; break; }
         if (issuer) {
           const uint32_t bar = smem_u32(&x_full[s]), to = sbase + s * X_STAGE;
           const bool two = 2 * j + 1 < nkb;              // 64 inputs each
@@ -348,8 +352,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
               for (int kk = 0; kk < BK / UK; ++kk)
                 mma_ta(d, a + k * 32 + kk * 8, (uint64_t)hi << 32 | (b + k * (X_HALF >> 4) + kk * 2), idesc,
                        (j > 0 || k > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&a_empty[sa]));
-          mma_commit(smem_u32(&x_empty[sx]));
+          mma_commit(smem_u32(&done[sx]));
         }
         any = true;
         if (++sa == SA) { sa = 0; pa ^= 1u; }
@@ -384,8 +387,9 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     const uint32_t to0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * BN;
     const int mine = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     const long long raws = (long long)mine * nraw;
-    int q = group, s = group, j = group;         // (j: stage of a tile) every NG-th is the group's
-    uint32_t qph = 0, ph = 1;
+    int q = group, j = group, last = group;      // (j: stage of a tile) every NG-th is the group's
+    uint32_t qph = 0, ph = 0;
+    const uint32_t to = to0 + group * 64;
     for (long long i = group; i < raws; i += NG) {
       if (!all_wait(smem_u32(&raw_full[q]), qph)) break;
       uint4 c4[4];
@@ -415,15 +419,17 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
         q4_runs<false>(c4[0], c4[1], sc[0], sc[1], w[0]);
         q4_runs<false>(c4[2], c4[3], sc[2], sc[3], w[1]);
       }
-      if (!all_wait(smem_u32(&a_empty[s]), ph)) break;
+      if (i >= NG) {                   // the products of its last stage
+        if (!all_wait(smem_u32(&done[last]), ph)) break;
+        last += NG;
+        if (last >= SX) { last -= SX; ph ^= 1u; }
+      }
       tc_fence_after();
-      tmem_st32(to0 + s * 64, w[0]);
-      tmem_st32(to0 + s * 64 + 32, w[1]);
+      tmem_st32(to, w[0]);
+      tmem_st32(to + 32, w[1]);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
-      s += NG;
-      if (s >= SA) { s -= SA; ph ^= 1u; }
+      if (lane == 0) mbar_arrive(smem_u32(&a_full[group]));
     }
   } else {
     const int quarter = warp & 3;            // of the accumulator's lanes that this warp may read
