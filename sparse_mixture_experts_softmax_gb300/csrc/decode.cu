@@ -44,6 +44,16 @@
 // them 1.21 ms; one ring of bulk copies for the block, its K split over 16 warps,
 // 1.60 to 1.99 ms (a bulk copy takes its thread some 0.1 us to issue, and the
 // block waits for the slowest warp of every stage).
+//
+// 4-bit layers widen each weight to bf16 in front of the same products, which then counts
+// more than HBM: all sixteen warps multiply, each with stages of 256 bytes (512 inputs) of
+// 16 rows, and up to four tokens have a kernel of their own (Q4Few).  Measured, the large
+// layer: 64 tokens (1.6 GB of weights) 390 us, 4.6 TB/s; one token (105 MB) 41 us, of which
+// 7 go to the logits and the selection, 4 to barriers and the last pass.  Left behind: eight
+// warps 61 and 599 us; stages of 128 bytes 64 tokens 519 (the instructions to copy a stage
+// are the same as for 256); the four-token form chosen for every tile within one kernel 43
+// and 400 (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45
+// and 392 then; a stage's loop unrolled four times the same times and 30 KB more code.
 #include "decode_experts.cuh"
 
 namespace moe {
@@ -186,6 +196,8 @@ cudaError_t launch_decode_init(int* ctl, cudaStream_t st) {
 }
 
 cudaError_t launch_decode(int kind, const DecodeArgs& a, cudaStream_t st) {
+  // (four tokens and 4-bit weights: the large layer of one token 41 us by Q4Few's kernel and
+  // 45 by Q4's)
   if (kind == DECODE_Q4) return a.T <= most_tokens<Q4Few>() ? launch_t<Q4Few>(a, st) : launch_t<Q4>(a, st);
   return kind == DECODE_BF16 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
 }
