@@ -104,6 +104,64 @@ def test_decode_every_code_and_eight_bit_scales():
     _check(wl, inp, d, d.decode(device_x(wl, inp)))
 
 
+@pytest.mark.parametrize("T", [3, 4])
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_decode_up_to_four_tokens(name, T):
+    test_decode(name, T)
+
+
+@pytest.mark.parametrize("T,kw", [(4, dict(D=32, F=8192, E=8, k=8)), (4, dict(D=16384, F=32, E=8, k=8)),
+                                  (4, dict(D=4096, F=1024, E=8, k=4, n_shared=2)),
+                                  (2, dict(D=32, F=32, E=256, k=32)), (4, dict(D=4096, F=4096, E=8, k=2))])
+def test_decode_up_to_four_tokens_sizes(T, kw):
+    wl = _wl(T=T, **kw)
+    inp, ms = _quantized(wl, 5, 32)
+    d = MoEDecoder(**_args(wl, inp, ms), max_tokens=T)
+    _check(wl, inp, d, d.decode(device_x(wl, inp)))
+
+
+@pytest.mark.parametrize("T", [1, 4, 7, 12])
+@pytest.mark.parametrize("up,down", [(2.0 ** 20, 2.0 ** -24), (2.0 ** -40, 2.0 ** 44), (2.0 ** -100, 2.0 ** 100)])
+def test_decode_scales_of_any_size(T, up, down):
+    """Scales of both projections on either side of what the kernel widens the short way;
+    ReLU keeps the layer's scale."""
+    from tests import q4_cases as C
+    wl = _wl(T=T, D=320, F=160, E=8, k=2, act="relu")
+    inp = _inputs(wl, 1)
+    rng, ms = np.random.default_rng(2), {}
+    for n, times in (("w1", up), ("w2", down)):
+        E, N, K = inp[n].shape
+        codes, scales = C.random_matrix(rng, E, N, K, 64, five_bits=False)
+        scales = C.bf16(scales * times)
+        ms[n] = C.device_matrix(codes, scales, 64)
+        v = torch.from_numpy(C.weights(codes, scales, 64)).float()
+        inp[n], inp[n + "_bf16"] = v, v.bfloat16()
+    d = MoEDecoder(**_args(wl, inp, ms), max_tokens=wl.T)
+    _check(wl, inp, d, d.decode(device_x(wl, inp)))
+
+
+@pytest.mark.parametrize("T", [1, 4, 6, 20])
+def test_decode_infinite_scale(T):
+    """An infinite and a NaN scale of the down projection stay in their outputs."""
+    wl = _wl(T=T, D=96, F=160, E=8, k=8)
+    inp, ms = _quantized(wl, 3, 32)
+    m = ms["w2"]
+    m.codes[m.codes == 0x88] = 0x99              # no weight of zero in either place of a byte
+    codes = m.codes.cpu().numpy()
+    codes[(codes & 15) == 8] += 1
+    codes[(codes >> 4) == 8] += 16
+    m.codes.copy_(torch.from_numpy(codes))
+    d = MoEDecoder(**_args(wl, inp, ms), max_tokens=T)
+    x = device_x(wl, inp)
+    want = d.decode(x).clone()
+    m.scales[:, 2, 5] = float("inf")
+    m.scales[:, 4, 70] = float("nan")
+    got = d.decode(x)
+    rest = [i for i in range(96) if i not in (5, 70)]
+    assert torch.equal(got[:, rest], want[:, rest]) and bool(want.isfinite().all())
+    assert not bool(got[:, 5].isfinite().any()) and bool(got[:, 70].isnan().all())
+
+
 def _forward_want(wl, inp, layer, x, idx_from):
     """The oracle's y with the kernel's choice between nearly equal experts."""
     cfg = oracle_config(wl)
