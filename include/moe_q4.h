@@ -21,7 +21,8 @@
  * The conventions of moe.h hold: device pointers, 16-byte aligned, dense
  * row-major tensors, caller-owned memory, work enqueued on `stream`, arguments
  * checked on the host before the first launch, no floating-point atomics (the
- * same inputs give the same bits), no host synchronisation, no allocation.
+ * same inputs give the same bits), no host synchronisation, no allocation.  An
+ * output overlaps neither an input nor another output.
  */
 #ifndef MOE_Q4_GB300_H
 #define MOE_Q4_GB300_H
