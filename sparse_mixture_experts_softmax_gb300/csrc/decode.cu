@@ -47,13 +47,14 @@
 //
 // 4-bit layers widen each weight to bf16 in front of the same products, which then counts
 // more than HBM: all sixteen warps multiply, each with stages of 256 bytes (512 inputs) of
-// 16 rows, and up to four tokens have a kernel of their own (Q4Few).  Measured, the large
-// layer: 64 tokens (1.6 GB of weights) 390 us, 4.6 TB/s; one token (105 MB) 41 us, of which
-// 7 go to the logits and the selection, 4 to barriers and the last pass.  Left behind: eight
-// warps 61 and 599 us; stages of 128 bytes 64 tokens 519 (the instructions to copy a stage
-// are the same as for 256); the four-token form chosen for every tile within one kernel 43
-// and 400 (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45
-// and 392 then; a stage's loop unrolled four times the same times and 30 KB more code.
+// 16 rows, tiles are of up to 8 tokens, and calls of up to four tokens have a kernel of
+// their own (Q4Few).  Measured, the large layer: 64 tokens (1.6 GB of weights) 368 to 374
+// us, 4.8 TB/s; one token (105 MB) 41 us, of which 7 go to the logits and the selection and
+// 4 to barriers and the last pass.  Left behind: eight warps 61 and 599 us (one and 64
+// tokens); stages of 128 bytes 64 tokens 519 (the instructions to copy a stage are the same
+// as for 256); the four-token form chosen for every tile within one kernel 43 and 400
+// (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45 and 392
+// then; a stage's loop unrolled four times the same times and 30 KB more code.
 #include "decode_experts.cuh"
 
 namespace moe {
@@ -196,9 +197,13 @@ cudaError_t launch_decode_init(int* ctl, cudaStream_t st) {
 }
 
 cudaError_t launch_decode(int kind, const DecodeArgs& a, cudaStream_t st) {
-  // (four tokens and 4-bit weights: the large layer of one token 41 us by Q4Few's kernel and
-  // 45 by Q4's)
-  if (kind == DECODE_Q4) return a.T <= most_tokens<Q4Few>() ? launch_t<Q4Few>(a, st) : launch_t<Q4>(a, st);
+  // 4-bit weights, one token of the large layer: 41 us by Q4Few's kernel, 45 by tiles of up
+  // to 16 tokens.  More tokens, tiles of up to 16 and of up to 8 (us; registers for 16 spill, and
+  // a second tile's weights come from L2): the large layer, 64 tokens 389 and 374; 64 experts of
+  // 1024 and 704, k = 6, 16 and 64 tokens 38.5, 55.1 and 36.1, 45.0; 16 of 1024 and 1024, k = 4, 48
+  // tokens 42.1 and 35.1; 8 of 512 and 1024, k = 2, 5 and 64 tokens 18.5, 30.4 and 17.6, 26.6.
+  if (kind == DECODE_Q4)
+    return a.T <= most_tokens<Q4Few>() ? launch_t<Q4Few>(a, st) : launch_t<Q4Eight>(a, st);
   return kind == DECODE_BF16 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
 }
 

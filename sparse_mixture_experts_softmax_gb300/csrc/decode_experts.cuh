@@ -17,6 +17,7 @@ constexpr int WARPS = 16, THREADS = WARPS * 32;
 // The tokens' rows have zeros up to a multiple of BLOCK values, which is what a lane
 // group of the products takes at once.
 struct Q4 {};                                   // 4-bit weights (q4.cuh)
+struct Q4Eight {};                              // the same, in tiles of at most eight tokens
 struct Q4Few {};                                // the same, of a call of at most four tokens
 template <typename WT> struct Stored;
 template <> struct Stored<float> {
@@ -38,11 +39,10 @@ template <> struct Stored<Q4> {
                        CW = 16, NS = 2;
   static __host__ __device__ __forceinline__ int row(int K) { return K / 2; }
 };
+template <> struct Stored<Q4Eight> : Stored<Q4> {};
 template <> struct Stored<Q4Few> : Stored<Q4> {};
 template <typename WT> constexpr bool kBf16Tokens = sizeof(typename Stored<WT>::Act) == 2;
 template <typename WT> constexpr bool kQ4 = Stored<WT>::BLOCK == 128;
-template <typename WT> constexpr bool kFew = false;
-template <> constexpr bool kFew<Q4Few> = true;
 template <typename WT> constexpr int kCThreads = Stored<WT>::CW * 32;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) & ~15; }
@@ -55,7 +55,9 @@ __host__ __device__ inline int row_pitch(int K) {
   return kBf16Tokens<WT> ? (K * 2 + B - 1) / B * B + 64 : K * 4;
 }
 template <typename WT>
-__host__ __device__ constexpr int most_tokens() { return kBf16Tokens<WT> && !kFew<WT> ? 16 : 4; }
+__host__ __device__ constexpr int most_tokens() { return kBf16Tokens<WT> ? 16 : 4; }
+template <> __host__ __device__ constexpr int most_tokens<Q4Eight>() { return 8; }
+template <> __host__ __device__ constexpr int most_tokens<Q4Few>() { return 4; }
 // Floats of one warp's partial results: rows by tokens (16 x 8 or 16, or 16 x 4).
 template <typename WT>
 __host__ __device__ inline int part_floats(int tt) { return !kBf16Tokens<WT> ? 64 : tt > 8 ? 256 : 128; }
@@ -314,12 +316,13 @@ __device__ __forceinline__ void emit(const DecodeArgs& a, const Tile& tl, int bl
 // columns 0 to 3 of the one tile and the second parts columns 4 to 7: half the products and
 // reads (one token of the large layer 45 -> 41 us).
 template <typename WT, bool UP> struct Products;
-template <bool UP, bool Q4W, bool FEW> struct MmaProducts {
+template <bool UP, bool Q4W, int MOST> struct MmaProducts {
+  static constexpr bool FEW = MOST <= 4;
   uint32_t at0, at1;           // the lane's token rows of the two token tiles
   int plane, n;
   // token tiles of 8 by chains of dependent products: the two steps of a block,
   // and for hidden activations their two parts
-  static constexpr int T8 = FEW ? 1 : 2, CH = UP || FEW ? 2 : 4;
+  static constexpr int T8 = MOST > 8 ? 2 : 1, CH = UP || FEW ? 2 : 4;
   float acc[T8][CH][4];
   // A sum over the first parts that is not finite is the result: the second
   // parts, zeros or of the other sign, would make a NaN of an infinite weight's
@@ -378,7 +381,7 @@ template <bool UP, bool Q4W, bool FEW> struct MmaProducts {
     }
   }
 };
-template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false, false> {
+template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false, most_tokens<bf16>()> {
   static constexpr int PIECE = Stored<bf16>::PIECE;
   __device__ __forceinline__ void stage(uint32_t from, int v0, int left, int lane) {
     const int g = lane >> 2, blocks = min(PIECE / 64, (left + 31) / 32);
@@ -405,12 +408,14 @@ template <bool UP> struct Products<bf16, UP> : MmaProducts<UP, false, false> {
 // 4-bit weights: a lane reads 32 inputs' codes of its two rows at once, in which the
 // scale does not change, and multiplies word by word.  The four lanes of a row take
 // 128 inputs in turn, lane c words 4 c to 4 c + 3.
-template <bool UP, bool FEW> struct Q4Products : MmaProducts<UP, true, FEW> {
+template <bool UP, int MOST> struct Q4Products : MmaProducts<UP, true, MOST> {
+  static constexpr bool FEW = MOST <= 4;
+  static constexpr int T8 = MOST > 8 ? 2 : 1;
   static constexpr int PIECE = Stored<Q4>::PIECE;
   static_assert(PIECE == 256, "four blocks of 128 inputs");
   uint32_t code_at, scale_at, scale_step;      // the lane's, in a stage; from one block to the next
   __device__ __forceinline__ void begin(const Part& p, const char* rows, int pitch, int tokens, int lane) {
-    MmaProducts<UP, true, FEW>::begin(p, rows, pitch, tokens, lane);
+    MmaProducts<UP, true, MOST>::begin(p, rows, pitch, tokens, lane);
     const int g = lane >> 2, c = lane & 3;
     code_at = g * PIECE + ((c * 16) ^ ((g & 1) << 6));
     scale_at = 16 * PIECE + g * 2 + (c * 32 >> p.log_g) * 32;
@@ -456,15 +461,16 @@ template <bool UP, bool FEW> struct Q4Products : MmaProducts<UP, true, FEW> {
       ok &= q4_fast(s.x) & q4_fast(s.y) & q4_fast(s.z) & q4_fast(s.w);
     }
     if (__all_sync(0xffffffffu, ok == 0x80008000u)) {
-      if (!FEW && this->n > 8) blocks<true, FEW ? 1 : 2>(from, v0, end);
+      if (T8 > 1 && this->n > 8) blocks<true, T8>(from, v0, end);
       else blocks<true, 1>(from, v0, end);
     } else {
-      blocks<false, FEW ? 1 : 2>(from, v0, end);
+      blocks<false, T8>(from, v0, end);
     }
   }
 };
-template <bool UP> struct Products<Q4, UP> : Q4Products<UP, false> {};
-template <bool UP> struct Products<Q4Few, UP> : Q4Products<UP, true> {};
+template <bool UP> struct Products<Q4, UP> : Q4Products<UP, most_tokens<Q4>()> {};
+template <bool UP> struct Products<Q4Eight, UP> : Q4Products<UP, most_tokens<Q4Eight>()> {};
+template <bool UP> struct Products<Q4Few, UP> : Q4Products<UP, most_tokens<Q4Few>()> {};
 // Products<float>: a lane multiplies 4 values of each row with 4 of each token.
 template <bool UP> struct Products<float, UP> {
   uint32_t at;
