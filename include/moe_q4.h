@@ -101,7 +101,8 @@ typedef struct {
 } moe_q4_weights;
 
 /* moe_decode with those weights: the same arguments, limits, workspace
- * (moe_decode_workspace_size, moe_decode_init, moe_decode_status) and precision. */
+ * (moe_decode_workspace_size, moe_decode_init, moe_decode_status) and precision.  An
+ * expert's weights are read once for each tile of up to 8 of its tokens. */
 MOE_API moe_status moe_q4_decode(const moe_config* cfg, const moe_q4_weights* w, const void* x,
                                  void* y, int32_t* idx, float* gate, void* workspace,
                                  size_t workspace_bytes, void* stream);
