@@ -55,6 +55,7 @@
 // as for 256); the four-token form chosen for every tile within one kernel 43 and 400
 // (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45 and 392
 // then; a stage's loop unrolled four times the same times and 30 KB more code.
+#include "../../include/moe_block.h"
 #include "decode_experts.cuh"
 
 namespace moe {
@@ -173,12 +174,22 @@ int sm_count() {
   return v;
 }
 
+// A tile of one token has room whatever the entry points let through: the lists of the
+// most tokens, of 32 choices among 256 experts, beside the widest rows.
+template <typename WT>
+constexpr bool always_fits(int T) {
+  return row_bytes<WT>(MOE_DECODE_MAX_ROW_BYTES / (int)sizeof(typename Stored<WT>::Act), MOE_DECODE_MAX_F) <=
+         make_plan<WT>(T, 32, 256, MOE_DECODE_MAX_F, 1).rows_bytes;
+}
+static_assert(always_fits<float>(MOE_DECODE_MAX_TOKENS) && always_fits<bf16>(MOE_DECODE_MAX_TOKENS) &&
+              always_fits<Q4Wide>(MOE_DECODE_MAX_TOKENS) && always_fits<Q4Few>(most_tokens<Q4Few>()), "limits");
+
 template <typename WT>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
   const int sms = sm_count(), tt = tile_tokens<WT>(a);
   if (sms <= 0) return cudaErrorUnknown;
-  if (tt <= 0) return cudaErrorInvalidValue;    // (past the entry point's limits)
+  if (tt <= 0) return cudaErrorInvalidValue;    // (past the entry points' limits)
   // a block per SM, or fewer where each would have less than 8 KB of weights (the
   // kernel's time hardly goes with it: 4 KB, 16 KB and a block on every SM are
   // within 0.2 us of 13.4 at 96 KB of weights, of 13.6 at 390 KB, of 14.4 at
@@ -202,8 +213,10 @@ cudaError_t launch_decode(int kind, const DecodeArgs& a, cudaStream_t st) {
   // a second tile's weights come from L2): the large layer, 64 tokens 389 and 374; 64 experts of
   // 1024 and 704, k = 6, 16 and 64 tokens 38.5, 55.1 and 36.1, 45.0; 16 of 1024 and 1024, k = 4, 48
   // tokens 42.1 and 35.1; 8 of 512 and 1024, k = 2, 5 and 64 tokens 18.5, 30.4 and 17.6, 26.6.
-  if (kind == DECODE_Q4)
-    return a.T <= most_tokens<Q4Few>() ? launch_t<Q4Few>(a, st) : launch_t<Q4Eight>(a, st);
+  // Their buffers and the longest lists leave no room for the widest rows (of 64 tokens' 32
+  // choices among 256 experts, for rows of more than 18 KB): those calls go by half the warps.
+  if (kind == DECODE_Q4 && a.T <= most_tokens<Q4Few>()) return launch_t<Q4Few>(a, st);
+  if (kind == DECODE_Q4) return tile_tokens<Q4Eight>(a) > 0 ? launch_t<Q4Eight>(a, st) : launch_t<Q4Wide>(a, st);
   return kind == DECODE_BF16 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
 }
 

@@ -19,6 +19,7 @@ constexpr int WARPS = 16, THREADS = WARPS * 32;
 struct Q4 {};                                   // 4-bit weights (q4.cuh)
 struct Q4Eight {};                              // the same, in tiles of at most eight tokens
 struct Q4Few {};                                // the same, of a call of at most four tokens
+struct Q4Wide {};                               // the same, with room for wide rows
 template <typename WT> struct Stored;
 template <> struct Stored<float> {
   typedef float Act;
@@ -41,6 +42,11 @@ template <> struct Stored<Q4> {
 };
 template <> struct Stored<Q4Eight> : Stored<Q4> {};
 template <> struct Stored<Q4Few> : Stored<Q4> {};
+// Half the warps: 80 KB less of buffers and partial results, for calls whose lists leave
+// the other forms no room for a row.
+template <> struct Stored<Q4Wide> : Stored<Q4> {
+  static constexpr int CW = 8;
+};
 template <typename WT> constexpr bool kBf16Tokens = sizeof(typename Stored<WT>::Act) == 2;
 template <typename WT> constexpr bool kQ4 = Stored<WT>::BLOCK == 128;
 template <typename WT> constexpr int kCThreads = Stored<WT>::CW * 32;
@@ -50,7 +56,7 @@ __host__ __device__ constexpr int up16(int v) { return (v + 15) & ~15; }
 // that the two rows a quarter-warp reads fall on different banks, and room for
 // zeros up to a multiple of BLOCK values; fp32 rows are read along the row.
 template <typename WT>
-__host__ __device__ inline int row_pitch(int K) {
+__host__ __device__ constexpr int row_pitch(int K) {
   constexpr int B = Stored<WT>::BLOCK * 2 > 128 ? Stored<WT>::BLOCK * 2 : 128;
   return kBf16Tokens<WT> ? (K * 2 + B - 1) / B * B + 64 : K * 4;
 }
@@ -58,16 +64,17 @@ template <typename WT>
 __host__ __device__ constexpr int most_tokens() { return kBf16Tokens<WT> ? 16 : 4; }
 template <> __host__ __device__ constexpr int most_tokens<Q4Eight>() { return 8; }
 template <> __host__ __device__ constexpr int most_tokens<Q4Few>() { return 4; }
+template <> __host__ __device__ constexpr int most_tokens<Q4Wide>() { return 8; }
 // Floats of one warp's partial results: rows by tokens (16 x 8 or 16, or 16 x 4).
 template <typename WT>
-__host__ __device__ inline int part_floats(int tt) { return !kBf16Tokens<WT> ? 64 : tt > 8 ? 256 : 128; }
+__host__ __device__ constexpr int part_floats(int tt) { return !kBf16Tokens<WT> ? 64 : tt > 8 ? 256 : 128; }
 // Shared memory of a call with token tiles of tt, the same on host and device.
 struct Plan {
   int off_red, off_idx, off_gate, off_tok, off_slot, off_tile, off_at, off_rows, rows_bytes;
 };
 template <typename WT>
-__host__ __device__ inline Plan make_plan(int T, int k, int E, int Fs, int tt) {
-  Plan p;
+__host__ __device__ constexpr Plan make_plan(int T, int k, int E, int Fs, int tt) {
+  Plan p{};
   const int R = T * k;
   const int tiles = (E < R ? E : R) + R / tt + (Fs ? (T + tt - 1) / tt : 0);
   // (the router's and the selection's scratch lies there first)
@@ -83,14 +90,20 @@ __host__ __device__ inline Plan make_plan(int T, int k, int E, int Fs, int tt) {
   p.rows_bytes = SMEM_MAX - o;
   return p;
 }
-static_assert((768 + WARPS * 256) * 4 <= Stored<Q4>::CW * Stored<Q4>::NS * Stored<Q4>::STAGE, "scratch");
+static_assert((768 + WARPS * 256) * 4 <= Stored<Q4Wide>::CW * Stored<Q4Wide>::NS * Stored<Q4Wide>::STAGE,
+              "scratch");
+// Bytes of one token's widest row of an operand.
+template <typename WT>
+__host__ __device__ constexpr long long row_bytes(int D, int width) {
+  const long long up = row_pitch<WT>(D), down = (long long)row_pitch<WT>(width) * (kBf16Tokens<WT> ? 2 : 1);
+  return up > down ? up : down;
+}
 // Tokens of a tile: as many as there is room for one tile of, or 0.
 template <typename WT>
 int tile_tokens(const DecodeArgs& a) {
-  const long long up = row_pitch<WT>(a.D), width = a.F > a.Fs ? a.F : a.Fs;
-  const long long down = row_pitch<WT>((int)width) * (kBf16Tokens<WT> ? 2 : 1);
+  const long long row = row_bytes<WT>(a.D, a.F > a.Fs ? a.F : a.Fs);
   for (int tt = most_tokens<WT>(); tt >= 1; --tt)
-    if (tt * (up > down ? up : down) <= make_plan<WT>(a.T, a.k, a.E, a.Fs, tt).rows_bytes) return tt;
+    if (tt * row <= make_plan<WT>(a.T, a.k, a.E, a.Fs, tt).rows_bytes) return tt;
   return 0;
 }
 
@@ -471,6 +484,7 @@ template <bool UP, int MOST> struct Q4Products : MmaProducts<UP, true, MOST> {
 template <bool UP> struct Products<Q4, UP> : Q4Products<UP, most_tokens<Q4>()> {};
 template <bool UP> struct Products<Q4Eight, UP> : Q4Products<UP, most_tokens<Q4Eight>()> {};
 template <bool UP> struct Products<Q4Few, UP> : Q4Products<UP, most_tokens<Q4Few>()> {};
+template <bool UP> struct Products<Q4Wide, UP> : Q4Products<UP, most_tokens<Q4Wide>()> {};
 // Products<float>: a lane multiplies 4 values of each row with 4 of each token.
 template <bool UP> struct Products<float, UP> {
   uint32_t at;

@@ -268,3 +268,17 @@ def test_refused_calls():
             with pytest.raises(ValueError, match="captured"):
                 Q4Layer(**args, max_tokens=4)
             layer.workspace[:1].zero_()
+
+
+@pytest.mark.parametrize("group,kw", [
+    (64, dict(D=16384, F=32, E=256, k=32)), (32, dict(D=32, F=8192, E=256, k=32)),
+    (128, dict(D=64, F=4096, E=256, k=32, n_shared=2)), (64, dict(D=16384, F=32, E=32, k=25)),
+    (32, dict(D=32, F=8192, E=64, k=32, act="relu", has_bias=True)),
+])
+def test_decode_widest_rows_beside_the_longest_lists(group, kw):
+    """Every layer within the limits is served: rows of the greatest width beside the lists
+    of the most tokens."""
+    wl = _wl(T=64, **kw)
+    inp, ms = _quantized(wl, 9, group)
+    d = MoEDecoder(**_args(wl, inp, ms), max_tokens=wl.T)
+    _check(wl, inp, d, d.decode(device_x(wl, inp)))
