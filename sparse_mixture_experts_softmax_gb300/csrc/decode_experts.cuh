@@ -435,10 +435,10 @@ template <bool UP, int MOST> struct Q4Products : MmaProducts<UP, true, MOST> {
     scale_step = 128 * 32 >> p.log_g;
   }
   template <bool FAST, int TT>
-  __device__ __forceinline__ void block(uint32_t codes, uint32_t scales, const uint32_t (&x)[2]) {
+  __device__ __forceinline__ void block(uint32_t codes, uint32_t scales, const uint32_t (&x)[2], bool on) {
     const uint4 w0 = load_rows(codes), w1 = load_rows(codes + 8 * PIECE);
     uint4 r[2][4];
-    q4_runs<FAST>(w0, w1, load_scale(scales), load_scale(scales + 16), r);
+    q4_runs<FAST>(w0, w1, on ? load_scale(scales) : 0u, on ? load_scale(scales + 16) : 0u, r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint4 a = r[0][j], b = r[1][j];
@@ -452,14 +452,16 @@ template <bool UP, int MOST> struct Q4Products : MmaProducts<UP, true, MOST> {
         }
     }
   }
+  // Past a row's end lie codes of any value, which meet zeros of x.  Where their group's scale
+  // may be an infinity or a NaN (never the short way's) it is taken as a zero there.
   template <bool FAST, int TT>
-  __device__ __forceinline__ void blocks(uint32_t from, int v0, int end) {
+  __device__ __forceinline__ void blocks(uint32_t from, int v0, int end, int left, int lane) {
     uint32_t x[2] = {this->at0 + v0 * 2, this->at1 + v0 * 2};
     uint32_t scales = from + scale_at;
     const uint32_t codes = from + code_at;       // (a stage starts at a multiple of 256 bytes)
 #pragma unroll 1
     for (int u = 0; u < end; u += 64) {
-      block<FAST, TT>(codes ^ u, scales, x);
+      block<FAST, TT>(codes ^ u, scales, x, FAST || u * 2 + (lane & 3) * 32 < left);
       scales += scale_step;
       x[0] += 256;
       x[1] += 256;
@@ -474,10 +476,10 @@ template <bool UP, int MOST> struct Q4Products : MmaProducts<UP, true, MOST> {
       ok &= q4_fast(s.x) & q4_fast(s.y) & q4_fast(s.z) & q4_fast(s.w);
     }
     if (__all_sync(0xffffffffu, ok == 0x80008000u)) {
-      if (T8 > 1 && this->n > 8) blocks<true, T8>(from, v0, end);
-      else blocks<true, 1>(from, v0, end);
+      if (T8 > 1 && this->n > 8) blocks<true, T8>(from, v0, end, left, lane);
+      else blocks<true, 1>(from, v0, end, left, lane);
     } else {
-      blocks<false, T8>(from, v0, end);
+      blocks<false, T8>(from, v0, end, left, lane);
     }
   }
 };
@@ -653,7 +655,7 @@ __device__ __forceinline__ void compute(const Job& job, const Part& p, const Til
       if constexpr (kQ4<WT>) {
         // two rows at a time, then the scales: lane 2 g + h has group g's of half h.
         // What lies in the place of codes past the row's end are codes, which meet
-        // zeros of x; their scales are zeros.
+        // zeros of x; the scales of groups past it are zeros.
         const bool on = q4_left > 0;
         const uint32_t slot_at = put_slot * STAGE;
         copy16_rows(q4_to + slot_at, lp, 2 * row, on);

@@ -357,3 +357,26 @@ def test_streams_and_graphs(counts):
         graph.replay()
         assert torch.equal(out, p.forward(buf, off))
     assert p.status() == 0
+
+
+@pytest.mark.parametrize("counts", [[1, 2], [3, 4], [20, 50], [200, 4000]])
+@pytest.mark.parametrize("K,group", [(160, 64), (160, 128), (544, 128), (96, 64)])
+def test_infinite_scale_of_a_short_group(counts, K, group):
+    """An infinite scale of a group that ends with its inputs gives the infinity of its sum:
+    positive rows and weights.  The other outputs do not see it."""
+    c = _product_case(19, counts, 72, K, group, "none", False)
+    last = K // group
+    codes, scales = c["m"][0].copy(), c["m"][1].copy()
+    codes[:, 5, last * group:] = np.maximum(codes[:, 5, last * group:], 9)
+    c["x"] = np.abs(c["x"]) + 2.0 ** -8
+    c["x"] = C.bf16(c["x"])
+    c["m"] = codes, scales
+    p, x, off = _device(c)
+    want = p.forward(x, off)
+    _check(c, want)
+    scales = scales.copy()
+    scales[:, last, 5] = np.inf
+    got = Q4Product(C.device_matrix(codes, scales, group)).forward(x, off)
+    rest = [i for i in range(72) if i != 5]
+    assert torch.equal(got[:, rest], want[:, rest])
+    assert bool((got[:, 5] == float("inf")).all())

@@ -282,3 +282,25 @@ def test_decode_widest_rows_beside_the_longest_lists(group, kw):
     inp, ms = _quantized(wl, 9, group)
     d = MoEDecoder(**_args(wl, inp, ms), max_tokens=wl.T)
     _check(wl, inp, d, d.decode(device_x(wl, inp)))
+
+
+@pytest.mark.parametrize("group,F", [(64, 160), (128, 160), (128, 544)])
+@pytest.mark.parametrize("T", [1, 3, 6, 20])
+def test_decode_infinite_scale_of_a_short_group(T, group, F):
+    """An infinite scale of a group that ends with its inputs gives the infinity of its sum:
+    positive hidden activations and weights."""
+    wl = _wl(T=T, D=96, F=F, E=8, k=8, act="relu", has_bias=True)
+    inp, _ = _quantized(wl, 3, group)
+    inp["b1"] = inp["b1"].abs() + 50.0               # every hidden activation is positive
+    ms = {n: quantize(inp[n].cuda(), group) for n in ("w1", "w2")}
+    last = F // group
+    codes = ms["w2"].codes
+    codes[:, 5, last * group // 2:] = 0xee           # codes of 14
+    d = MoEDecoder(**_args(wl, inp, ms), max_tokens=T)
+    x = device_x(wl, inp)
+    want = d.decode(x).clone()
+    ms["w2"].scales[:, last, 5] = float("inf")
+    got = d.decode(x)
+    rest = [i for i in range(96) if i != 5]
+    assert torch.equal(got[:, rest], want[:, rest]) and bool(want.isfinite().all())
+    assert bool((got[:, 5] == float("inf")).all())
