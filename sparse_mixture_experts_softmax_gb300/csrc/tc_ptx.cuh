@@ -147,13 +147,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 // (8 significant bits), so the sigmoid uses the hardware's approximate
 // exponential and division (__expf, __fdividef: relative errors of a few fp32
 // ulps, far below the bf16 rounding that follows) and is evaluated once per
-// element; tanh is 2 sigmoid(2u) - 1.  The CUDA-core GEMMs of fp32 layers keep
-// the IEEE-accurate functions of common.cuh.
+// element; tanh u is 2 sigmoid(2u) - 1, and GELU, 0.5 h (1 + tanh u), is
+// h sigmoid(2u), which keeps its digits where tanh u is next to -1.  The
+// CUDA-core GEMMs of fp32 layers keep the IEEE-accurate functions of common.cuh.
 __device__ __forceinline__ float sigmoid_epi(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 __device__ __forceinline__ float gelu_epi(float h) {
   const float c = 0.7978845608028654f, a = 0.044715f;
-  const float t = 2.0f * sigmoid_epi(2.0f * c * (h + a * h * h * h)) - 1.0f;
-  return 0.5f * h * (1.0f + t);
+  return h * sigmoid_epi(2.0f * c * (h + a * h * h * h));
 }
 
 // ------------------------------------------------------------------- host --

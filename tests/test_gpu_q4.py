@@ -380,3 +380,24 @@ def test_infinite_scale_of_a_short_group(counts, K, group):
     rest = [i for i in range(72) if i != 5]
     assert torch.equal(got[:, rest], want[:, rest])
     assert bool((got[:, 5] == float("inf")).all())
+
+
+@pytest.mark.parametrize("rows", [40, 777, 5000])
+def test_product_gelu_of_negative_inputs(rows):
+    """GELU keeps its digits where it is small: one input of a row times a weight of one, so
+    that the pre-activation h is exact.  h sigmoid(2 u), u = c (h + a h^3): in fp32 the
+    roundings of 2 u, a few of 2^-24 of it (with the constants' own 2^-21), are an error of
+    25 2^-21 of the exponential where |2 u| is at most 25; the exponential and the division
+    add less than 2^-17; in all below 2^-15 of the result, which is rounded once to bf16."""
+    h = C.bf16(np.linspace(-6.0, 6.0, rows))
+    codes, scales = np.full((1, 8, 32), 8), np.ones((1, 1, 8))
+    codes[:, :, 0] = 9
+    x = np.zeros((rows, 32))
+    x[:, 0] = h
+    p = Q4Product(C.device_matrix(codes, scales, 32), act="gelu_tanh")
+    got = p.forward(torch.from_numpy(x).bfloat16().cuda(),
+                    torch.tensor([0, rows], dtype=torch.int32, device="cuda")).double().cpu().numpy()
+    u2 = 2 * np.sqrt(2 / np.pi) * (h + 0.044715 * h ** 3)
+    want = (h / (1 + np.exp(-u2)))[:, None]
+    assert (np.abs(got - want) <= (C.BF16_HALF + 2.0 ** -14) * np.abs(want)).all(), \
+        float((np.abs(got - want) / np.maximum(np.abs(want), 1e-30)).max())
