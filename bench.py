@@ -44,8 +44,8 @@ FFMA_PER_SM_PER_CLK = 128
 # same per-expert shapes at 8 experts, scaled by 16.  Valid only for the GEMM
 # source it was taken from: reported as null once one of its files changes.
 GEMM_SOURCE = ("gemm_tc.cu", "tc_ptx.cuh")
-GEMM_TRAFFIC = {"bytes_per_step": 107.3e9, "workload": "large",
-                "gemm_source_sha256_prefix": "93971f2313de58a2", "gradients_stored": False}
+GEMM_TRAFFIC = {"bytes_per_step": 106.8e9, "workload": "large",
+                "gemm_source_sha256_prefix": "281ffe947b5ea3d5", "gradients_stored": False}
 
 
 def gemm_traffic(wl: W.Workload, store_grads: bool = False):
