@@ -8,6 +8,7 @@ nothing itself.
 from __future__ import annotations
 
 import ctypes
+from typing import Callable, NamedTuple
 
 import torch
 
@@ -15,6 +16,77 @@ from . import binding as B
 from .q4 import Q4Matrix
 
 _DTYPE = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+class Weights(NamedTuple):
+    """The checked weights of a layer that serves, as the C ABI takes them."""
+    device: torch.device
+    dtype: torch.dtype        # the tokens' type
+    D: int
+    make: Callable            # the configuration for a number of tokens
+    hold: list                # keeps the storage alive, even if a parameter's is replaced
+    entry: str                # the few-token form's entry point
+    struct: ctypes.Structure
+
+
+def check_weights(w_gate, w1, w2, w3=None, b1=None, b2=None, k=1, act="relu", score="softmax",
+                  n_groups=1, topk_groups=1, group_score="top2_sum", logit_bias=None,
+                  corr_bias=None, n_shared=0, ws1=None, ws3=None, ws2=None,
+                  capacity_factor=0.0) -> Weights:
+    """The weights of a ``MoEDecoder`` (which describes them) or raises."""
+    q4 = isinstance(w1, Q4Matrix)
+    if not q4 and w1.dtype not in _DTYPE:
+        raise ValueError(f"w1 must be float32, bfloat16 or a Q4Matrix, got {w1.dtype}")
+    if len(w1.shape) != 3:
+        raise ValueError(f"w1 must be [E, F, D], got {tuple(w1.shape)}")
+    E, F, D = w1.shape
+    Fs = int(n_shared) * F
+    if (w3 is not None) != (act == "swiglu"):
+        raise ValueError("w3 goes with swiglu experts, and only with them")
+    if (b1 is None) != (b2 is None):
+        raise ValueError("b1 and b2 come together")
+    f32, dt = torch.float32, torch.bfloat16 if q4 else w1.dtype
+    one = (1,) if q4 else ()
+    want = dict(w_gate=(w_gate, f32, (E, D)), w1=(w1, dt, (E, F, D)), w2=(w2, dt, (E, D, F)),
+                w3=(w3, dt, (E, F, D)), b1=(b1, f32, (E, F)), b2=(b2, f32, (E, D)),
+                logit_bias=(logit_bias, f32, (E,)), corr_bias=(corr_bias, f32, (E,)),
+                ws1=(ws1, dt, one + (Fs, D)), ws3=(ws3, dt, one + (Fs, D)),
+                ws2=(ws2, dt, one + (D, Fs)))
+    matrices = {}
+    for name, (t, dtype, shape) in want.items():
+        if name.startswith("ws") and (t is not None) != (n_shared > 0):
+            raise ValueError("ws1, ws3 and ws2 go with n_shared > 0")
+        if t is None:
+            continue
+        if q4 and dtype is dt:
+            if not isinstance(t, Q4Matrix) or t.shape != shape or t.group != w1.group:
+                raise ValueError(f"{name} must be a Q4Matrix of shape {shape} with groups of "
+                                 f"{w1.group}, like w1")
+            matrices[name] = t
+        elif (isinstance(t, Q4Matrix) or t.dtype != dtype or tuple(t.shape) != shape or
+              not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {dtype} of shape {shape}, got "
+                             f"{getattr(t, 'dtype', 'a Q4Matrix')} {tuple(t.shape)}")
+        if t.device != w1.device:
+            raise ValueError(f"{name} is on {t.device}, w1 on {w1.device}")
+
+    def make(T):
+        return B.make_config(T, D, F, E, k, act=act, score=score, n_groups=n_groups,
+                             topk_groups=topk_groups, group_score=group_score, dtype=_DTYPE[dt],
+                             has_bias=b1 is not None, n_shared=n_shared,
+                             capacity_factor=capacity_factor)
+
+    hold = [t._held if isinstance(t, Q4Matrix) else t.detach() for t, _, _ in want.values()
+            if t is not None]
+    if q4:
+        entry = "moe_q4_decode"
+        struct = B.make_q4_weights(w_gate, w1.group, b1=b1, b2=b2, logit_bias=logit_bias,
+                                   corr_bias=corr_bias,
+                                   **{n: m.c_matrix() for n, m in matrices.items()})
+    else:
+        entry = "moe_decode"
+        struct = B.make_weights(w_gate, w1, w2, w3, b1, b2, logit_bias, corr_bias, ws1, ws3, ws2)
+    return Weights(w1.device, dt, D, make, hold, entry, struct)
 
 
 class MoEDecoder:
@@ -42,63 +114,17 @@ class MoEDecoder:
                  score="softmax", n_groups=1, topk_groups=1, group_score="top2_sum",
                  logit_bias=None, corr_bias=None, n_shared=0, ws1=None, ws3=None, ws2=None,
                  capacity_factor=0.0, max_tokens=B.MOE_DECODE_MAX_TOKENS):
-        q4 = isinstance(w1, Q4Matrix)
-        if not q4 and w1.dtype not in _DTYPE:
-            raise ValueError(f"w1 must be float32, bfloat16 or a Q4Matrix, got {w1.dtype}")
-        if len(w1.shape) != 3:
-            raise ValueError(f"w1 must be [E, F, D], got {tuple(w1.shape)}")
-        E, F, D = w1.shape
-        Fs = int(n_shared) * F
-        if (w3 is not None) != (act == "swiglu"):
-            raise ValueError("w3 goes with swiglu experts, and only with them")
-        if (b1 is None) != (b2 is None):
-            raise ValueError("b1 and b2 come together")
         if not 1 <= max_tokens <= B.MOE_DECODE_MAX_TOKENS:
             raise ValueError(f"max_tokens must be 1 to {B.MOE_DECODE_MAX_TOKENS}")
-        f32, dt = torch.float32, torch.bfloat16 if q4 else w1.dtype
-        one = (1,) if q4 else ()
-        want = dict(w_gate=(w_gate, f32, (E, D)), w1=(w1, dt, (E, F, D)), w2=(w2, dt, (E, D, F)),
-                    w3=(w3, dt, (E, F, D)), b1=(b1, f32, (E, F)), b2=(b2, f32, (E, D)),
-                    logit_bias=(logit_bias, f32, (E,)), corr_bias=(corr_bias, f32, (E,)),
-                    ws1=(ws1, dt, one + (Fs, D)), ws3=(ws3, dt, one + (Fs, D)),
-                    ws2=(ws2, dt, one + (D, Fs)))
-        matrices = {}
-        for name, (t, dtype, shape) in want.items():
-            if name.startswith("ws") and (t is not None) != (n_shared > 0):
-                raise ValueError("ws1, ws3 and ws2 go with n_shared > 0")
-            if t is None:
-                continue
-            if q4 and dtype is dt:
-                if not isinstance(t, Q4Matrix) or t.shape != shape or t.group != w1.group:
-                    raise ValueError(f"{name} must be a Q4Matrix of shape {shape} with groups of "
-                                     f"{w1.group}, like w1")
-                matrices[name] = t
-            elif (isinstance(t, Q4Matrix) or t.dtype != dtype or tuple(t.shape) != shape or
-                  not t.is_contiguous()):
-                raise ValueError(f"{name} must be contiguous {dtype} of shape {shape}, got "
-                                 f"{getattr(t, 'dtype', 'a Q4Matrix')} {tuple(t.shape)}")
-            if t.device != w1.device:
-                raise ValueError(f"{name} is on {t.device}, w1 on {w1.device}")
-        if w1.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        w = check_weights(w_gate, w1, w2, w3, b1, b2, k, act, score, n_groups, topk_groups,
+                          group_score, logit_bias, corr_bias, n_shared, ws1, ws3, ws2,
+                          capacity_factor)
+        if w.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
             raise ValueError("a decoder cannot be made while its stream is being captured")
-        self.device, self.dtype, self.D, self.k = w1.device, dt, D, int(k)
+        D, dt, f32 = w.D, w.dtype, torch.float32
+        self.device, self.dtype, self.D, self.k = w.device, dt, D, int(k)
         self.max_tokens = int(max_tokens)
-        self._make = lambda T: B.make_config(
-            T, D, F, E, k, act=act, score=score, n_groups=n_groups, topk_groups=topk_groups,
-            group_score=group_score, dtype=_DTYPE[dt], has_bias=b1 is not None,
-            n_shared=n_shared, capacity_factor=capacity_factor)
-        # that storage stays alive as long as the decoder does, even if a parameter's is replaced
-        self._hold = [t._held if isinstance(t, Q4Matrix) else t.detach()
-                      for t, _, _ in want.values() if t is not None]
-        if q4:
-            self._entry = "moe_q4_decode"
-            self._weights = B.make_q4_weights(w_gate, w1.group, b1=b1, b2=b2, logit_bias=logit_bias,
-                                              corr_bias=corr_bias,
-                                              **{n: m.c_matrix() for n, m in matrices.items()})
-        else:
-            self._entry = "moe_decode"
-            self._weights = B.make_weights(w_gate, w1, w2, w3, b1, b2, logit_bias, corr_bias, ws1,
-                                           ws3, ws2)
+        self._make, self._hold, self._entry, self._weights = w.make, w.hold, w.entry, w.struct
         self._weights_ref = ctypes.byref(self._weights)
         self._calls = {}
         self.cfg = self._make(self.max_tokens)

@@ -2,7 +2,7 @@
 
 ``Q4Layer`` holds references to the router's weights and the 4-bit expert matrices,
 owns the workspace and calls ``moe_q4_forward`` (``include/moe_q4.h``); ``decoder`` is
-its form for a few tokens.  It computes nothing itself.
+its form for a few tokens, where it has one.  It computes nothing itself.
 """
 
 from __future__ import annotations
@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .decode import MoEDecoder
+from .decode import MoEDecoder, check_weights
 from .layer import MoELayer
 from .q4 import quantize
 
@@ -24,9 +24,10 @@ class Q4Layer:
     """w_gate [E,D] fp32; w1, w3 [E,F,D] and w2 [E,D,F] Q4Matrix; the shared branch ws1,
     ws3 [1,n_shared F,D] and ws2 [1,D,n_shared F] Q4Matrix; b1 [E,F], b2 [E,D], logit_bias
     [E], corr_bias [E] fp32 or None: used in place, in the storage that they have when the
-    layer is made.  The limits are those of the few-token form (moe_decode's on D, F and
-    n_shared F).  Calls run on the current stream of their GPU, which has to be the
-    current one; those of one layer share its workspace and must not overlap on the GPU."""
+    layer is made.  ``decoder`` is None where D, F or n_shared F are past the few-token
+    form's limits (moe_decode's).  Calls run on the current stream of their GPU, which has
+    to be the current one; those of one layer share its workspace and must not overlap on
+    the GPU."""
 
     # calls pass addresses and configurations made from these once
     _FIXED = frozenset(("workspace", "cfg", "device", "D", "max_tokens", "matrices"))
@@ -42,25 +43,32 @@ class Q4Layer:
                  capacity_factor=0.0, max_tokens=4096):
         if max_tokens < 1:
             raise ValueError("max_tokens must be positive")
-        # the decoder's making checks every argument and keeps the weights' storage
-        self.decoder = MoEDecoder(
-            w_gate, w1, w2, w3=w3, b1=b1, b2=b2, k=k, act=act, score=score, n_groups=n_groups,
+        args = dict(
+            w3=w3, b1=b1, b2=b2, k=k, act=act, score=score, n_groups=n_groups,
             topk_groups=topk_groups, group_score=group_score, logit_bias=logit_bias,
             corr_bias=corr_bias, n_shared=n_shared, ws1=ws1, ws3=ws3, ws2=ws2,
-            capacity_factor=capacity_factor,
-            max_tokens=min(max_tokens, B.MOE_DECODE_MAX_TOKENS))
-        if self.decoder._entry != "moe_q4_decode":
+            capacity_factor=capacity_factor)
+        w = check_weights(w_gate, w1, w2, **args)
+        if w.entry != "moe_q4_decode":
             raise ValueError("the expert weights must be Q4Matrix objects")
-        self.device, self.D, self.max_tokens = w1.device, w1.K, int(max_tokens)
+        if w.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise ValueError("a layer cannot be made while its stream is being captured")
+        self.device, self.D, self.max_tokens = w.device, w.D, int(max_tokens)
         self.matrices = {n: m for n, m in zip(_MATRICES, (w1, w3, w2, ws1, ws3, ws2)) if m is not None}
+        self._make, self._hold, self._weights = w.make, w.hold, w.struct
+        self._weights_ref = ctypes.byref(self._weights)
         self._calls = {}
-        self.cfg = self.decoder._make(self.max_tokens)
+        self.cfg = w.make(self.max_tokens)
         nbytes = B.moe_q4_workspace_size(self.cfg)
         if nbytes == 0:
             raise B.MoEError("moe_q4_workspace_size", B.MOE_ERR_INVALID_ARG,
                              "invalid or unsupported configuration")
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.workspace[:16].zero_()      # the status word, for a look before the first call
+        few = min(self.max_tokens, B.MOE_DECODE_MAX_TOKENS)
+        self.decoder: Optional[MoEDecoder] = None
+        if B.moe_decode_workspace_size(w.make(few)) > 0:
+            self.decoder = MoEDecoder(w_gate, w1, w2, max_tokens=few, **args)
 
     @classmethod
     def from_layer(cls, layer: MoELayer, group=64, max_tokens=None) -> "Q4Layer":
@@ -104,10 +112,9 @@ class Q4Layer:
         if c is None:
             if len(self._calls) >= 64:
                 self._calls.clear()
-            cfg = self.decoder._make(T)
+            cfg = self._make(T)
             c = self._calls[T] = cfg, ctypes.byref(cfg)
-        d = self.decoder
-        status = B.lib().moe_q4_forward(c[1], d._weights_ref, x.data_ptr(), y.data_ptr(),
+        status = B.lib().moe_q4_forward(c[1], self._weights_ref, x.data_ptr(), y.data_ptr(),
                                         self.workspace.data_ptr(), self.workspace.numel(),
                                         B._stream_on(None, self.device))
         if status != B.MOE_OK:
@@ -116,6 +123,8 @@ class Q4Layer:
 
     def decode(self, x, y=None):
         """y [T, D] bf16 for a few tokens (``MoEDecoder.decode``)."""
+        if self.decoder is None:
+            raise ValueError("D, F or n_shared F are past the few-token form's limits: use forward")
         return self.decoder.decode(x, y)
 
     def status(self) -> int:

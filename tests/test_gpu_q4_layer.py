@@ -304,3 +304,28 @@ def test_decode_infinite_scale_of_a_short_group(T, group, F):
     rest = [i for i in range(96) if i != 5]
     assert torch.equal(got[:, rest], want[:, rest]) and bool(want.isfinite().all())
     assert bool((got[:, 5] == float("inf")).all())
+
+
+@pytest.mark.parametrize("T", [1, 70])
+@pytest.mark.parametrize("kw", [dict(D=64, F=8224), dict(D=16416, F=32), dict(D=32, F=4128, n_shared=2)])
+def test_forward_past_the_few_token_limits(kw, T):
+    wl = _wl(T=T, E=8, k=2, **kw)
+    inp, ms = _quantized(wl, 6, 128)
+    layer = Q4Layer(**_args(wl, inp, ms), max_tokens=T)
+    assert layer.decoder is None
+    x = device_x(wl, inp)
+    y = layer.forward(x)
+    assert layer.status() == 0
+    want = _forward_want(wl, inp, layer, x, _routing_of(layer, T, wl.k, wl.E))
+    assert_close("y", np64(y), want, TOL["bf16"])
+
+
+def test_from_a_layer_past_the_few_token_limits():
+    """A trained layer of wide experts has a 4-bit form as well."""
+    wl = _wl(T=40, D=64, F=8224)
+    inp = _inputs(wl, 2)
+    inp["target"] = torch.zeros(40, 64)
+    q = Q4Layer.from_layer(make_layer(wl, inp), group=32)
+    x = device_x(wl, inp)
+    assert q.decoder is None and q.matrices["w1"].shape == (8, 8224, 64)
+    assert bool(q.forward(x).isfinite().all()) and q.status() == 0

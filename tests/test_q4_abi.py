@@ -329,3 +329,26 @@ def test_product_class_refusals():
         p.forward(x, off)
     with pytest.raises(AttributeError):
         p.shape = (1, 2, 3)
+
+
+@pytest.mark.parametrize("D,F,n_shared", [(32, 8224, 0), (16416, 32, 0), (32, 4128, 2)])
+def test_layer_past_the_few_token_limits(D, F, n_shared):
+    """The layer for prompts takes what moe_q4_forward takes; its form for a few tokens is
+    absent there, and says so."""
+    from sparse_mixture_experts_softmax_gb300.decode import MoEDecoder
+    from sparse_mixture_experts_softmax_gb300.q4_layer import Q4Layer
+    g, up, down = torch.zeros(8, D), _matrix(8, F, D), _matrix(8, D, F)
+    args = dict(w3=up, act="swiglu", k=2, n_shared=n_shared)
+    if n_shared:
+        args.update(ws1=_matrix(1, n_shared * F, D), ws3=_matrix(1, n_shared * F, D),
+                    ws2=_matrix(1, D, n_shared * F))
+    with pytest.raises(B.MoEError):
+        MoEDecoder(g, up, down, **args)
+    layer = Q4Layer(g, up, down, max_tokens=3, **args)
+    assert layer.decoder is None
+    with pytest.raises(ValueError, match="use forward"):
+        layer.decode(torch.zeros(3, D).bfloat16())
+    with pytest.raises(ValueError, match="GPU"):
+        layer.forward(torch.zeros(3, D).bfloat16())
+    with pytest.raises(B.MoEError):                          # past moe_q4_forward's own
+        Q4Layer(g, up, down, max_tokens=1 << 30, **args)
