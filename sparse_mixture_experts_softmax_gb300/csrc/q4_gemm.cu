@@ -161,6 +161,18 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile i
     }
   }
 }
+// A look at a barrier that returns at once (a try may take its time).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // The one lane of a warp that issues.
 __device__ __forceinline__ bool elect() {
   uint32_t v;
@@ -328,7 +340,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
     uint32_t pa = 0, px = 0, aph = 0;
     bool ok = true, any = false;
     // (the next stage's barriers are looked at while this one's products are on their way)
-    bool x_in = mbar_try_wait(smem_u32(&x_full[0]), 0), a_in = mbar_try_wait(smem_u32(&a_full[0]), 0);
+    bool x_in = false, a_in = false;
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile T = tile_at(t, p, tb);
       if (!all_wait(smem_u32(&acc_empty[buf]), aph ^ 1u)) break;
@@ -357,8 +369,8 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
         any = true;
         if (++sa == SA) { sa = 0; pa ^= 1u; }
         if (++sx == SX) { sx = 0; px ^= 1u; }
-        x_in = mbar_try_wait(smem_u32(&x_full[sx]), px);
-        a_in = mbar_try_wait(smem_u32(&a_full[sa]), pa);
+        x_in = mbar_test(smem_u32(&x_full[sx]), px);
+        a_in = mbar_test(smem_u32(&a_full[sa]), pa);
       }
       if (!ok) break;
       if (issuer) mma_commit(smem_u32(&acc_full[buf]));
