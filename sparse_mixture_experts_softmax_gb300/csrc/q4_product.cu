@@ -149,17 +149,25 @@ cudaError_t launch_q4_product(const Q4Product& p, cudaStream_t st) {
   if (tt == 0) return launch_q4_gemm(p, st);
   // Every row tile reads its expert's matrix again, most of it from L2, and widens it
   // again; the other kernel does so once for up to 160 rows, but its tiles of 128 outputs
-  // leave SMs without work where there are few.  So the few-row kernel is taken where
-  // experts have three quarters of a tile's rows or less in the mean, or where all its
-  // tiles' weights are 24 MB or less.  Measured, few and many (us, with 8 for the events
-  // around a call): 128 experts of 4096 inputs and 2 x 2048 outputs, 1, 4, 8 and 16 rows an
-  // expert 203, 214, 399, 590 and 267, 270, 271, 274; 16 of 2048 inputs and 2 x 2048 outputs, 8
-  // and 16 rows 29, 50 and 36, 36; one matrix of 4096 x 4096, 16, 64 and 128 rows 15, 25, 42 and
-  // 22, 23, 25; 2048 x 2048, 128 and 192 rows 19, 22 and 19, 19; 1024 x 1024, 256 and 512 rows
-  // 15, 17 and 17, 17; 1000 x 480, 333 and 1000 rows 13, 17 and 17, 17.
+  // leave SMs without work where there are few, and a tile's chain along K then takes 2 us for
+  // 1024 inputs.  Its tensor maps cost the host 1.3 us more.  So the few-row kernel is taken where
+  // experts have three quarters of a tile's rows or less in the mean, or where all its tiles'
+  // weights are no more than 8 MB (either way below the host's time for a call, 8 and 9.4 us) or
+  // 1.5 K^2 bytes.  Measured, few and many (us, from a graph, rows dealt evenly): 128 experts of
+  // 4096 inputs and 2 x 2048 outputs, 1, 4, 5, 8 and 16 rows an expert 190, 200, 201, 381, 569 and
+  // 250, 252, 252, 254, 258; 16 of 2048 inputs and 2 x 2048 outputs, 8, 12 and 16 rows 20, 25, 41 and
+  // 23, 23, 23; one matrix of 2048 x 8192 (outputs, inputs), 16, 32 and 48 rows 12.5, 18.9, 27.5 and
+  // 20.9, 21.1, 21.5; of 4096 x 4096, 16, 32 and 64 rows 9.1, 12.4, 18.8 and 12.5, 12.8, 13.5; of
+  // 2048 x 2048, 16, 32, 48 and 64 rows 6.6, 8.2, 7.7, 11.7 and 8.3, 8.4, 8.7, 9.0; of 1024 x 1024, 32,
+  // 128, 256 and 512 rows 6.0, 7.6, 9.5, 11.9 and 6.3, 7.6, 7.6, 7.7.  Call after call through Python:
+  // 8 experts of 480 inputs and 1000 outputs, 42 and 80 rows an expert 8.3, 11.0 and 9.5, 9.4; one
+  // matrix of 1024 x 1024, 64 and 256 rows 7.8, 10.3 and 9.0, 9.4.  Left behind: weights of 24 MB in
+  // place of 8 (1000 rows of 1000 x 480 11.3 and 7.1).
+  // The host does not see where the rows are: 128, 256 and 640 rows of the 128 experts, all of
+  // them on four, take the few-row kernel's 42, 71 and 146 us, where the other's are 13, 14 and 18.
   const long long tiles = (p.E < p.R ? p.E : p.R) + p.R / tt;
   const long long bytes = tiles * p.N * (p.K / 2) * (p.act == 2 ? 2 : 1);
-  const bool few = 4ll * p.R <= 3ll * tt * p.E || bytes <= (24ll << 20);
+  const bool few = 4ll * p.R <= 3ll * tt * p.E || bytes <= (8ll << 20) || 2 * bytes <= 3ll * p.K * p.K;
   if (!few || tiles * ((p.N + 7) / 8) > INT_MAX) return launch_q4_gemm(p, st);
   return launch_q4_rows(p, tt, st);
 }

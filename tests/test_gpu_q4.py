@@ -401,3 +401,50 @@ def test_product_gelu_of_negative_inputs(rows):
     want = (h / (1 + np.exp(-u2)))[:, None]
     assert (np.abs(got - want) <= (C.BF16_HALF + 2.0 ** -14) * np.abs(want)).all(), \
         float((np.abs(got - want) / np.maximum(np.abs(want), 1e-30)).max())
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("act,bias", [("none", False), ("gelu_tanh", True), ("relu", True), ("swiglu", False)])
+def test_product_few_rows_crowded(act, bias, shape):
+    """Few rows of many experts, most of them on two: several row tiles of an expert in the
+    few-row kernel."""
+    N, K, group = shape
+    c = _product_case(N + 3 * K, [0, 33, 0, 0, 1, 0, 0, 0, 17, 0], N, K, group, act, bias, before=2, behind=3)
+    p, x, off = _device(c)
+    out = torch.full((c["R"], N), 7.0, dtype=torch.bfloat16, device="cuda")
+    p.forward(x, off, out)
+    _check(c, out, fill=7.0)
+    assert p.status() == 0
+
+
+def test_infinite_scale_of_a_short_group_crowded():
+    """As test_infinite_scale_of_a_short_group, several row tiles of an expert in the few-row
+    kernel."""
+    c = _product_case(20, [40, 0, 0, 0, 9, 0, 0, 0], 72, 160, 64, "none", False)
+    codes, scales = c["m"][0].copy(), c["m"][1].copy()
+    codes[:, 5, 128:] = np.maximum(codes[:, 5, 128:], 9)
+    c["x"], c["m"] = C.bf16(np.abs(c["x"]) + 2.0 ** -8), (codes, scales)
+    p, x, off = _device(c)
+    want = p.forward(x, off)
+    _check(c, want)
+    scales = scales.copy()
+    scales[:, 2, 5] = np.inf
+    got = Q4Product(C.device_matrix(codes, scales, 64)).forward(x, off)
+    rest = [i for i in range(72) if i != 5]
+    assert torch.equal(got[:, rest], want[:, rest]) and bool((got[:, 5] == float("inf")).all())
+
+
+def test_product_gelu_of_negative_inputs_few_rows():
+    """As test_product_gelu_of_negative_inputs, with its bound, in the few-row kernel: the rows
+    of one of eight experts."""
+    h = C.bf16(np.linspace(-6.0, -2.0, 90))
+    codes, scales = np.full((8, 8, 32), 8), np.ones((8, 1, 8))
+    codes[:, :, 0] = 9
+    x = np.zeros((90, 32))
+    x[:, 0] = h
+    p = Q4Product(C.device_matrix(codes, scales, 32), act="gelu_tanh")
+    off = torch.tensor([0, 0, 0] + [90] * 6, dtype=torch.int32, device="cuda")
+    got = p.forward(torch.from_numpy(x).bfloat16().cuda(), off).double().cpu().numpy()
+    u2 = 2 * np.sqrt(2 / np.pi) * (h + 0.044715 * h ** 3)
+    want = (h / (1 + np.exp(-u2)))[:, None]
+    assert (np.abs(got - want) <= (C.BF16_HALF + 2.0 ** -14) * np.abs(want)).all()
