@@ -184,8 +184,10 @@ class Q4Product:
             if len(self._calls) >= 64:
                 self._calls.clear()
             cfg = self._make(R)
-            # (a new tensor like another takes half the time of one from its shape)
-            like = torch.empty((R, N), dtype=torch.bfloat16, device=device) if R <= 64 else None
+            # (a new tensor like another takes half the time of one from its shape; those kept
+            # for it are of 512 KB at most)
+            small = R <= 64 and R * N <= 1 << 18
+            like = torch.empty((R, N), dtype=torch.bfloat16, device=device) if small else None
             c = self._calls[R] = cfg, ctypes.byref(cfg), like
         if out is not None:
             _want("out", out, torch.bfloat16, (R, N), device)

@@ -448,3 +448,17 @@ def test_product_gelu_of_negative_inputs_few_rows():
     u2 = 2 * np.sqrt(2 / np.pi) * (h + 0.044715 * h ** 3)
     want = (h / (1 + np.exp(-u2)))[:, None]
     assert (np.abs(got - want) <= (C.BF16_HALF + 2.0 ** -14) * np.abs(want)).all()
+
+
+def test_product_keeps_little_memory():
+    """Calls of many numbers of rows leave no more than 32 MB behind, whatever the outputs."""
+    p = Q4Product(quantize(torch.randn(1, 1 << 17, 32, device="cuda"), 32))
+    x = torch.randn(64, 32, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for R in range(1, 41):
+        out = p.forward(x[:R], torch.tensor([0, R], dtype=torch.int32, device="cuda"))
+        assert out.shape == (R, 1 << 17)
+    del out
+    assert torch.cuda.memory_allocated() - before <= 32 << 20
+    assert p.status() == 0
