@@ -57,6 +57,7 @@
 // then; a stage's loop unrolled four times the same times and 30 KB more code.
 #include "../../include/moe_block.h"
 #include "decode_experts.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -161,19 +162,6 @@ __global__ void decode_init_kernel(int* ctl) {
   if (threadIdx.x < DC_WORDS) ctl[threadIdx.x] = threadIdx.x == DC_MAGIC ? DECODE_MAGIC : 0;
 }
 
-int sm_count() {
-  static std::atomic<int> n{0};
-  int v = n.load(std::memory_order_relaxed);
-  if (v == 0) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return 0;
-    n.store(v, std::memory_order_relaxed);
-  }
-  return v;
-}
-
 // A tile of one token has room whatever the entry points let through: the lists of the
 // most tokens, of 32 choices among 256 experts, beside the widest rows.
 template <typename WT>
@@ -187,8 +175,7 @@ static_assert(always_fits<float>(MOE_DECODE_MAX_TOKENS) && always_fits<bf16>(MOE
 template <typename WT>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  const int sms = sm_count(), tt = tile_tokens<WT>(a);
-  if (sms <= 0) return cudaErrorUnknown;
+  const int sms = tc::sm_count(), tt = tile_tokens<WT>(a);
   if (tt <= 0) return cudaErrorInvalidValue;    // (past the entry points' limits)
   // a block per SM, or fewer where each would have less than 8 KB of weights (the
   // kernel's time hardly goes with it: 4 KB, 16 KB and a block on every SM are

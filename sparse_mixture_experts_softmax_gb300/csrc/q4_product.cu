@@ -9,6 +9,7 @@
 
 #include "decode_experts.cuh"
 #include "q4.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -122,15 +123,7 @@ cudaError_t launch_q4_rows(const Q4Product& p, int tt, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t err = ensure_dynamic_smem(q4_rows_kernel, SMEM_MAX, attr_done);
   if (err != cudaSuccess) return err;
-  static std::atomic<int> sms{0};
-  int n = sms.load(std::memory_order_relaxed);
-  if (n == 0) {
-    int dev = 0;
-    if ((err = cudaGetDevice(&dev)) != cudaSuccess ||
-        (err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-      return err;
-    sms.store(n, std::memory_order_relaxed);
-  }
+  const int n = tc::sm_count();
   // a block an SM, or fewer where each would have less than 8 KB of weights and less than
   // eight items (1000 rows of 64 x 32, 1 KB of weights: 83 us on one block, 12 on the 32
   // that the items ask for; 333 rows of 1000 x 480 21 on 30 blocks, 13 on all)
