@@ -602,10 +602,6 @@ Q4_ACT = dict(ACT, none=MOE_Q4_ACT_NONE)
 Q4_GROUPS = (32, 64, 128)
 
 
-def make_q4_matrix(codes, scales) -> moe_q4_matrix:
-    return moe_q4_matrix(_ptr(codes), _ptr(scales))
-
-
 def moe_q4_quantize(E, N, K, group, w_type, w, codes, scales, stream=None):
     _check("moe_q4_quantize",
            lib().moe_q4_quantize(int(E), int(N), int(K), int(group), DTYPE[w_type], _ptr(w),

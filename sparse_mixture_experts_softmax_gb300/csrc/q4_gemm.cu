@@ -261,11 +261,7 @@ q4_gemm_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUten
   const uint32_t tmem = tmem_slot;
   const int total = tb.first[p.E] * p.nF;
   const int nraw = (p.K + RAW_K - 1) / RAW_K, nkb = (p.K + BK - 1) / BK;   // 2 nraw or one less
-  // (bar: a barrier's address in shared memory)
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, p.status, p.limit_ns);
-  };
-  auto all_wait = [&](uint32_t bar, uint32_t parity) {     // by a whole warp
+  auto all_wait = [&](uint32_t bar, uint32_t parity) {     // by a whole warp; bar: its shared address
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
            __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag, p.status, p.limit_ns));
   };
