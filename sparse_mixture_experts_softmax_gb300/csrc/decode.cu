@@ -188,6 +188,27 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
                             attr_done, st, a, tt);
 }
 
+// Whether a call of 4-bit weights goes by half the warps.  Their tiles have more tokens where
+// rows are wide, so that an expert's weights are read and widened fewer times, but a reading
+// takes up to 1.2 times as long: they are chosen where the readings, tokens dealt evenly, are
+// less than 1 / 1.2, or where the others have no room for a row at all (64 tokens' 32 choices
+// among 256 experts beside rows of more than 18 KB).  Measured, 16 and 8 warps (us, from a
+// graph; D = 4096 where not stated): 8 experts, k = 2, F = 8192, T = 5, 8, 16, 32, 64: 92, 130, 212,
+// 364, 1211 and 106, 128, 172, 278, 460; F = 4096: 55, 72, 86, 123, 249 and 61, 80, 88, 105, 161; F =
+// 2816: 40, 54, 68, 95, 147 and 44, 60, 67, 91, 125; D = 16384, F = 512, T = 5, 16, 64: 43, 80, 366 and
+// 46, 72, 167; 64 experts, k = 8, F = 4096, T = 16, 64: 334, 947 and 358, 565; F = 1408 and four shared
+// experts: 224, 702 and 197, 397; 16 experts, k = 4, D = F = 2048, T = 64: 87 and 95; the large layer,
+// T = 16, 64: 215, 359 and 258, 420.
+bool wide_rows(const DecodeArgs& a) {
+  const long long R = (long long)a.T * a.k, experts = R < a.E ? R : a.E;
+  const long long eight = tile_tokens<Q4Eight>(a), wide = tile_tokens<Q4Wide>(a);
+  auto readings = [&](long long tt) {          // times tt
+    const long long routed = experts * tt > R ? experts * tt : R, shared = a.T > tt ? a.T : tt;
+    return routed + (a.Fs > 0 ? a.n_shared * shared : 0);
+  };
+  return 5 * wide * readings(eight) > 6 * eight * readings(wide);
+}
+
 }  // namespace
 
 cudaError_t launch_decode_init(int* ctl, cudaStream_t st) {
@@ -200,10 +221,8 @@ cudaError_t launch_decode(int kind, const DecodeArgs& a, cudaStream_t st) {
   // a second tile's weights come from L2): the large layer, 64 tokens 389 and 374; 64 experts of
   // 1024 and 704, k = 6, 16 and 64 tokens 38.5, 55.1 and 36.1, 45.0; 16 of 1024 and 1024, k = 4, 48
   // tokens 42.1 and 35.1; 8 of 512 and 1024, k = 2, 5 and 64 tokens 18.5, 30.4 and 17.6, 26.6.
-  // Their buffers and the longest lists leave no room for the widest rows (of 64 tokens' 32
-  // choices among 256 experts, for rows of more than 18 KB): those calls go by half the warps.
   if (kind == DECODE_Q4 && a.T <= most_tokens<Q4Few>()) return launch_t<Q4Few>(a, st);
-  if (kind == DECODE_Q4) return tile_tokens<Q4Eight>(a) > 0 ? launch_t<Q4Eight>(a, st) : launch_t<Q4Wide>(a, st);
+  if (kind == DECODE_Q4) return wide_rows(a) ? launch_t<Q4Wide>(a, st) : launch_t<Q4Eight>(a, st);
   return kind == DECODE_BF16 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
 }
 

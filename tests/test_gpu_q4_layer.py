@@ -329,3 +329,22 @@ def test_from_a_layer_past_the_few_token_limits():
     x = device_x(wl, inp)
     assert q.decoder is None and q.matrices["w1"].shape == (8, 8224, 64)
     assert bool(q.forward(x).isfinite().all()) and q.status() == 0
+
+
+@pytest.mark.parametrize("T", [9, 33, 64])
+@pytest.mark.parametrize("group,kw", [
+    (32, dict(D=64, F=4096, E=8, k=4)), (64, dict(D=96, F=8192, E=8, k=2, act="relu", has_bias=True)),
+    (128, dict(D=160, F=4128, E=8, k=4, act="gelu_tanh", has_bias=True)), (64, dict(D=16384, F=64, E=8, k=3)),
+    (128, dict(D=64, F=2080, E=16, k=4, n_shared=2)), (32, dict(D=8224, F=96, E=8, k=8, capacity_factor=0.5)),
+    (64, dict(D=32, F=5632, E=16, k=4, zipf_skew=1.2, zipf_empty=4)),
+    (32, dict(D=64, F=4096, E=32, k=8, score="sigmoid", n_groups=4, topk_groups=2, corr_bias_scale=0.1)),
+])
+def test_decode_wide_rows(group, kw, T):
+    """The form of eight warps: every kind of layer whose rows are wide."""
+    wl = _wl(T=T, **kw)
+    inp, ms = _quantized(wl, T, group)
+    d = MoEDecoder(**_args(wl, inp, ms), max_tokens=T)
+    x = device_x(wl, inp)
+    y = d.decode(x).clone()
+    _check(wl, inp, d, y)
+    assert torch.equal(d.decode(x), y)
