@@ -41,9 +41,10 @@ typedef struct {
 
 /* codes and scales of w [E, N, K] (w_type: MOE_F32 or MOE_BF16).  Per group of an
  * output, with a = max |w|:  scale is the smallest bf16 value of five significant
- * bits that is not below a / 7, and  code = 8 + the whole number nearest to
- * w / scale, ties to even (8 where a is 0).  Codes are 1 to 15.  A group with an
- * infinity or a NaN gets a NaN scale, so that all of it reads as NaN. */
+ * bits that is not below a / 7 (the smallest multiple of 2^-130 where a / 7 is
+ * below 2^-126), and  code = 8 + the whole number nearest to w / scale, ties to
+ * even (8 where a is 0).  Codes are 1 to 15.  A group with an infinity or a NaN
+ * gets a NaN scale, so that all of it reads as NaN. */
 MOE_API moe_status moe_q4_quantize(int32_t E, int32_t N, int32_t K, int32_t group, int32_t w_type,
                                    const void* w, void* codes, void* scales, void* stream);
 
@@ -68,7 +69,8 @@ typedef struct {
  * and c is rounded once.  w and w3 (NULL unless act is MOE_ACT_SWIGLU) are 4-bit
  * matrices; bias [E, N] fp32 or NULL (NULL with MOE_ACT_SWIGLU).  offsets [E+1]
  * (int32) lie on the device; values that decrease or leave [0, R] are clamped.
- * Rows outside of every segment are not read and left as they are in c.  c must
+ * Rows outside of every segment are left as they are in c, and those of x reach no
+ * result (all R of them have to be readable: tiles of rows are read whole).  c must
  * not overlap an input.  E <= MOE_Q4_MAX_EXPERTS, R <= MOE_Q4_MAX_ROWS, R K and
  * R N < 2^40.  Here, in moe_q4_decode and in moe_q4_forward, weights below 2^-118 in
  * magnitude are rounded to multiples of 2^-125, and sums below it may lose bits.
@@ -102,7 +104,9 @@ typedef struct {
 
 /* moe_decode with those weights: the same arguments, limits, workspace
  * (moe_decode_workspace_size, moe_decode_init, moe_decode_status) and precision.  An
- * expert's weights are read once for each tile of up to 8 of its tokens. */
+ * expert's weights are read once for each tile of up to 8 of its tokens, fewer where
+ * rows are wide (4 at F = 8192 or D = 16384): on experts of F = 4096 or more
+ * moe_q4_forward is faster from 16 to 64 tokens on. */
 MOE_API moe_status moe_q4_decode(const moe_config* cfg, const moe_q4_weights* w, const void* x,
                                  void* y, int32_t* idx, float* gate, void* workspace,
                                  size_t workspace_bytes, void* stream);
@@ -111,8 +115,9 @@ MOE_API moe_status moe_q4_decode(const moe_config* cfg, const moe_q4_weights* w,
  * grows with T: one made for the most tokens serves every call): x [T, D] bf16,
  * y [T, D] fp32, which must not overlap x or a weight.  Hidden activations and the
  * experts' outputs are rounded to bf16, as in moe_forward.  T k <= MOE_Q4_MAX_ROWS.
- * moe_q4_status reads the last call's device status: 0, or MOE_ERR_TIMEOUT when a
- * bounded device-side wait expired (y is then invalid).  It synchronises `stream`. */
+ * moe_q4_status reads the device status of the last call of a token or more: 0, or
+ * MOE_ERR_TIMEOUT when a bounded device-side wait expired (y is then invalid).  It
+ * synchronises `stream`. */
 MOE_API size_t moe_q4_workspace_size(const moe_config* cfg);
 MOE_API moe_status moe_q4_forward(const moe_config* cfg, const moe_q4_weights* w, const void* x,
                                   float* y, void* workspace, size_t workspace_bytes, void* stream);

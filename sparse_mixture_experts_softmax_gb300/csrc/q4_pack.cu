@@ -87,7 +87,8 @@ __device__ __forceinline__ long long scales_at(const Q4Shape& s, const Part& p) 
 }
 
 // The scale of a group whose largest magnitude is a (finite, >= 0): the smallest value
-// of five significant bits that is not below a / 7.  The four bits behind the first stay
+// of five significant bits that is not below a / 7 (below 2^-126, where an fp32 number has
+// no leading bit of its own, the smallest multiple of 2^-130).  The four bits behind the first stay
 // and what follows rounds up.  The factor is the largest fp32 value below 1 / 7, so the
 // quotient is at most a last place too small, and 7 s, which is exact (3 bits by 5), tells
 // where that has left s one step too small.

@@ -93,8 +93,9 @@ class Q4Matrix:
 def quantize(w, group=64, out=None) -> Q4Matrix:
     """The 4-bit matrix of w [E, N, K] or [N, K] (then E is 1), float32 or bfloat16.  A
     group's scale is the smallest value of five significant bits that is not below
-    max |w| / 7, its codes 8 + the nearest whole numbers to w / scale.  ``out``: a
-    matrix of that shape and group that is rewritten (what was made with it follows)."""
+    max |w| / 7 (the smallest multiple of 2^-130 where that is below 2^-126), its codes
+    8 + the nearest whole numbers to w / scale.  ``out``: a matrix of that shape and group
+    that is rewritten (what was made with it follows)."""
     kind, device = _CODE.get(w.dtype), w.device
     if kind is None:
         raise ValueError(f"w must be float32 or bfloat16, got {w.dtype}")
@@ -166,8 +167,8 @@ class Q4Product:
     def forward(self, x, offsets, out=None):
         """c [R, N] bfloat16 of the rows x [R, K] bfloat16.  The rows of expert e are
         offsets[e] to offsets[e + 1] - 1 (int32 [E + 1], on the GPU); values that decrease
-        or leave 0 .. R are clamped.  Rows outside of every expert's are not read and are
-        left as they are in ``out`` (undefined without one)."""
+        or leave 0 .. R are clamped.  Rows outside of every expert's reach no result and are
+        left as they are in ``out`` (undefined without one), which must not overlap x."""
         E, N, K = self.shape
         device, shape = self.device, x.shape
         if (len(shape) != 2 or shape[1] != K or x.dtype is not torch.bfloat16 or

@@ -128,6 +128,6 @@ class Q4Layer:
         return self.decoder.decode(x, y)
 
     def status(self) -> int:
-        """Device status of the last ``forward`` (0, or a MOE_ERR_* code).  Waits for the
-        current stream."""
+        """Device status of the last ``forward`` of a token or more (0, or a MOE_ERR_* code).
+        Waits for the current stream."""
         return B.moe_q4_status(self.cfg, self.workspace, B._stream_on(None, self.device))
