@@ -48,9 +48,10 @@
 // 4-bit layers widen each weight to bf16 in front of the same products, which then counts
 // more than HBM: all sixteen warps multiply, each with stages of 256 bytes (512 inputs) of
 // 16 rows, tiles are of up to 8 tokens, and calls of up to four tokens have a kernel of
-// their own (Q4Few).  Measured, the large layer: 64 tokens (1.6 GB of weights) 368 to 374
-// us, 4.8 TB/s; one token (105 MB) 41 us, of which 7 go to the logits and the selection and
-// 4 to barriers and the last pass.  Left behind: eight warps 61 and 599 us (one and 64
+// their own (Q4Few); where rows are wide, eight warps with larger tiles (wide_rows).  Measured,
+// the large layer: 64 tokens (1.78 GB of codes and scales, groups of 32) 361 to 377 us, 4.7 to
+// 4.9 TB/s; one token (106 MB with the router's weights, groups of 128) 41 us, of which 7 go to
+// the logits and the selection and 4 to barriers and the last pass.  Left behind: eight warps 61 and 599 us (one and 64
 // tokens); stages of 128 bytes 64 tokens 519 (the instructions to copy a stage are the same
 // as for 256); the four-token form chosen for every tile within one kernel 43 and 400
 // (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45 and 392

@@ -24,11 +24,12 @@
 // What bounds it: the matrix instructions (their pipe is 74 to 77 % busy at 160-row tiles,
 // the rest being a tile's beginning and end and waits for the widening warps), and with few
 // rows an expert the chain of a stage: widening, the issue of its products (some 27 clocks
-// each) and the wait for their end.  Measured, 128 experts, 4096 inputs, 2 x 2048 outputs
-// with SwiGLU: 256 rows an expert 0.69 ms, 1.60 PFLOP/s; 32768 rows dealt unevenly, as a
-// router does, 0.79 ms; 16 rows an expert 271 us, 4.2 TB/s of codes, scales and rows.
-// Without SwiGLU, 2048 inputs and 4096 outputs: 0.39 ms, 1.42 PFLOP/s.  One matrix of
-// 4096 x 4096 and 65536 rows: 1.15 ms, 1.91 PFLOP/s.
+// each) and the wait for their end.  Measured in bursts of a few calls, 128 experts, 4096
+// inputs, 2 x 2048 outputs with SwiGLU: 160 rows an expert 0.39 ms, 1.75 PFLOP/s; 256 rows 0.67
+// ms, 1.65; 32768 rows dealt as a router does 0.68 ms (0.77 to 0.82 call after call, under the
+// power limit); 16 rows an expert 258 us, 4.4 TB/s of codes, scales and rows.  Without SwiGLU,
+// 2048 inputs and 4096 outputs, 256 rows an expert: 0.36 ms, 1.54 PFLOP/s.  One matrix of 4096 x
+// 4096 and 65536 rows: 1.12 ms, 1.97 PFLOP/s.
 //
 // Left behind (the 32768 rows dealt unevenly): widened weights in shared memory as the A
 // operand, which take its rate from the rows, 1.19 ms; then 64 inputs a stage and one store
@@ -36,7 +37,8 @@
 // an expert 0.79 ms, whatever the stages of codes.  Prefetches of the rows into L2 by the
 // warp that copies them 0.73 (its own instructions count).  Tiles of 192 rows leave tensor
 // memory for two stages of widened weights only; without them 161 to 192 rows of an expert are
-// two tiles of 96 (192 rows an expert: 0.63 ms where 160 rows take 0.42).
+// two tiles of 96 (192 rows an expert: 0.60 ms where 160 rows take 0.39).  A look ahead at the
+// next stage's barriers that may suspend the warp: 4 us more for a small call.
 #include "q4.cuh"
 #include "q4.h"
 #include "tc_ptx.cuh"
