@@ -51,10 +51,10 @@
 // their own (Q4Few); where rows are wide, eight warps with larger tiles (wide_rows).  Measured,
 // the large layer: 64 tokens (1.78 GB of codes and scales, groups of 32) 361 to 377 us, 4.7 to
 // 4.9 TB/s; one token (106 MB with the router's weights, groups of 128) 41 us, of which 7 go to
-// the logits and the selection and 4 to barriers and the last pass.  Left behind: eight warps 61 and 599 us (one and 64
-// tokens); stages of 128 bytes 64 tokens 519 (the instructions to copy a stage are the same
-// as for 256); the four-token form chosen for every tile within one kernel 43 and 400
-// (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45 and 392
+// the logits and the selection and 4 to barriers and the last pass.  Left behind: eight warps 61
+// and 599 us (one and 64 tokens); stages of 128 bytes 64 tokens 519 (the instructions to copy a
+// stage are the same as for 256); the four-token form chosen for every tile within one kernel 43
+// and 400 (its registers spill); W2's first rows copied to L2 ahead 47 and 394, against 45 and 392
 // then; a stage's loop unrolled four times the same times and 30 KB more code.
 #include "../../include/moe_block.h"
 #include "decode_experts.cuh"

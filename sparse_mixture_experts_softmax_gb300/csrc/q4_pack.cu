@@ -88,9 +88,9 @@ __device__ __forceinline__ long long scales_at(const Q4Shape& s, const Part& p) 
 
 // The scale of a group whose largest magnitude is a (finite, >= 0): the smallest value
 // of five significant bits that is not below a / 7 (below 2^-126, where an fp32 number has
-// no leading bit of its own, the smallest multiple of 2^-130).  The four bits behind the first stay
-// and what follows rounds up.  The factor is the largest fp32 value below 1 / 7, so the
-// quotient is at most a last place too small, and 7 s, which is exact (3 bits by 5), tells
+// no leading bit of its own, the smallest multiple of 2^-130).  The four bits behind the
+// first stay and what follows rounds up.  The factor is the largest fp32 value below 1 / 7, so
+// the quotient is at most a last place too small, and 7 s, which is exact (3 bits by 5), tells
 // where that has left s one step too small.
 __device__ __forceinline__ float scale_of(float a) {
   const uint32_t b = (__float_as_uint(__fmul_rd(a, 0x1.249248p-3f)) + 0x7ffffu) & ~0x7ffffu;
